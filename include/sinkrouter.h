@@ -66,7 +66,11 @@ typedef enum sr_status {
                                    expected); outputs of that launch are invalid and the
                                    workspace must be re-initialised with sr_workspace_init */
 #define SR_DEVERR_APPEND_SLOT 8 /* sr_rope_append_route: a sequence's slot seq_lens[b] was
-                                   outside [0, min(Lmax, max_pos)); nothing was appended for it */
+                                   outside [0, min(Lmax, max_pos)); nothing was appended for it.
+                                   sr_kv_append_quant, sr_kv_dequant: a row's position was outside
+                                   [0, Lmax); the row was skipped */
+#define SR_DEVERR_ROW_COUNT 16  /* sr_kv_append_quant, sr_kv_dequant: a sequence's row count was
+                                   outside [0, n_tokens] ([0, n_rows]); it was clamped */
 
 /*
  * sr_route -- cosine routing of every unit (README decode list: compare the RoPE
@@ -345,6 +349,186 @@ int32_t sr_decode_grid_size(void);
 
 /* Message of the last CUDA error seen by this library on this thread ("" if none). */
 const char *sr_last_cuda_error(void);
+
+/* What a KV cache holds. */
+typedef enum sr_kv_type {
+    SR_KV_BF16 = 0,
+    SR_KV_E4M3 = 1, /* 8-bit floating point codes (OCP e4m3) with a scale per row */
+    SR_KV_INT8 = 2  /* 8-bit integer codes, two's complement, with a scale per row */
+} sr_kv_type;
+
+/*
+ * The 8-bit KV cache
+ * ------------------
+ * The caches hold one byte a value, k_cache and v_cache [B, Hkv, Lmax, d], and
+ *   kv_scales   fp32 [B, Hkv, Lmax, 2]: the scale of the key row, then of the
+ *               value row, of every position
+ * and a row stands for code * scale. A bf16 row x is written, with
+ * top = max(max_i |x_i|, 2^-100), as
+ *   e4m3: scale = the power of two with 224 < top / scale <= 448,
+ *         code_i = x_i / scale rounded to e4m3 (nearest, ties to even)
+ *   int8: scale = top / 127 rounded to fp32,
+ *         code_i = 127 x_i / top rounded to an integer (nearest, ties to even)
+ * A row with an infinity or a NaN gets codes 0 and scale NaN, so that it reads
+ * back as NaN. Readers take any finite scale, not only the writer's. The
+ * position-0 key and value k0 / v0 stay bf16: routing and the sink bypass work
+ * on the unquantised rows.
+ */
+
+/* Strides, in elements, of a bf16 tensor [B, T, Hkv, d] whose last dimension is
+   contiguous; each a multiple of 8, so that every row is 16-byte aligned. */
+typedef struct sr_row_strides {
+    int64_t batch, token, head;
+} sr_row_strides;
+
+/*
+ * sr_kv_append_quant -- quantise a chunk of new keys and values into the 8-bit
+ * cache (README decode list: the new token's key and value join the cache, and
+ * the position-0 key is recorded when the first token is written; this is the
+ * prefill's form, many tokens at once). Token t < n_new[b] of sequence b goes to
+ * slot start[b] + t; nothing else of the caches or the scales is touched.
+ * Where the slot is 0, k0[b] and v0[b] receive the bf16 rows. The keys are
+ * stored as given (already rotated).
+ *
+ *   dims        batch, n_kv_heads, head_dim and max_seq_len are used
+ *   kv_type     SR_KV_E4M3 or SR_KV_INT8
+ *   n_tokens    T >= 1: tokens per sequence in k_new / v_new
+ *   k_new, v_new  bf16 [B, T, Hkv, d] with the strides k_strides, v_strides
+ *               (views of a fused projection, say); must not overlap the outputs
+ *   start       int32 [B] device
+ *   n_new       int32 [B] device, each in [0, T] (else clamped, SR_DEVERR_ROW_COUNT)
+ *   k_cache, v_cache, kv_scales   out, as above; start[b] + t outside [0, Lmax)
+ *               is skipped (SR_DEVERR_APPEND_SLOT)
+ *   k0, v0      out bf16 [B, Hkv, d], or both NULL
+ *   device_error optional device int32 (NULL = not wanted); bits are ORed in
+ * One launch, asynchronous on `stream`, no workspace. Errors:
+ * SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
+ */
+sr_status sr_kv_append_quant(const sr_dims *dims, int32_t kv_type, int32_t n_tokens, const void *k_new,
+                             const sr_row_strides *k_strides, const void *v_new,
+                             const sr_row_strides *v_strides, const int32_t *start, const int32_t *n_new,
+                             void *k_cache, void *v_cache, float *kv_scales, void *k0, void *v0,
+                             int32_t *device_error, void *stream);
+
+/*
+ * sr_kv_dequant -- read rows of the 8-bit cache back as bf16, in the layout of a
+ * bf16 cache: k_out[b, g, t] = bf16(code * scale) of position start[b] + t for
+ * t < n[b]; rows behind n[b] are left as they were. (An engineering addition: it
+ * moves a context to the bf16 entry points, a shared prefix among them.)
+ *
+ *   n_rows      T >= 1: rows allocated per unit in k_out / v_out
+ *   start, n    int32 [B] device, as for sr_kv_append_quant
+ *   k_out, v_out out bf16 [B, Hkv, T, d]
+ *   device_error optional device int32, as for sr_kv_append_quant
+ * code * scale is rounded to fp32 and then to bf16; with e4m3 rows of this
+ * library's writers both are exact. One launch, no workspace. Errors:
+ * SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
+ */
+sr_status sr_kv_dequant(const sr_dims *dims, int32_t kv_type, int32_t n_rows, const void *k_cache,
+                        const void *v_cache, const float *kv_scales, const int32_t *start, const int32_t *n,
+                        void *k_out, void *v_out, int32_t *device_error, void *stream);
+
+/*
+ * sr_rope_append_route_kv -- sr_rope_append_route for a cache of any sr_kv_type
+ * and for sequences whose own cache begins at a later position (behind a prefix
+ * that the batch shares). Everything is as there, with these differences:
+ *   kv_type     what k_cache / v_cache hold; for the 8-bit types the rotated key
+ *               (as the correctly rounded bf16 row) and the value are quantised
+ *               into slot seq_lens[b] and its scales
+ *   kv_scales   in/out fp32 [B, Hkv, Lmax, 2], 16-byte aligned; NULL for SR_KV_BF16
+ *   pos_offset  >= 0: slot p holds position pos_offset + p, which rotates the
+ *               query and the key and must be below max_pos; k0 / v0 are
+ *               captured when that position is 0
+ *   seq_lens    int32 [B]: the slot to write
+ *   seq_lens_out out int32 [B]: seq_lens[b] + 1, or seq_lens[b] where nothing was
+ *               appended; may be seq_lens itself
+ * One launch. Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
+ */
+sr_status sr_rope_append_route_kv(const sr_dims *dims, int32_t kv_type, int32_t pos_offset, const void *q_in,
+                                  const void *k_new, const void *v_new, const float *rope_cos,
+                                  const float *rope_sin, int32_t max_pos, const int32_t *seq_lens,
+                                  int32_t *seq_lens_out, void *k_cache, void *v_cache, float *kv_scales,
+                                  void *k0, void *v0, float tau, void *q_out, uint8_t *route_mask,
+                                  int32_t *active_list, int32_t *device_error, void *stream);
+
+/*
+ * sr_decode_attention_quant -- sr_decode_attention over the 8-bit cache: the
+ * softmax attention of the values that the codes stand for. Sink units are
+ * served from v0 as there. fp32 logits, softmax statistics and sums; the query
+ * and the softmax weights (times the value rows' scales) enter the products in
+ * fp16, scaled by powers of two (query: exact to 2^-24 of the row's largest
+ * magnitude; weights: relative 2^-11).
+ *
+ *   kv_type     SR_KV_E4M3 or SR_KV_INT8
+ *   k_cache, v_cache, kv_scales   as above, 16-byte aligned; codes and scales of
+ *               positions >= L_b are never used and may be anything
+ *   lse         optional out fp32 [B, Hq] (NULL = not wanted), as for
+ *               sr_decode_attention_lse
+ * Other arguments, results, workspace and errors: as sr_decode_attention.
+ */
+sr_status sr_decode_attention_quant(const sr_dims *dims, int32_t kv_type, const void *q, const void *k_cache,
+                                    const void *v_cache, const float *kv_scales, const void *v0,
+                                    const int32_t *seq_lens, const int32_t *active_list, int32_t n_splits,
+                                    void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* sr_decode_attention_quant_partial -- the same scan with the outputs of
+   sr_decode_attention_partial (fp32 o_part, lse_part). */
+sr_status sr_decode_attention_quant_partial(const sr_dims *dims, int32_t kv_type, const void *q,
+                                            const void *k_cache, const void *v_cache, const float *kv_scales,
+                                            const void *v0, const int32_t *seq_lens,
+                                            const int32_t *active_list, int32_t n_splits, float *o_part,
+                                            float *lse_part, void *workspace, size_t workspace_bytes,
+                                            void *stream);
+
+/*
+ * sr_prefix_attention -- one decode token of every sequence of a batch over a
+ * prefix that all of them share, read once for the whole batch, joined with each
+ * sequence's own suffix (the README's split-K reduction, carried across two
+ * caches). For query head h of an active unit (b, g):
+ *     over the prefix   lse_p = log sum_j exp(<q, K[g, j]> / sqrt(d)), j < prefix_len,
+ *                       o_p the softmax attention over those positions
+ *     without a suffix  out = bf16(o_p), lse = lse_p
+ *     with one          lse = log(exp(lse_p) + exp(lse_s)),
+ *                       out = bf16(exp(lse_p - lse) o_p + exp(lse_s - lse) o_s)
+ * Heads of a sink unit get v0 bit for bit and lse NaN. Where there is no
+ * position at all (prefix_len 0 and no suffix, or lse_s = -inf) out is 0 and lse
+ * -inf.
+ *
+ *   dims        as everywhere; max_seq_len is the capacity of the prefix
+ *   prefix_len  0 .. max_seq_len; positions behind it are never used
+ *   q           bf16 [B, Hq, d]
+ *   k_prefix, v_prefix  bf16 [Hkv, max_seq_len, d]
+ *   v0          bf16 [B, Hkv, d]
+ *   route_mask  uint8 [B*Hkv] as written by sr_route (0 = active)
+ *   o_suffix, lse_suffix  fp32 [B, Hq, d] and [B, Hq], as sr_decode_attention_partial
+ *               or _quant_partial writes them; both NULL: no suffix
+ *   out         bf16 [B, Hq, d]
+ *   lse         optional out fp32 [B, Hq] (NULL = not wanted)
+ *   workspace   device buffer of >= sr_prefix_workspace_bytes(dims) bytes,
+ *               256-byte aligned, zeroed once by sr_workspace_init; calls that
+ *               overlap on the GPU must not share one. Its first word is the
+ *               device error word (sr_get_device_error).
+ * fp32 logits, statistics and sums; the softmax weights enter the second product
+ * in bf16. Asynchronous on `stream`. Errors: SR_ERR_INVALID_ARG,
+ * SR_ERR_UNSUPPORTED, SR_ERR_WORKSPACE, SR_ERR_CUDA.
+ */
+sr_status sr_prefix_attention(const sr_dims *dims, int32_t prefix_len, const void *q, const void *k_prefix,
+                              const void *v_prefix, const void *v0, const uint8_t *route_mask,
+                              const float *o_suffix, const float *lse_suffix, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* sr_prefix_attention_partial -- the prefix's part alone, in the form that
+   sr_combine_partials takes: o_part fp32 [B, Hq, d] (v0 widened for sink heads, 0
+   where prefix_len is 0) and lse_part fp32 [B, Hq] (NaN for sink heads). */
+sr_status sr_prefix_attention_partial(const sr_dims *dims, int32_t prefix_len, const void *q,
+                                      const void *k_prefix, const void *v_prefix, const void *v0,
+                                      const uint8_t *route_mask, float *o_part, float *lse_part,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* sr_prefix_workspace_bytes -- workspace of the two calls above, for any
+   prefix_len. 0 for invalid or unsupported dims. */
+size_t sr_prefix_workspace_bytes(const sr_dims *dims);
 
 /* Size of the fixed scratch array behind sr_decode_attention_static_scratch. */
 #define SR_STATIC_SCRATCH_BYTES (8u << 20)

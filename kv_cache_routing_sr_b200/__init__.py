@@ -7,7 +7,7 @@ call into ``native`` does, and raises if it is missing or cannot run.
 """
 from importlib import import_module
 
-__all__ = ["native", "inputs", "multilayer", "context_parallel", "proxy_quality", "build"]
+__all__ = ["native", "inputs", "multilayer", "context_parallel", "shared_prefix", "proxy_quality", "build"]
 
 
 def __getattr__(name):

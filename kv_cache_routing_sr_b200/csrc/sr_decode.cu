@@ -36,9 +36,29 @@
 //    v0 into the output of every unit absent from the active list.
 //  * Every wait is bounded in time; a timeout sets a device error bit and the
 //    CTA leaves after its in-flight copies have landed.
+//
+// 8-bit caches (sr_decode_attention_quant; the format is sr_quant.cuh's) run the
+// same kernel with these parts exchanged:
+//  * A stage holds one [BN x 128]-byte box of key codes, one of value codes and
+//    the rows' scale pairs, which an untiled bulk copy brings (rounded out to
+//    16-byte boundaries).
+//  * Codes become fp16 in registers (exact for both types), four at a time. For
+//    the keys, ldmatrix leaves a lane four consecutive elements of a row, which
+//    it feeds to the two k halves of an m16n8k16: the order of the contraction
+//    is free as long as the query fragments use the same one. For the values,
+//    ldmatrix.trans leaves a lane elements d, d + 1 of two positions; a byte
+//    permute pairs the positions, so row r of the MMA is column 2 r of the
+//    16-column chunk and row r + 8 column 2 r + 1.
+//  * The key rows' scales multiply the fp32 logits; the value rows' scales
+//    multiply the softmax weights before these are rounded to fp16 (relative
+//    2^-11), relative to the largest value scale that the warp has met in the
+//    split, times 2^14: the full range of fp16 is below a row that matters. The
+//    query enters in fp16 times a power of two that puts its largest element in
+//    [2^13, 2^14).
 #include <climits>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <mutex>
@@ -61,6 +81,17 @@
 #define SR_DECODE_STAGES 2
 #endif
 
+// 8-bit caches: row blocks of 16 per consumer warp and tile, stages, consumer warps.
+#ifndef SR_QUANT_RB
+#define SR_QUANT_RB 1
+#endif
+#ifndef SR_QUANT_STAGES
+#define SR_QUANT_STAGES 4
+#endif
+#ifndef SR_QUANT_CW
+#define SR_QUANT_CW 8
+#endif
+
 SR_TL_DEFINE(tl_decode)
 #ifdef SR_TIMELINE
 // latest %globaltimer at which a decode CTA left (atomicMax); the next kernel
@@ -73,20 +104,20 @@ extern "C" int sr_timeline_last_exit_addr(void **p) { return (int)cudaGetSymbolA
 namespace sr {
 namespace {
 
-constexpr int kCWarps = 4;
-constexpr int kThreads = 32 * (kCWarps + 1);
 constexpr long long kMinChunk = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull; // 2 s: far above any legitimate wait
+constexpr int kMaxCWarps = 8; // consumer warps of the widest configuration
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;
 constexpr float kScaleLog2 = 0.12751743082459868f; // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMergeThreads = 32 * kCWarps;
 // Partials in flight per thread in the final merge (at most 32: lane k of a
 // warp loads the (m, l) of the batch's k-th partial). Each batch costs one
 // round trip for lines other SMs have just written (~0.9 us); 25 covers the 74
 // partials of a unit at 512K with 2 of 8 units active in 3 batches, and the 37
 // at 128K with 4 active in 2.
-constexpr int kMergeBatch = 25;
+// Eight consumer warps leave a thread 168 registers instead of 240, and twice
+// the threads: 12.
+__host__ __device__ constexpr int merge_batch(int warps) { return warps > 4 ? 12 : 25; }
 // Row stride (floats) of the split-end scratch that holds each warp's O per
 // head: 4 floats of padding put the lanes that store the same row of
 // different head pairs in different banks.
@@ -95,6 +126,7 @@ constexpr int kCombStride = 128 + 4;
 // so the lanes that read the same word of different heads hit different banks.
 constexpr int kQRowBytes = kHeadDim * 2 + 16;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kMinValueScale = 7.70371978e-34f; // 2^-110: value scales count as at least this in O's units
 constexpr int kFastUnits = 32; // launches with at most this many units plan in registers
 
 struct alignas(16) TileHdr {
@@ -105,7 +137,7 @@ struct alignas(16) TileHdr {
     int32_t slot;       // partial slot of this split
     int32_t nseg;       // splits of this unit
     int32_t slot_first; // slot of the unit's first split (its slots are consecutive)
-    int32_t pad;
+    int32_t sc0;        // 8-bit caches: scale pair of tile row 0 in the stage's scale buffer
 };
 
 #ifndef SR_DECODE_SEQTAB
@@ -132,7 +164,7 @@ struct Misc {
     int i0;
     int pad;
     long long s0;
-    long long wsum[kCWarps + 1];
+    long long wsum[kMaxCWarps + 1];
     int first_bad; // first malformed entry of the active list (INT_MAX: none)
     int first_u;   // unit of the producer's first active entry (-1: none)
     uint8_t sflag[32]; // fused routing of at most 32 units: sink flags
@@ -156,17 +188,28 @@ struct Params {
     int32_t *active_out; // may be null
     float *lse;          // [B, Hq] natural-log log-sum-exp of the logits; may be null
     float *out_f32;      // when set, the output is written here in fp32 instead of `out`
+    const float2 *scales; // 8-bit caches: (key, value) scale of every position
 };
 
-template <int RB, int STAGES> struct Cfg {
-    static constexpr int BN = 16 * RB * kCWarps; // positions per tile
-    static constexpr int HALF = BN * 128;        // one [BN x 64] bf16 box
-    static constexpr int STAGE = 4 * HALF;       // K lo, K hi, V lo, V hi
+template <int RB_, int STAGES_, int CW_, int KV_> struct Cfg {
+    static constexpr int RB = RB_, STAGES = STAGES_;
+    static constexpr int CW = CW_; // consumer warps
+    static constexpr int KV = KV_;
+    static constexpr bool QUANT = KV != SR_KV_BF16;
+    static constexpr int THREADS = 32 * (CW + 1);
+    static constexpr int MERGE_THREADS = 32 * CW;
+    static constexpr int BN = 16 * RB * CW;      // positions per tile
+    static constexpr int HALF = BN * 128;        // one [BN x 64] bf16 box, or one [BN x 128] box of codes
+    static constexpr int NBOX = QUANT ? 2 : 4;   // K, V codes; or K lo, K hi, V lo, V hi
+    static constexpr int OFF_V = NBOX / 2 * HALF; // value boxes in a stage
+    static constexpr int STAGE = NBOX * HALF;
+    static constexpr int SCALES = QUANT ? (BN + 2) * 8 : 0; // rows, and one more at either end
     static constexpr int QBYTES = kMaxGroup * kQRowBytes;
     static constexpr int OFF_Q = STAGES * STAGE;
     static constexpr int OFF_COMB = OFF_Q + STAGES * QBYTES;
-    static constexpr int OFF_ML = OFF_COMB + kCWarps * kMaxGroup * kCombStride * 4;
-    static constexpr int OFF_HDR = OFF_ML + kCWarps * kMaxGroup * 8;
+    static constexpr int OFF_ML = OFF_COMB + CW * kMaxGroup * kCombStride * 4;
+    static constexpr int OFF_SCALES = OFF_ML + CW * kMaxGroup * 8;
+    static constexpr int OFF_HDR = OFF_SCALES + STAGES * SCALES;
     static constexpr int OFF_BAR = OFF_HDR + STAGES * (int)sizeof(TileHdr);
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2) * 8;
     static constexpr int OFF_BITMAP = OFF_MISC + 256;
@@ -177,6 +220,8 @@ template <int RB, int STAGES> struct Cfg {
     static constexpr int BYTES = OFF_RANK + 32 * (int)sizeof(RankInfo);
     static constexpr int ALLOC = BYTES + 1024; // room to align the base to 1024 B
     static_assert(sizeof(Misc) <= 256, "misc block");
+    static_assert(CW <= kMaxCWarps, "block_scan");
+    static_assert(OFF_SCALES % 16 == 0 && SCALES % 16 == 0 && OFF_HDR % 16 == 0, "alignment");
     // Prologue tables (active lengths, active units, sink flags) live in the
     // stage buffers before the first copy is issued.
     static_assert(SR_MAX_UNITS * 7 <= STAGES * STAGE, "prologue tables");
@@ -237,6 +282,7 @@ __device__ __forceinline__ int next_set_bit(const uint32_t *bm, int from, int U)
 }
 
 // Inclusive block-wide prefix of a 64-bit value; *total receives the block sum.
+template <int NWARPS>
 __device__ __forceinline__ long long block_scan(long long x, Misc *misc, long long *total)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +298,7 @@ __device__ __forceinline__ long long block_scan(long long x, Misc *misc, long lo
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kCWarps + 1; ++w) {
+    for (int w = 0; w < NWARPS; ++w) {
         const long long s = misc->wsum[w];
         before += (w < warp) ? s : 0;
         all += s;
@@ -266,40 +312,127 @@ __device__ __forceinline__ long long block_scan(long long x, Misc *misc, long lo
 // arithmetic (sr_route_math.cuh, one warp per GQA group, loads straight from
 // global memory), so its decisions equal sr_route's bit for bit; CTA 0 also
 // writes the route mask. flag[u] = sink. Called by all threads; no barrier.
-template <int M>
+template <int M, int NWARPS>
 __device__ __forceinline__ void route_all_units(const Params &p, int U, uint8_t *flag)
 {
     route_units_warp<M, true>(reinterpret_cast<const uint4 *>(p.q), reinterpret_cast<const uint4 *>(p.k0), U, p.tau,
-                              (int)threadIdx.x >> 5, kThreads / 32, [&](int u, bool sink) {
+                              (int)threadIdx.x >> 5, NWARPS, [&](int u, bool sink) {
                                   flag[u] = sink ? 1 : 0;
                                   if (blockIdx.x == 0 && p.mask_out)
                                       p.mask_out[u] = sink ? 1 : 0;
                               });
 }
 
+template <int NWARPS>
 __device__ __forceinline__ void route_all_units(const Params &p, int U, uint8_t *flag, int M)
 {
     switch (M) {
     case 1:
-        route_all_units<1>(p, U, flag);
+        route_all_units<1, NWARPS>(p, U, flag);
         break;
     case 2:
-        route_all_units<2>(p, U, flag);
+        route_all_units<2, NWARPS>(p, U, flag);
         break;
     case 4:
-        route_all_units<4>(p, U, flag);
+        route_all_units<4, NWARPS>(p, U, flag);
         break;
     default:
-        route_all_units<8>(p, U, flag);
+        route_all_units<8, NWARPS>(p, U, flag);
         break;
     }
 }
 
-template <int RB, int STAGES, bool FUSED>
-__global__ void __launch_bounds__(kThreads, 1)
+// Issues the copies of one tile into a stage, all counted on its full barrier,
+// which must already expect tile_bytes() of them. Returns the scale pair of tile
+// row 0 in the stage's scale buffer.
+template <class C> struct TileScales {
+    int32_t sc0 = 0;      // scale pair of row 0 in the buffer
+    uint32_t bytes = 0;   // bulk copy
+    const float2 *src = nullptr;
+    bool tail = false;    // the pair behind the copy is moved by the issuing lane
+};
+
+// The scale pairs of rows [pos0, pos0 + BN) of unit u that exist, rounded out to
+// 16-byte boundaries. Only the array's very last pair can have no neighbour to
+// round to (an odd number of pairs): that one is moved on its own.
+template <class C> __device__ __forceinline__ TileScales<C> tile_scales(const Params &p, int u, int pos0)
+{
+    TileScales<C> r;
+    if constexpr (C::QUANT) {
+        const long long base = (long long)u * p.Lmax, total = (long long)p.B * p.Hkv * p.Lmax;
+        const long long i0 = base + pos0, i1 = base + min((long long)pos0 + C::BN, (long long)p.Lmax);
+        const long long a0 = i0 & ~1ll;
+        long long a1 = (i1 + 1) & ~1ll;
+        if (a1 > total) {
+            a1 -= 2;
+            r.tail = true;
+        }
+        r.sc0 = (int32_t)(i0 - a0);
+        r.bytes = (uint32_t)(a1 - a0) * 8u;
+        r.src = p.scales + a0;
+    }
+    return r;
+}
+
+template <class C>
+__device__ __forceinline__ void issue_tile(const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *smem, int stage,
+                                           uint32_t fb, int pos0, int unit, const TileScales<C> &sc, uint64_t pol)
+{
+    const uint32_t sb = smem_u32(smem + stage * C::STAGE);
+    if constexpr (C::QUANT) {
+        tma_load_3d(sb, tmK, fb, 0, pos0, unit, pol);
+        tma_load_3d(sb + C::OFF_V, tmV, fb, 0, pos0, unit, pol);
+        uint8_t *dst = smem + C::OFF_SCALES + stage * C::SCALES;
+        if (sc.bytes)
+            bulk_load(smem_u32(dst), sc.src, sc.bytes, fb);
+        if (sc.tail)
+            *reinterpret_cast<float2 *>(dst + sc.bytes) = __ldg(sc.src + sc.bytes / 8);
+    } else {
+        tma_load_3d(sb, tmK, fb, 0, pos0, unit, pol);
+        tma_load_3d(sb + C::HALF, tmK, fb, 64, pos0, unit, pol);
+        tma_load_3d(sb + 2 * C::HALF, tmV, fb, 0, pos0, unit, pol);
+        tma_load_3d(sb + 3 * C::HALF, tmV, fb, 64, pos0, unit, pol);
+    }
+}
+
+// Four codes -> four fp16 (exact): elements 0, 1 in lo and 2, 3 in hi.
+template <int KV> __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (KV == SR_KV_E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // code + 128 as the low byte of an fp16 in [1024, 1280), then - 1152
+        const uint32_t x = w ^ 0x80808080u;
+        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        const uint32_t l = __byte_perm(x, 0x64u, 0x4140), h = __byte_perm(x, 0x64u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), bias);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), bias);
+        lo = *reinterpret_cast<const uint32_t *>(&a);
+        hi = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 2^n for -126 <= n <= 127
+__device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+
+template <class C, bool FUSED>
+__global__ void __launch_bounds__(C::THREADS, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
 {
-    using C = Cfg<RB, STAGES>;
+    constexpr int RB = C::RB, STAGES = C::STAGES;
+    constexpr int kCWarps = C::CW, kThreads = C::THREADS, kMergeThreads = C::MERGE_THREADS;
+    constexpr int kMergeBatch = merge_batch(C::CW);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     TileHdr *hdr = reinterpret_cast<TileHdr *>(smem + C::OFF_HDR);
@@ -399,7 +532,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             lane_unit = (lane < n) ? e : 0;
             act_bits = __reduce_or_sync(kFull, (lane < n) ? (1u << lane_unit) : 0u);
         } else {
-            route_all_units(p, U, misc->sflag, M);
+            route_all_units<kThreads / 32>(p, U, misc->sflag, M);
             __syncthreads();
             act_bits = __ballot_sync(kFull, lane < U && !misc->sflag[lane]);
             n = __popc(act_bits);
@@ -492,7 +625,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         if (seq_smem)
             for (int b = tid; b < p.B; b += kThreads)
                 seqtab[b] = __ldg(p.seq_lens + b);
-        route_all_units(p, U, sflag, M);
+        route_all_units<kThreads / 32>(p, U, sflag, M);
         __syncthreads();
         // Ordered compaction of the active units into the same tables the
         // work-list path builds.
@@ -500,7 +633,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             const int u = c0 + tid;
             const bool act = (u < U) && !sflag[u];
             long long tot;
-            const long long incl = block_scan(act ? 1 : 0, misc, &tot);
+            const long long incl = block_scan<kThreads / 32>(act ? 1 : 0, misc, &tot);
             if (act) {
                 const int i = n + (int)incl - 1;
                 int L = seq_smem ? seqtab[u / p.Hkv] : __ldg(p.seq_lens + u / p.Hkv);
@@ -521,7 +654,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             p.active_out[0] = n;
     }
     if (!fast) {
-        (void)block_scan(local, misc, &P);
+        (void)block_scan<kThreads / 32>(local, misc, &P);
         if (errbits && blockIdx.x == 0)
             atomicOr(p.err, errbits);
     }
@@ -562,14 +695,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 // position r0 - s0, with the group's q rows) into stage 0 now:
                 // its full barrier expects the bytes but cannot complete
                 // before the header is written and the producer arrives.
-                const uint32_t sb = smem_u32(smem);
                 const uint64_t pol0 = l2_policy_evict_first();
-                mbar_expect_tx(full0, (uint32_t)C::STAGE + (uint32_t)(M * kHeadDim * 2));
                 const int pos0 = (int)(r0 - s0);
-                tma_load_3d(sb, &tmK, full0, 0, pos0, fu, pol0);
-                tma_load_3d(sb + C::HALF, &tmK, full0, 64, pos0, fu, pol0);
-                tma_load_3d(sb + 2 * C::HALF, &tmV, full0, 0, pos0, fu, pol0);
-                tma_load_3d(sb + 3 * C::HALF, &tmV, full0, 64, pos0, fu, pol0);
+                const TileScales<C> sc = tile_scales<C>(p, fu, pos0);
+                mbar_expect_tx(full0, (uint32_t)C::STAGE + (uint32_t)(M * kHeadDim * 2) + sc.bytes);
+                issue_tile<C>(&tmK, &tmV, smem, 0, full0, pos0, fu, sc, pol0);
                 const uint8_t *qsrc = reinterpret_cast<const uint8_t *>(p.q + (size_t)fq * kHeadDim);
                 for (int hq = 0; hq < M; ++hq)
                     bulk_load(smem_u32(smem + C::OFF_Q + hq * kQRowBytes), qsrc + hq * kHeadDim * 2, kHeadDim * 2,
@@ -602,7 +732,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 const int i = base + tid;
                 const int L = (i < n) ? ltab[i] : 0;
                 long long tot;
-                const long long incl = block_scan(L, misc, &tot);
+                const long long incl = block_scan<kThreads / 32>(L, misc, &tot);
                 const long long S = carry + incl - L;
                 if (i < n && L > 0 && S <= r0 && r0 < S + L) {
                     misc->i0 = i;
@@ -643,7 +773,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             issued_parity[0] = 0; // the first tile's copies are in flight
         bool ok = true;
 
-        auto emit = [&](const TileHdr &h, const void *qsrc, uint32_t qbytes) -> bool {
+        auto emit = [&](TileHdr h, const void *qsrc, uint32_t qbytes) -> bool {
 #ifdef SR_TIMELINE
             const bool tl_first = issued_parity[stage] < 0 && stage == 0 && ph == 0;
             if (tl_first)
@@ -655,6 +785,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             if (tl_first)
                 SR_STAMP(tl_decode, 18);
 #endif
+            TileScales<C> sc;
+            if (h.nvalid > 0)
+                sc = tile_scales<C>(p, h.unit, h.pos0);
+            h.sc0 = sc.sc0;
             hdr[stage] = h;
             const uint32_t fb = full0 + 8 * stage;
             if (early) {
@@ -668,19 +802,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 }
                 return true;
             }
-            const uint32_t bytes = (h.nvalid > 0 ? (uint32_t)C::STAGE : 0u) + qbytes;
+            const uint32_t bytes = (h.nvalid > 0 ? (uint32_t)C::STAGE + sc.bytes : 0u) + qbytes;
             if (bytes) {
                 mbar_arrive_expect_tx(fb, bytes);
                 if (h.nvalid > 0) {
-                    const uint32_t sb = smem_u32(smem + stage * C::STAGE);
 #ifdef SR_TIMELINE
                     if (tl_first)
                         SR_STAMP(tl_decode, 19);
 #endif
-                    tma_load_3d(sb, &tmK, fb, 0, h.pos0, h.unit, pol);
-                    tma_load_3d(sb + C::HALF, &tmK, fb, 64, h.pos0, h.unit, pol);
-                    tma_load_3d(sb + 2 * C::HALF, &tmV, fb, 0, h.pos0, h.unit, pol);
-                    tma_load_3d(sb + 3 * C::HALF, &tmV, fb, 64, h.pos0, h.unit, pol);
+                    issue_tile<C>(&tmK, &tmV, smem, stage, fb, h.pos0, h.unit, sc, pol);
                 }
                 // the group's q rows, one copy per head into the padded rows
                 if (qbytes)
@@ -719,7 +849,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 h.slot = slot;
                 h.nseg = nseg;
                 h.slot_first = slot_first;
-                h.pad = 0;
+                h.sc0 = 0;
                 const uint32_t qb = (t == 0 && len > 0) ? (uint32_t)(M * kHeadDim * 2) : 0u;
                 if (!emit(h, qsrc, qb))
                     return false;
@@ -875,6 +1005,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     }
     mrun[0] = mrun[1] = -INFINITY;
     lrun[0] = lrun[1] = 0.f;
+    // 8-bit caches: logit factor of heads 2t and 2t + 1 (the query's power of two
+    // taken back, and log2(e) / sqrt(d)); the largest value scale met in the
+    // split, in whose units times 2^-14 O accumulates
+    float cq0 = 0.f, cq1 = 0.f, vref = kMinValueScale;
 
     int stage = 0;
     uint32_t ph = 0, cph = 0;
@@ -927,27 +1061,70 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             // with them and every split's last tile resets them.
             if (h.nvalid > 0) {
                 const uint32_t *qs = reinterpret_cast<const uint32_t *>(smem + C::OFF_Q + stage * C::QBYTES);
+                if constexpr (!C::QUANT) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    qf[ks][0] = (g < M) ? qs[g * (kQRowBytes / 4) + ks * 8 + t] : 0u;
-                    qf[ks][1] = (g < M) ? qs[g * (kQRowBytes / 4) + ks * 8 + 4 + t] : 0u;
+                    for (int ks = 0; ks < 8; ++ks) {
+                        qf[ks][0] = (g < M) ? qs[g * (kQRowBytes / 4) + ks * 8 + t] : 0u;
+                        qf[ks][1] = (g < M) ? qs[g * (kQRowBytes / 4) + ks * 8 + 4 + t] : 0u;
+                    }
+                } else {
+                    // elements 16 ks + 4t .. + 3 of the head's row
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            qf[ks][e] = (g < M) ? qs[g * (kQRowBytes / 4) + ks * 8 + 2 * t + e] : 0u;
+                            top = __vmaxu2(top, qf[ks][e] & 0x7fff7fffu);
+                        }
+                    top = max(top & 0xffffu, top >> 16);
+                    top = max(top, __shfl_xor_sync(kFull, top, 1));
+                    top = max(top, __shfl_xor_sync(kFull, top, 2));
+                    // 2^n brings the largest element into [2^13, 2^14); a row
+                    // below 2^-100 counts as 2^-100
+                    const int ex = max((int)(top >> 7) - 127, -100);
+                    const float mul = exp2_int(13 - ex);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            qf[ks][e] = pack_f16x2(__uint_as_float(qf[ks][e] << 16) * mul,
+                                                   __uint_as_float(qf[ks][e] & 0xffff0000u) * mul);
+                    const float back = exp2_int(ex - 13) * kScaleLog2;
+                    cq0 = __shfl_sync(kFull, back, 8 * t);
+                    cq1 = __shfl_sync(kFull, back, 8 * t + 4);
                 }
             }
         }
 
         if (h.nvalid > my_row0) {
-            if (h.nvalid < my_row0 + RB * 16) {
+            if (C::KV != SR_KV_INT8 && h.nvalid < my_row0 + RB * 16) {
                 // Rows past the split may be padding (even NaN): zero this
                 // warp's V rows there so that P = 0 contributes exactly 0.
                 const int z0 = h.nvalid, nz = my_row0 + RB * 16 - z0;
-                for (int e = lane; e < nz * 16; e += 32) {
-                    const int row = z0 + (e >> 4), c = e & 15;
-                    uint4 *dst = reinterpret_cast<uint4 *>(smem + stage * C::STAGE + (2 + (c >> 3)) * C::HALF +
+                constexpr int CH = C::QUANT ? 8 : 16; // 16-byte chunks of a value row
+                for (int e = lane; e < nz * CH; e += 32) {
+                    const int row = z0 + e / CH, c = e % CH;
+                    uint4 *dst = reinterpret_cast<uint4 *>(smem + stage * C::STAGE + C::OFF_V + (c >> 3) * C::HALF +
                                                            row * 128 + (c & 7) * 16);
                     *dst = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
+            }
+
+            // 8-bit caches: the scale pairs of this lane's rows g, g + 8 of each
+            // block; rows behind the split count as zero.
+            float2 rsc[RB][2];
+            if constexpr (C::QUANT) {
+                const float2 *scs = reinterpret_cast<const float2 *>(smem + C::OFF_SCALES + stage * C::SCALES) + h.sc0;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = my_row0 + rb * 16 + g + e * 8;
+                        rsc[rb][e] = (row < h.nvalid) ? scs[row] : make_float2(0.f, 0.f);
+                    }
             }
 
             // S^T[16 rows x 8 heads] per row block, two accumulators per block.
@@ -959,18 +1136,37 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sa[rb][e] = sb[rb][e] = 0.f;
+                if constexpr (C::QUANT) {
+                    // two 16-element chunks a ldmatrix
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t kb = st + (uint32_t)(ks >> 2) * C::HALF;
-                    const uint32_t cx = (uint32_t)(((ks & 3) * 2 + (mi >> 1)) ^ ri) << 4;
+                    for (int k2 = 0; k2 < 4; ++k2) {
+                        const uint32_t cx = (uint32_t)((k2 * 2 + (mi >> 1)) ^ ri) << 4;
 #pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) {
-                        uint32_t a[4];
-                        ldmatrix_x4(a, kb + rowK[rb] + cx);
-                        if (ks & 1)
-                            mma_bf16_16816(sb[rb], a, qf[ks][0], qf[ks][1]);
-                        else
-                            mma_bf16_16816(sa[rb], a, qf[ks][0], qf[ks][1]);
+                        for (int rb = 0; rb < RB; ++rb) {
+                            uint32_t r[4], a[4];
+                            ldmatrix_x4(r, st + rowK[rb] + cx);
+                            codes_to_f16<C::KV>(r[0], a[0], a[2]);
+                            codes_to_f16<C::KV>(r[1], a[1], a[3]);
+                            mma_f16_16816(sa[rb], a, qf[2 * k2][0], qf[2 * k2][1]);
+                            codes_to_f16<C::KV>(r[2], a[0], a[2]);
+                            codes_to_f16<C::KV>(r[3], a[1], a[3]);
+                            mma_f16_16816(sb[rb], a, qf[2 * k2 + 1][0], qf[2 * k2 + 1][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t kb = st + (uint32_t)(ks >> 2) * C::HALF;
+                        const uint32_t cx = (uint32_t)(((ks & 3) * 2 + (mi >> 1)) ^ ri) << 4;
+#pragma unroll
+                        for (int rb = 0; rb < RB; ++rb) {
+                            uint32_t a[4];
+                            ldmatrix_x4(a, kb + rowK[rb] + cx);
+                            if (ks & 1)
+                                mma_bf16_16816(sb[rb], a, qf[ks][0], qf[ks][1]);
+                            else
+                                mma_bf16_16816(sa[rb], a, qf[ks][0], qf[ks][1]);
+                        }
                     }
                 }
 #pragma unroll
@@ -978,7 +1174,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int row = my_row0 + rb * 16 + g + (e >> 1) * 8;
-                        sacc[rb][e] = (row < h.nvalid) ? (sa[rb][e] + sb[rb][e]) * kScaleLog2 : -INFINITY;
+                        float f = kScaleLog2;
+                        if constexpr (C::QUANT)
+                            f = rsc[rb][e >> 1].x * ((e & 1) ? cq1 : cq0);
+                        sacc[rb][e] = (row < h.nvalid) ? (sa[rb][e] + sb[rb][e]) * f : -INFINITY;
                     }
             }
 
@@ -1000,6 +1199,26 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             const float al0 = exp2f(mrun[0] - mu0), al1 = exp2f(mrun[1] - mu1);
             mrun[0] = mn0;
             mrun[1] = mn1;
+            // 8-bit caches: factors of the weights (value scale over the reference)
+            // and of the O so far (old reference over new)
+            float wv[RB][2], grow = 1.f;
+            if constexpr (C::QUANT) {
+                float vm = vref;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+                    vm = fmaxf(vm, fmaxf(fabsf(rsc[rb][0].y), fabsf(rsc[rb][1].y)));
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    vm = fmaxf(vm, __shfl_xor_sync(kFull, vm, off));
+                const float inv = __fdividef(1.f, vm);
+                grow = vref * inv;
+                vref = vm;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    wv[rb][0] = rsc[rb][0].y * inv * 16384.f;
+                    wv[rb][1] = rsc[rb][1].y * inv * 16384.f;
+                }
+            }
             float ps0 = 0.f, ps1 = 0.f;
             uint32_t pf[RB][2];
 #pragma unroll
@@ -1008,29 +1227,53 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 const float p2 = exp2f(sacc[rb][2] - mu0), p3 = exp2f(sacc[rb][3] - mu1);
                 ps0 += p0 + p2;
                 ps1 += p1 + p3;
-                pf[rb][0] = movmatrix_trans(pack_bf16x2(p0, p1));
-                pf[rb][1] = movmatrix_trans(pack_bf16x2(p2, p3));
+                if constexpr (C::QUANT) {
+                    pf[rb][0] = movmatrix_trans(pack_f16x2(p0 * wv[rb][0], p1 * wv[rb][0]));
+                    pf[rb][1] = movmatrix_trans(pack_f16x2(p2 * wv[rb][1], p3 * wv[rb][1]));
+                } else {
+                    pf[rb][0] = movmatrix_trans(pack_bf16x2(p0, p1));
+                    pf[rb][1] = movmatrix_trans(pack_bf16x2(p2, p3));
+                }
             }
             lrun[0] = lrun[0] * al0 + ps0;
             lrun[1] = lrun[1] * al1 + ps1;
+            const float ao0 = C::QUANT ? al0 * grow : al0, ao1 = C::QUANT ? al1 * grow : al1;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j][0] *= al0;
-                o[j][1] *= al1;
-                o[j][2] *= al0;
-                o[j][3] *= al1;
+                o[j][0] *= ao0;
+                o[j][1] *= ao1;
+                o[j][2] *= ao0;
+                o[j][3] *= ao1;
             }
 
             // O^T[128 x 8 heads] += V^T * P^T, 16 head-dim rows per MMA.
+            if constexpr (C::QUANT) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t vb = st + (uint32_t)(2 + (j >> 2)) * C::HALF;
-                const uint32_t cx = (uint32_t)(((j & 3) * 2 + (mi & 1)) ^ ri) << 4;
+                for (int j = 0; j < 8; j += 2) {
+                    const uint32_t cx = (uint32_t)((j + (mi >> 1)) ^ ri) << 4;
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    uint32_t a[4];
-                    ldmatrix_x4_trans(a, vb + rowV[rb] + cx);
-                    mma_bf16_16816(o[j], a, pf[rb][0], pf[rb][1]);
+                    for (int rb = 0; rb < RB; ++rb) {
+                        uint32_t r[4], a[4];
+                        ldmatrix_x4_trans(r, st + C::OFF_V + rowK[rb] + cx);
+                        codes_to_f16<C::KV>(__byte_perm(r[0], 0u, 0x3120), a[0], a[1]);
+                        codes_to_f16<C::KV>(__byte_perm(r[1], 0u, 0x3120), a[2], a[3]);
+                        mma_f16_16816(o[j], a, pf[rb][0], pf[rb][1]);
+                        codes_to_f16<C::KV>(__byte_perm(r[2], 0u, 0x3120), a[0], a[1]);
+                        codes_to_f16<C::KV>(__byte_perm(r[3], 0u, 0x3120), a[2], a[3]);
+                        mma_f16_16816(o[j + 1], a, pf[rb][0], pf[rb][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t vb = st + (uint32_t)(2 + (j >> 2)) * C::HALF;
+                    const uint32_t cx = (uint32_t)(((j & 3) * 2 + (mi & 1)) ^ ri) << 4;
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) {
+                        uint32_t a[4];
+                        ldmatrix_x4_trans(a, vb + rowV[rb] + cx);
+                        mma_bf16_16816(o[j], a, pf[rb][0], pf[rb][1]);
+                    }
                 }
             }
         }
@@ -1057,16 +1300,31 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             }
             // Unscaled O of this warp; the readers below weight the four warps.
             float *cw = comb + w * (kMaxGroup * kCombStride);
+            if constexpr (C::QUANT) {
+                const float unit = vref * 6.103515625e-05f; // 2^-14
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d0 = 16 * j + g;
-                if (2 * t < M) {
-                    cw[(2 * t) * kCombStride + d0] = o[j][0];
-                    cw[(2 * t) * kCombStride + d0 + 8] = o[j][2];
+                for (int j = 0; j < 8; ++j) {
+                    const int d0 = 16 * j + 2 * g;
+                    if (2 * t < M)
+                        *reinterpret_cast<float2 *>(cw + (2 * t) * kCombStride + d0) =
+                            make_float2(o[j][0] * unit, o[j][2] * unit);
+                    if (2 * t + 1 < M)
+                        *reinterpret_cast<float2 *>(cw + (2 * t + 1) * kCombStride + d0) =
+                            make_float2(o[j][1] * unit, o[j][3] * unit);
                 }
-                if (2 * t + 1 < M) {
-                    cw[(2 * t + 1) * kCombStride + d0] = o[j][1];
-                    cw[(2 * t + 1) * kCombStride + d0 + 8] = o[j][3];
+                vref = kMinValueScale;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int d0 = 16 * j + g;
+                    if (2 * t < M) {
+                        cw[(2 * t) * kCombStride + d0] = o[j][0];
+                        cw[(2 * t) * kCombStride + d0 + 8] = o[j][2];
+                    }
+                    if (2 * t + 1 < M) {
+                        cw[(2 * t + 1) * kCombStride + d0] = o[j][1];
+                        cw[(2 * t + 1) * kCombStride + d0 + 8] = o[j][3];
+                    }
                 }
             }
             if (!(ok = cbar_sync()))
@@ -1272,24 +1530,50 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// 3-D view [units][Lmax][128] of a bf16 cache; a box is 64 columns (128 bytes,
-// swizzled 128B) by `rows` positions of one unit. Rows past Lmax read as zero.
-bool make_cache_map(CUtensorMap *map, const void *base, int units, int lmax, int rows)
+// 3-D view [units][Lmax][128] of a cache; a box is 128 bytes of a row (64 bf16
+// values, or all 128 codes; swizzled 128B) by `rows` positions of one unit. Rows
+// past Lmax read as zero.
+bool make_cache_map(CUtensorMap *map, const void *base, int units, int lmax, int rows, bool quant)
 {
     auto fn = encode_fn();
     if (!fn)
         return false;
+    const cuuint64_t row_bytes = quant ? kHeadDim : kHeadDim * 2;
     cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)lmax, (cuuint64_t)units};
-    cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)lmax * kHeadDim * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+    cuuint64_t strides[2] = {row_bytes, (cuuint64_t)lmax * row_bytes};
+    cuuint32_t box[3] = {quant ? 128u : 64u, (cuuint32_t)rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
-using DecodeCfg = Cfg<SR_DECODE_RB, SR_DECODE_STAGES>;
+using DecodeCfg = Cfg<SR_DECODE_RB, SR_DECODE_STAGES, 4, SR_KV_BF16>;
+// 8-bit caches: eight consumer warps of one row block each, the same 128 rows a
+// tile, in four 32 KB stages.
+template <int KV> using QuantCfg = Cfg<SR_QUANT_RB, SR_QUANT_STAGES, SR_QUANT_CW, KV>;
+
+// One kernel of the family: its launch shape.
+struct Variant {
+    KernelFn fn;
+    int threads, smem, rows;
+};
+
+template <class C, bool FUSED> Variant variant()
+{
+    return {decode_kernel<C, FUSED>, C::THREADS, C::ALLOC, C::BN};
+}
+
+Variant pick(int kv, bool fused)
+{
+    if (kv == SR_KV_E4M3)
+        return variant<QuantCfg<SR_KV_E4M3>, false>();
+    if (kv == SR_KV_INT8)
+        return variant<QuantCfg<SR_KV_INT8>, false>();
+    return fused ? variant<DecodeCfg, true>() : variant<DecodeCfg, false>();
+}
 
 cudaError_t configure(int dev, DeviceInfo &info)
 {
@@ -1299,16 +1583,17 @@ cudaError_t configure(int dev, DeviceInfo &info)
     cudaError_t e = cudaDeviceGetAttribute(&info.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    KernelFn k = decode_kernel<SR_DECODE_RB, SR_DECODE_STAGES, false>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg::ALLOC);
-    if (e != cudaSuccess)
-        return e;
-    e = cudaFuncSetAttribute(decode_kernel<SR_DECODE_RB, SR_DECODE_STAGES, true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg::ALLOC);
-    if (e != cudaSuccess)
-        return e;
+    // Every variant takes more than half of an SM's shared memory, so the
+    // grid (one CTA per SM) is the same for all of them.
+    const Variant all[] = {pick(SR_KV_BF16, false), pick(SR_KV_BF16, true), pick(SR_KV_E4M3, false),
+                           pick(SR_KV_INT8, false)};
+    for (const Variant &v : all) {
+        e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e != cudaSuccess)
+            return e;
+    }
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kThreads, DecodeCfg::ALLOC);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, all[0].fn, all[0].threads, all[0].smem);
     if (e != cudaSuccess)
         return e;
     if (per_sm < 1)
@@ -1351,8 +1636,10 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream)
         return e;
     const int U = a.batch * a.n_kv_heads;
     CUtensorMap tmK, tmV;
-    if (!make_cache_map(&tmK, a.k_cache, U, a.max_seq_len, DecodeCfg::BN) ||
-        !make_cache_map(&tmV, a.v_cache, U, a.max_seq_len, DecodeCfg::BN))
+    const Variant v = pick(a.kv, a.fused);
+    const bool quant = a.kv != SR_KV_BF16;
+    if (!make_cache_map(&tmK, a.k_cache, U, a.max_seq_len, v.rows, quant) ||
+        !make_cache_map(&tmV, a.v_cache, U, a.max_seq_len, v.rows, quant))
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     Params p;
@@ -1377,20 +1664,18 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream)
     p.active_out = a.active_out;
     p.lse = a.lse;
     p.out_f32 = a.out_f32;
+    p.scales = reinterpret_cast<const float2 *>(a.scales);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(info->grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = DecodeCfg::ALLOC;
+    cfg.blockDim = dim3((unsigned)v.threads);
+    cfg.dynamicSmemBytes = (size_t)v.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.fused)
-        e = cudaLaunchKernelEx(&cfg, decode_kernel<SR_DECODE_RB, SR_DECODE_STAGES, true>, tmK, tmV, p);
-    else
-        e = cudaLaunchKernelEx(&cfg, decode_kernel<SR_DECODE_RB, SR_DECODE_STAGES, false>, tmK, tmV, p);
+    e = cudaLaunchKernelEx(&cfg, v.fn, tmK, tmV, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -70,19 +70,61 @@ struct DecodeArgs {
     // Partial outputs for context parallelism (sr_decode_attention_partial):
     // fp32 output instead of `out`.
     float *out_f32 = nullptr;
+    // Cache type (SR_KV_*) and, for the 8-bit ones, the scale pairs.
+    int kv = SR_KV_BF16;
+    const float *scales = nullptr;
 };
 
-// RoPE + append + position-0 capture + routing (sr_rope_append_route).
+// RoPE + append + position-0 capture + routing (sr_rope_append_route,
+// sr_rope_append_route_kv).
 struct PrestepArgs {
     const void *q_in, *k_new, *v_new;
     const float *rope_cos, *rope_sin;
-    int32_t *seq_lens;
+    const int32_t *seq_lens;
+    int32_t *seq_lens_out;
     void *k_cache, *v_cache, *k0, *v0, *q_out;
     uint8_t *mask;
     int32_t *active;
     int32_t *error;
     float tau;
     int batch, n_q_heads, n_kv_heads, max_seq_len, max_pos;
+    int kv = SR_KV_BF16;
+    float *scales = nullptr; // 8-bit caches only
+    int pos_offset = 0;      // position of a sequence's slot 0
+};
+
+// Rows written into an 8-bit cache (sr_kv_append_quant) and read out of one
+// (sr_kv_dequant).
+struct KvWriteArgs {
+    const void *k_new, *v_new;
+    sr_row_strides ks, vs;
+    const int32_t *start, *n;
+    void *k_cache, *v_cache;
+    float *scales;
+    void *k0, *v0;
+    int32_t *error;
+    int kv, batch, n_kv_heads, max_seq_len, n_tokens;
+};
+struct KvReadArgs {
+    const void *k_cache, *v_cache;
+    const float *scales;
+    const int32_t *start, *n;
+    void *k_out, *v_out;
+    int32_t *error;
+    int kv, batch, n_kv_heads, max_seq_len, n_rows;
+};
+
+// Attention of every active query row over one prefix that the whole batch
+// shares (sr_prefix_attention, sr_prefix_attention_partial).
+struct PrefixArgs {
+    const void *q, *k_prefix, *v_prefix, *v0;
+    const uint8_t *mask;
+    const float *o_suffix, *lse_suffix; // joined when given
+    void *out;                          // bf16 result, or
+    float *out_f32;                     // the partial one
+    float *lse;
+    void *workspace;
+    int batch, n_q_heads, n_kv_heads, max_seq_len, prefix_len;
 };
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream);
@@ -97,6 +139,11 @@ cudaError_t launch_position0(int B, int Hq, int Hkv, int Lmax, const void *q, co
 cudaError_t launch_combine(int n_heads, int n_parts, const float *o_parts, const float *lse_parts, int64_t part_stride,
                            void *out, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_write(const KvWriteArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream);
+// Workspace of the prefix attention (0: no device).
+size_t prefix_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 // Persistent CTAs of the decode kernel on the current device (0 on error).
 int decode_grid_size();
 // Records a CUDA failure for sr_last_cuda_error and returns SR_ERR_CUDA.

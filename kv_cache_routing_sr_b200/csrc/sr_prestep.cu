@@ -21,7 +21,12 @@
 // exponent, makes the double rounding innocuous; fp32 has sixteen more than
 // bf16). The result is the correctly rounded bf16 of the fp64 rotation.
 //
-// Layout: one CTA of 512 threads walking the units in chunks whose rows fit in
+// The same step writes the 8-bit cache (sr_quant.cuh): the new key is the
+// correctly rounded bf16 rotation first and is quantised from that, by the
+// eight lanes that hold it, so the position-0 key is the bf16 row in either case.
+//
+// Layout: one CTA of 512 threads, or a cluster of eight with a share of the
+// units each, walking its units in chunks whose rows fit in
 // shared memory. Per chunk, in one pass where each thread takes its own item:
 // eight threads per new key rotate it (each takes 8 elements and their 8
 // partners), write the cache slot, and stage the group's position-0 key (the
@@ -31,12 +36,15 @@
 // (q_out, k0) bit for bit. Lengths advance after every read of
 // them; the compaction is the routing kernel's.
 #include <atomic>
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "sinkrouter.h"
 #include "sr_internal.h"
 #include "sr_ptx.cuh"
+#include "sr_quant.cuh"
 #include "sr_route_math.cuh"
 
 namespace sr {
@@ -45,19 +53,24 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowBudget = 160 * 1024; // shared bytes for staged q / k0 rows
+constexpr int kClusterCtas = 8;
+constexpr int kOneCtaUnits = 16; // launches of at most this many units use one CTA
 
 template <int M> __host__ __device__ constexpr int chunk_units() { return kRowBudget / ((M + 1) * 256); }
 
 struct PrestepParams {
     const __nv_bfloat16 *q_in, *k_new, *v_new;
     const float *rope_cos, *rope_sin;
-    int32_t *seq_lens;
-    __nv_bfloat16 *k_cache, *v_cache, *k0, *v0, *q_out;
+    const int32_t *seq_lens;
+    int32_t *seq_lens_out;           // may be seq_lens
+    uint8_t *k_cache, *v_cache;      // rows of 256 (bf16) or 128 bytes
+    float2 *scales;                  // 8-bit caches only
+    __nv_bfloat16 *k0, *v0, *q_out;
     uint8_t *mask;
     int32_t *active;
     int32_t *error;
     float tau;
-    int B, Hkv, Lmax, max_pos;
+    int B, Hkv, Lmax, max_pos, pos_offset;
 };
 
 // Correctly rounded fp64 -> bf16 (nearest, ties to even) through round-to-odd
@@ -103,12 +116,40 @@ __device__ __forceinline__ void rope8(uint4 x_lo, uint4 x_hi, const float4 (&c)[
     o_hi = make_uint4(oh[0], oh[1], oh[2], oh[3]);
 }
 
-// Slot of sequence b, or -1 when it is outside [0, min(Lmax, max_pos)). Plain
-// loads: this kernel writes seq_lens at the end.
+// Slot of sequence b, or -1 when it is outside [0, min(Lmax, max_pos -
+// pos_offset)). Plain loads: this kernel may write seq_lens at the end.
 __device__ __forceinline__ int slot_of(const PrestepParams &p, int b)
 {
-    const int pos = p.seq_lens[b];
-    return (pos >= 0 && pos < p.Lmax && pos < p.max_pos) ? pos : -1;
+    const int slot = p.seq_lens[b];
+    return (slot >= 0 && slot < p.Lmax && (long long)slot + p.pos_offset < p.max_pos) ? slot : -1;
+}
+
+// Writes elements 8j .. 8j+7 (lo) and 64+8j .. 64+8j+7 (hi) of a cache row. For
+// an 8-bit cache the eight lanes that hold the row agree on its scale, which is
+// returned.
+template <int KV> __device__ __forceinline__ float store_row(uint8_t *cache, size_t row, int j, uint4 lo, uint4 hi)
+{
+    if constexpr (KV == SR_KV_BF16) {
+        uint4 *d = reinterpret_cast<uint4 *>(cache + row * (kHeadDim * 2));
+        d[j] = lo;
+        d[j + 8] = hi;
+        return 0.f;
+    } else {
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint32_t m = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            m = abs_max_bf16x2(m, w[e]);
+        const unsigned lanes = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            m = __vmaxu2(m, __shfl_xor_sync(lanes, m, o));
+        const RowQuant r = row_quant<KV>(max(m & 0xffffu, m >> 16));
+        uint2 *d = reinterpret_cast<uint2 *>(cache + row * kHeadDim);
+        d[j] = make_uint2(quant4<KV>(w[0], w[1], r), quant4<KV>(w[2], w[3], r));
+        d[j + 8] = make_uint2(quant4<KV>(w[4], w[5], r), quant4<KV>(w[6], w[7], r));
+        return r.scale;
+    }
 }
 
 __device__ __forceinline__ void load_table8(const float *tab, int pos, int j, float4 (&v)[2])
@@ -118,7 +159,7 @@ __device__ __forceinline__ void load_table8(const float *tab, int pos, int j, fl
     v[1] = __ldg(t + 1);
 }
 
-template <int M>
+template <int M, int KV, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepParams p, int cu)
 {
     extern __shared__ __align__(128) uint8_t dsm[]; // [cu*(M+1)*256 staged rows][B*Hkv sink flags]
@@ -126,8 +167,17 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     __shared__ int32_t warp_off[kWarps + 1];
 
     const int U = p.B * p.Hkv;
+    // This CTA's units [ub, ue): all of them, or its share of the cluster's.
+    const int per = CLUSTER ? (U + kClusterCtas - 1) / kClusterCtas : U;
+    const int ub = CLUSTER ? min((int)blockIdx.x * per, U) : 0;
+    const int ue = CLUSTER ? min(ub + per, U) : U;
     uint4 *rows = reinterpret_cast<uint4 *>(dsm);
     uint8_t *sink_flag = dsm + (size_t)cu * (M + 1) * 256;
+    uint8_t *all_flags = sink_flag; // CTA 0's, which compacts the active list
+    if constexpr (CLUSTER) {
+        all_flags = cooperative_groups::this_cluster().map_shared_rank(sink_flag, 0);
+        cooperative_groups::this_cluster().sync(); // CTA 0 runs: its shared memory may be written
+    }
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
     // Every input may come from the preceding kernel, and the previous decode
@@ -152,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
         uint4 lo = zero, hi = zero;
         if (pos >= 0) {
             float4 c[2], s[2];
-            load_table8(p.rope_cos, pos, j, c);
-            load_table8(p.rope_sin, pos, j, s);
+            load_table8(p.rope_cos, pos + p.pos_offset, j, c);
+            load_table8(p.rope_sin, pos + p.pos_offset, j, s);
             rope8(qlo, qhi, c, s, lo, hi);
         }
         qs[j] = lo;
@@ -163,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     };
 
     bool bad_slot = false;
-    for (int u0 = 0; u0 < U; u0 += cu) {
-        const int nu = (U - u0) < cu ? (U - u0) : cu;
+    for (int u0 = ub; u0 < ue; u0 += cu) {
+        const int nu = (ue - u0) < cu ? (ue - u0) : cu;
         uint4 *krows = rows + (size_t)nu * M * 16;
         // One pass over the chunk's items, each thread on its own item (at the
         // 8B shape every item has a thread), so that no thread takes a key and
@@ -194,18 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
                 continue;
             }
             float4 c[2], s[2];
-            load_table8(p.rope_cos, pos, j, c);
-            load_table8(p.rope_sin, pos, j, s);
+            load_table8(p.rope_cos, pos + p.pos_offset, j, c);
+            load_table8(p.rope_sin, pos + p.pos_offset, j, s);
             uint4 lo, hi;
             rope8(klo, khi, c, s, lo, hi);
-            const size_t slot = ((size_t)u * p.Lmax + pos) * kHeadDim;
-            uint4 *kd = reinterpret_cast<uint4 *>(p.k_cache + slot);
-            uint4 *vd = reinterpret_cast<uint4 *>(p.v_cache + slot);
-            kd[j] = lo;
-            kd[j + 8] = hi;
-            vd[j] = vlo;
-            vd[j + 8] = vhi;
-            if (pos == 0) {
+            const size_t slot = (size_t)u * p.Lmax + pos;
+            const float sk = store_row<KV>(p.k_cache, slot, j, lo, hi);
+            const float sv = store_row<KV>(p.v_cache, slot, j, vlo, vhi);
+            if (KV != SR_KV_BF16 && j == 0)
+                p.scales[slot] = make_float2(sk, sv);
+            if (pos + p.pos_offset == 0) {
                 uint4 *v0g = reinterpret_cast<uint4 *>(p.v0 + (size_t)u * kHeadDim);
                 k0g[j] = lo;
                 k0g[j + 8] = hi;
@@ -220,40 +268,44 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
         }
         __syncthreads();
         route_units_warp<M, false>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
-            sink_flag[u0 + lu] = sink ? 1 : 0;
+            all_flags[u0 + lu] = sink ? 1 : 0;
             p.mask[u0 + lu] = sink ? 1 : 0;
         });
         __syncthreads(); // the rows are overwritten by the next chunk
     }
 
-    // Every read of seq_lens is behind the barriers above.
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int pos = slot_of(p, b);
-        if (pos >= 0)
-            p.seq_lens[b] = pos + 1;
-    }
     if (p.error && __syncthreads_or(bad_slot) && threadIdx.x == 0)
         atomicOr(p.error, SR_DEVERR_APPEND_SLOT);
+    if constexpr (CLUSTER) {
+        cooperative_groups::this_cluster().sync();
+        if (blockIdx.x != 0)
+            return;
+    }
+    // Every other read of seq_lens, and every flag, is behind the barriers above.
+    for (int b = threadIdx.x; b < p.B; b += kThreads)
+        p.seq_lens_out[b] = p.seq_lens[b] + (slot_of(p, b) >= 0 ? 1 : 0);
     compact_active<kThreads>(sink_flag, U, p.active, warp_cnt, warp_off);
 }
 
-template <int M>
+template <int M, int KV, bool CLUSTER>
 cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
 {
     const int U = a.batch * a.n_kv_heads;
-    const int cu = U < chunk_units<M>() ? U : chunk_units<M>();
+    const int per = CLUSTER ? (U + kClusterCtas - 1) / kClusterCtas : U;
+    const int cu = per < chunk_units<M>() ? per : chunk_units<M>();
     const size_t smem = (size_t)cu * (M + 1) * 256 + (size_t)U;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    if (dev >= 0 && dev < 64 && !configured[dev].load()) {
-        e = cudaFuncSetAttribute(rope_append_route_kernel<M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+        e = cudaFuncSetAttribute(rope_append_route_kernel<M, KV, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)((size_t)chunk_units<M>() * (M + 1) * 256 + SR_MAX_UNITS));
         if (e != cudaSuccess)
             return e;
-        configured[dev].store(true);
+        if (dev >= 0 && dev < 64)
+            configured[dev].store(true);
     }
     PrestepParams p;
     p.q_in = static_cast<const __nv_bfloat16 *>(a.q_in);
@@ -262,8 +314,10 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     p.rope_cos = a.rope_cos;
     p.rope_sin = a.rope_sin;
     p.seq_lens = a.seq_lens;
-    p.k_cache = static_cast<__nv_bfloat16 *>(a.k_cache);
-    p.v_cache = static_cast<__nv_bfloat16 *>(a.v_cache);
+    p.seq_lens_out = a.seq_lens_out;
+    p.k_cache = static_cast<uint8_t *>(a.k_cache);
+    p.v_cache = static_cast<uint8_t *>(a.v_cache);
+    p.scales = reinterpret_cast<float2 *>(a.scales);
     p.k0 = static_cast<__nv_bfloat16 *>(a.k0);
     p.v0 = static_cast<__nv_bfloat16 *>(a.v0);
     p.q_out = static_cast<__nv_bfloat16 *>(a.q_out);
@@ -275,18 +329,40 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     p.Hkv = a.n_kv_heads;
     p.Lmax = a.max_seq_len;
     p.max_pos = a.max_pos;
+    p.pos_offset = a.pos_offset;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
+    cfg.gridDim = dim3(CLUSTER ? kClusterCtas : 1);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kClusterCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M>, p, cu);
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M, KV, CLUSTER>, p, cu);
+}
+
+template <int M, int KV> cudaError_t launch_kv(const PrestepArgs &a, cudaStream_t stream)
+{
+    return a.batch * a.n_kv_heads > kOneCtaUnits ? launch_m<M, KV, true>(a, stream) : launch_m<M, KV, false>(a, stream);
+}
+
+template <int M> cudaError_t launch_group(const PrestepArgs &a, cudaStream_t stream)
+{
+    switch (a.kv) {
+    case SR_KV_BF16:
+        return launch_kv<M, SR_KV_BF16>(a, stream);
+    case SR_KV_E4M3:
+        return launch_kv<M, SR_KV_E4M3>(a, stream);
+    default:
+        return launch_kv<M, SR_KV_INT8>(a, stream);
+    }
 }
 
 } // namespace
@@ -296,16 +372,16 @@ cudaError_t launch_rope_append_route(const PrestepArgs &a, cudaStream_t stream)
     cudaError_t e;
     switch (a.n_q_heads / a.n_kv_heads) {
     case 1:
-        e = launch_m<1>(a, stream);
+        e = launch_group<1>(a, stream);
         break;
     case 2:
-        e = launch_m<2>(a, stream);
+        e = launch_group<2>(a, stream);
         break;
     case 4:
-        e = launch_m<4>(a, stream);
+        e = launch_group<4>(a, stream);
         break;
     case 8:
-        e = launch_m<8>(a, stream);
+        e = launch_group<8>(a, stream);
         break;
     default:
         return cudaErrorInvalidValue;

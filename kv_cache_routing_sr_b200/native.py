@@ -18,6 +18,8 @@ LIBRARY = _build.LIBRARY
 
 SR_OK, SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_WORKSPACE, SR_ERR_CUDA = range(5)
 SR_DEVERR_SEQ_LEN, SR_DEVERR_ACTIVE_LIST, SR_DEVERR_TIMEOUT = 1, 2, 4
+SR_DEVERR_APPEND_SLOT, SR_DEVERR_ROW_COUNT = 8, 16
+SR_KV_BF16, SR_KV_E4M3, SR_KV_INT8 = range(3)
 SR_MAX_UNITS = 16384
 SR_MAX_SPLITS = 4096
 HEAD_DIM = 128
@@ -26,6 +28,14 @@ HEAD_DIM = 128
 class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("max_seq_len", ctypes.c_int32)]
+
+
+class RowStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+# What a cache tensor of each dtype is to the library.
+KV_TYPES = {torch.bfloat16: SR_KV_BF16, torch.float8_e4m3fn: SR_KV_E4M3, torch.int8: SR_KV_INT8}
 
 
 class SinkRouterError(RuntimeError):
@@ -43,7 +53,10 @@ EXPORTS = ["sr_route", "sr_decode_workspace_bytes", "sr_workspace_init", "sr_dec
            "sr_status_string", "sr_get_device_error", "sr_clear_device_error", "sr_decode_grid_size",
            "sr_last_cuda_error", "sr_decode_attention_static_scratch", "sr_route_decode_attention",
            "sr_decode_attention_lse", "sr_rope_append_route", "sr_decode_attention_partial",
-           "sr_combine_partials", "sr_selftest_bounded_wait", "sr_position0_weight"]
+           "sr_combine_partials", "sr_selftest_bounded_wait", "sr_position0_weight", "sr_kv_append_quant",
+           "sr_kv_dequant", "sr_rope_append_route_kv", "sr_decode_attention_quant",
+           "sr_decode_attention_quant_partial", "sr_prefix_attention", "sr_prefix_attention_partial",
+           "sr_prefix_workspace_bytes"]
 
 
 def load(path: str | None = None):
@@ -105,6 +118,24 @@ def load(path: str | None = None):
     lib.sr_combine_partials.restype = ctypes.c_int
     lib.sr_selftest_bounded_wait.argtypes = [i32, vp, vp, vp]
     lib.sr_selftest_bounded_wait.restype = ctypes.c_int
+    sp = ctypes.POINTER(RowStrides)
+    lib.sr_kv_append_quant.argtypes = [dp, i32, i32, vp, sp, vp, sp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sr_kv_append_quant.restype = ctypes.c_int
+    lib.sr_kv_dequant.argtypes = [dp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sr_kv_dequant.restype = ctypes.c_int
+    lib.sr_rope_append_route_kv.argtypes = [dp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                            ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.sr_rope_append_route_kv.restype = ctypes.c_int
+    lib.sr_decode_attention_quant.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, u64, vp]
+    lib.sr_decode_attention_quant.restype = ctypes.c_int
+    lib.sr_decode_attention_quant_partial.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, u64, vp]
+    lib.sr_decode_attention_quant_partial.restype = ctypes.c_int
+    lib.sr_prefix_workspace_bytes.argtypes = [dp]
+    lib.sr_prefix_workspace_bytes.restype = u64
+    lib.sr_prefix_attention.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
+    lib.sr_prefix_attention.restype = ctypes.c_int
+    lib.sr_prefix_attention_partial.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
+    lib.sr_prefix_attention_partial.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -140,6 +171,36 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     return t.data_ptr()
 
 
+def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype) -> int | None:
+    return None if t is None else _dev(t, name, dtype)
+
+
+def _shape(t: torch.Tensor, name: str, shape, device) -> None:
+    """The library sees pointers only: a tensor of another size or device would
+    be read out of bounds."""
+    if t is not None and (t.shape != shape or t.device != device):
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+
+
+def _kv_type(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales, quant_only: bool = True) -> int:
+    """sr_kv_type of a cache [B, Hkv, Lmax, 128] after checking its parts against each other."""
+    kv = KV_TYPES.get(k_cache.dtype)
+    if kv is None or (quant_only and kv == SR_KV_BF16):
+        raise ValueError(f"k_cache must be float8_e4m3fn or int8{'' if quant_only else ' or bfloat16'}, "
+                         f"got {k_cache.dtype}")
+    if k_cache.dim() != 4 or k_cache.shape[3] != HEAD_DIM:
+        raise ValueError(f"k_cache must be [B, Hkv, Lmax, {HEAD_DIM}], got {tuple(k_cache.shape)}")
+    _shape(v_cache, "v_cache", k_cache.shape, k_cache.device)
+    if kv == SR_KV_BF16:
+        if kv_scales is not None:
+            raise ValueError("a bfloat16 cache has no kv_scales")
+    elif kv_scales is None:
+        raise ValueError("an 8-bit cache needs kv_scales")
+    else:
+        _shape(kv_scales, "kv_scales", (*k_cache.shape[:3], 2), k_cache.device)
+    return kv
+
+
 def dims_of(batch: int, n_q_heads: int, n_kv_heads: int, max_seq_len: int, head_dim: int = HEAD_DIM) -> Dims:
     return Dims(batch, n_q_heads, n_kv_heads, head_dim, max_seq_len)
 
@@ -157,7 +218,10 @@ class Workspace:
     usable from any stream once constructed."""
 
     def __init__(self, batch, n_q_heads, n_kv_heads, max_seq_len, max_splits: int = 0, device=None):
-        self.nbytes = workspace_bytes(batch, n_q_heads, n_kv_heads, max_seq_len, max_splits)
+        self._allocate(workspace_bytes(batch, n_q_heads, n_kv_heads, max_seq_len, max_splits), device)
+
+    def _allocate(self, nbytes: int, device):
+        self.nbytes = nbytes
         self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buffer.data_ptr()) % 256
         self.view = self.buffer[off:off + self.nbytes]
@@ -366,6 +430,265 @@ def rope_append_route(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache,
     return q_out, route_mask, active_list
 
 
+class QuantCache:
+    """An empty 8-bit KV cache in torch-allocated device memory: k and v
+    [B, Hkv, Lmax, 128] of dtype float8_e4m3fn or int8, and scales fp32
+    [B, Hkv, Lmax, 2] (key, value)."""
+
+    def __init__(self, batch, n_kv_heads, max_seq_len, dtype=torch.float8_e4m3fn, device="cuda"):
+        if dtype not in (torch.float8_e4m3fn, torch.int8):
+            raise ValueError(f"an 8-bit cache is float8_e4m3fn or int8, got {dtype}")
+        shape = (batch, n_kv_heads, max_seq_len, HEAD_DIM)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype)
+        self.scales = torch.zeros((*shape[:3], 2), dtype=torch.float32, device=device)
+
+
+def _row_strides(t: torch.Tensor, name: str, shape, device) -> RowStrides:
+    """Strides of a bf16 [B, T, Hkv, 128] tensor, which may be a view."""
+    _shape(t, name, shape, device)
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor with a contiguous last dimension")
+    # the stride of a dimension of one entry is never used
+    return RowStrides(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+
+
+@_on_tensor_device
+def kv_append_quant(k_new, v_new, start, n_new, k_cache, v_cache, kv_scales, k0=None, v0=None, device_error=None,
+                    stream=None):
+    """sr_kv_append_quant: quantise tokens t < n_new[b] of k_new / v_new (bf16
+    [B, T, Hkv, 128], views allowed) into slots start[b] + t of the 8-bit cache.
+    k0 / v0 (both or neither) receive the bf16 rows that land in slot 0. Updates
+    k_cache, v_cache, kv_scales, k0 and v0 in place and returns the first three."""
+    kv = _kv_type(k_cache, v_cache, kv_scales)
+    B, Hkv, Lmax, d = k_cache.shape
+    dev = k_cache.device
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B, T, Hkv, 128]")
+    T = k_new.shape[1]
+    if T < 1:
+        return k_cache, v_cache, kv_scales
+    ks, vs = (_row_strides(t, n, (B, T, Hkv, d), dev) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    _shape(start, "start", (B,), dev)
+    _shape(n_new, "n_new", (B,), dev)
+    _shape(k0, "k0", (B, Hkv, d), dev)
+    _shape(v0, "v0", (B, Hkv, d), dev)
+    dims = dims_of(B, Hkv, Hkv, Lmax, d)
+    st = load().sr_kv_append_quant(
+        ctypes.byref(dims), kv, T, k_new.data_ptr(), ctypes.byref(ks), v_new.data_ptr(), ctypes.byref(vs),
+        _dev(start, "start", torch.int32), _dev(n_new, "n_new", torch.int32), _dev(k_cache, "k_cache", k_cache.dtype),
+        _dev(v_cache, "v_cache", k_cache.dtype), _dev(kv_scales, "kv_scales", torch.float32),
+        _opt(k0, "k0", torch.bfloat16), _opt(v0, "v0", torch.bfloat16),
+        _opt(device_error, "device_error", torch.int32), _stream(stream))
+    _check("sr_kv_append_quant", st)
+    return k_cache, v_cache, kv_scales
+
+
+@_on_tensor_device
+def kv_dequant(k_cache, v_cache, kv_scales, start, n, k_out, v_out, device_error=None, stream=None):
+    """sr_kv_dequant: positions start[b] .. start[b] + n[b] - 1 of the 8-bit cache
+    as bf16 rows 0 .. n[b] - 1 of k_out / v_out [B, Hkv, T, 128]; the other rows
+    stay. Returns (k_out, v_out)."""
+    kv = _kv_type(k_cache, v_cache, kv_scales)
+    B, Hkv, Lmax, d = k_cache.shape
+    dev = k_cache.device
+    if k_out.dim() != 4:
+        raise ValueError("k_out must be [B, Hkv, T, 128]")
+    T = k_out.shape[2]
+    _shape(k_out, "k_out", (B, Hkv, T, d), dev)
+    _shape(v_out, "v_out", (B, Hkv, T, d), dev)
+    _shape(start, "start", (B,), dev)
+    _shape(n, "n", (B,), dev)
+    if T < 1:
+        return k_out, v_out
+    dims = dims_of(B, Hkv, Hkv, Lmax, d)
+    st = load().sr_kv_dequant(
+        ctypes.byref(dims), kv, T, _dev(k_cache, "k_cache", k_cache.dtype), _dev(v_cache, "v_cache", k_cache.dtype),
+        _dev(kv_scales, "kv_scales", torch.float32), _dev(start, "start", torch.int32), _dev(n, "n", torch.int32),
+        _dev(k_out, "k_out", torch.bfloat16), _dev(v_out, "v_out", torch.bfloat16),
+        _opt(device_error, "device_error", torch.int32), _stream(stream))
+    _check("sr_kv_dequant", st)
+    return k_out, v_out
+
+
+@_on_tensor_device
+def rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache, v_cache, kv_scales, k0, v0, tau,
+                         pos_offset: int = 0, seq_lens_out=None, q_out=None, route_mask=None, active_list=None,
+                         device_error=None, stream=None):
+    """sr_rope_append_route_kv: rope_append_route for a bf16 or 8-bit cache
+    (kv_scales None for bf16) whose slot 0 holds position pos_offset. seq_lens
+    advances in place, or into seq_lens_out when that is given. Returns (q_out,
+    route_mask, active_list); q_out may be q_in."""
+    kv = _kv_type(k_cache, v_cache, kv_scales, quant_only=False)
+    B, Hkv, Lmax, d = k_cache.shape
+    dev = k_cache.device
+    Hq = q_in.shape[1]
+    if q_out is None:
+        q_out = torch.empty_like(q_in)
+    if route_mask is None:
+        route_mask = torch.empty(B * Hkv, dtype=torch.uint8, device=dev)
+    if active_list is None:
+        active_list = torch.empty(1 + B * Hkv, dtype=torch.int32, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    if rope_cos.shape != rope_sin.shape or rope_cos.dim() != 2 or rope_cos.shape[1] != d // 2:
+        raise ValueError("rope_cos / rope_sin must both be [max_pos, head_dim / 2]")
+    for t, name, shape in ((q_in, "q_in", (B, Hq, d)), (q_out, "q_out", (B, Hq, d)), (k_new, "k_new", (B, Hkv, d)),
+                           (v_new, "v_new", (B, Hkv, d)), (k0, "k0", (B, Hkv, d)), (v0, "v0", (B, Hkv, d)),
+                           (seq_lens, "seq_lens", (B,)), (seq_lens_out, "seq_lens_out", (B,)),
+                           (route_mask, "route_mask", (B * Hkv,)), (active_list, "active_list", (1 + B * Hkv,))):
+        _shape(t, name, shape, dev)
+    dims = dims_of(B, Hq, Hkv, Lmax, d)
+    st = load().sr_rope_append_route_kv(
+        ctypes.byref(dims), kv, int(pos_offset), _dev(q_in, "q_in", torch.bfloat16),
+        _dev(k_new, "k_new", torch.bfloat16), _dev(v_new, "v_new", torch.bfloat16),
+        _dev(rope_cos, "rope_cos", torch.float32), _dev(rope_sin, "rope_sin", torch.float32), int(rope_cos.shape[0]),
+        _dev(seq_lens, "seq_lens", torch.int32), _dev(seq_lens_out, "seq_lens_out", torch.int32),
+        _dev(k_cache, "k_cache", k_cache.dtype), _dev(v_cache, "v_cache", k_cache.dtype),
+        _opt(kv_scales, "kv_scales", torch.float32), _dev(k0, "k0", torch.bfloat16), _dev(v0, "v0", torch.bfloat16),
+        float(tau), _dev(q_out, "q_out", torch.bfloat16), _dev(route_mask, "route_mask", torch.uint8),
+        _dev(active_list, "active_list", torch.int32), _opt(device_error, "device_error", torch.int32),
+        _stream(stream))
+    _check("sr_rope_append_route_kv", st)
+    return q_out, route_mask, active_list
+
+
+def _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits):
+    """Checked arguments that both forms of the 8-bit scan share, and their dims."""
+    kv = _kv_type(k_cache, v_cache, kv_scales)
+    B, Hkv, Lmax, d = k_cache.shape
+    dev = k_cache.device
+    Hq = q.shape[1]
+    _shape(q, "q", (B, Hq, d), dev)
+    _shape(v0, "v0", (B, Hkv, d), dev)
+    _shape(seq_lens, "seq_lens", (B,), dev)
+    _shape(active_list, "active_list", (1 + B * Hkv,), dev)
+    dims = dims_of(B, Hq, Hkv, Lmax, d)
+    return dims, (ctypes.byref(dims), kv, _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", k_cache.dtype),
+                  _dev(v_cache, "v_cache", k_cache.dtype), _dev(kv_scales, "kv_scales", torch.float32),
+                  _dev(v0, "v0", torch.bfloat16), _dev(seq_lens, "seq_lens", torch.int32),
+                  _dev(active_list, "active_list", torch.int32), int(n_splits))
+
+
+@_on_tensor_device
+def decode_attention_quant(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, out=None, n_splits: int = 0,
+                           workspace: Workspace | None = None, stream=None, lse=None):
+    """sr_decode_attention_quant: decode_attention over an 8-bit cache. Returns
+    out bf16 [B, Hq, 128]; ``lse`` (fp32 [B, Hq]) receives the per-head
+    log-sum-exp (NaN for sink heads)."""
+    dims, args = _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits)
+    if out is None:
+        out = torch.empty_like(q)
+    _shape(out, "out", q.shape, q.device)
+    _shape(lse, "lse", q.shape[:2], q.device)
+    if workspace is None:
+        workspace = Workspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, n_splits, device=q.device)
+    _check("sr_decode_attention_quant",
+           load().sr_decode_attention_quant(*args, _dev(out, "out", torch.bfloat16), _opt(lse, "lse", torch.float32),
+                                            ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    return out
+
+
+@_on_tensor_device
+def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, o_part=None,
+                                   lse_part=None, n_splits: int = 0, workspace: Workspace | None = None, stream=None):
+    """sr_decode_attention_quant_partial: decode_attention_partial over an 8-bit
+    cache. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
+    dims, args = _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits)
+    if o_part is None:
+        o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if lse_part is None:
+        lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    _shape(o_part, "o_part", q.shape, q.device)
+    _shape(lse_part, "lse_part", q.shape[:2], q.device)
+    if workspace is None:
+        workspace = Workspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, n_splits, device=q.device)
+    _check("sr_decode_attention_quant_partial",
+           load().sr_decode_attention_quant_partial(*args, _dev(o_part, "o_part", torch.float32),
+                                                    _dev(lse_part, "lse_part", torch.float32),
+                                                    ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    return o_part, lse_part
+
+
+def prefix_workspace_bytes(batch, n_q_heads, n_kv_heads, max_prefix_len) -> int:
+    d = dims_of(batch, n_q_heads, n_kv_heads, max_prefix_len)
+    n = load().sr_prefix_workspace_bytes(ctypes.byref(d))
+    if n == 0:
+        raise ValueError("unsupported dims for the prefix workspace")
+    return int(n)
+
+
+class PrefixWorkspace(Workspace):
+    """A zero-initialised workspace of the prefix attention in torch-allocated
+    device memory, usable from any stream once constructed."""
+
+    def __init__(self, batch, n_q_heads, n_kv_heads, max_prefix_len, device=None):
+        self._allocate(prefix_workspace_bytes(batch, n_q_heads, n_kv_heads, max_prefix_len), device)
+
+
+def _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask):
+    """Checked arguments that both forms of the prefix attention share, and their dims."""
+    if k_prefix.dim() != 3 or k_prefix.shape[2] != HEAD_DIM or q.dim() != 3:
+        raise ValueError("q must be [B, Hq, 128] and k_prefix [Hkv, max_prefix_len, 128]")
+    Hkv, Lmax, d = k_prefix.shape
+    B, Hq, _ = q.shape
+    dev = q.device
+    _shape(q, "q", (B, Hq, d), dev)
+    _shape(k_prefix, "k_prefix", (Hkv, Lmax, d), dev)
+    _shape(v_prefix, "v_prefix", (Hkv, Lmax, d), dev)
+    _shape(v0, "v0", (B, Hkv, d), dev)
+    _shape(route_mask, "route_mask", (B * Hkv,), dev)
+    dims = dims_of(B, Hq, Hkv, Lmax, d)
+    return dims, (ctypes.byref(dims), int(prefix_len), _dev(q, "q", torch.bfloat16),
+                  _dev(k_prefix, "k_prefix", torch.bfloat16), _dev(v_prefix, "v_prefix", torch.bfloat16),
+                  _dev(v0, "v0", torch.bfloat16), _dev(route_mask, "route_mask", torch.uint8))
+
+
+@_on_tensor_device
+def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out=None, lse=None, o_suffix=None,
+                     lse_suffix=None, workspace: PrefixWorkspace | None = None, stream=None):
+    """sr_prefix_attention: one token of every sequence over the prefix that the
+    batch shares (k_prefix / v_prefix bf16 [Hkv, max_prefix_len, 128], the first
+    prefix_len positions of it), joined with each sequence's suffix when o_suffix
+    and lse_suffix (decode_attention_partial's) are given. Returns out bf16 [B, Hq,
+    128]; ``lse`` (fp32 [B, Hq]) receives the log-sum-exp (NaN for sink heads)."""
+    dims, args = _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask)
+    if out is None:
+        out = torch.empty_like(q)
+    for t, name, shape in ((out, "out", q.shape), (lse, "lse", q.shape[:2]), (o_suffix, "o_suffix", q.shape),
+                           (lse_suffix, "lse_suffix", q.shape[:2])):
+        _shape(t, name, shape, q.device)
+    if workspace is None:
+        workspace = PrefixWorkspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, device=q.device)
+    _check("sr_prefix_attention",
+           load().sr_prefix_attention(*args, _opt(o_suffix, "o_suffix", torch.float32),
+                                      _opt(lse_suffix, "lse_suffix", torch.float32),
+                                      _dev(out, "out", torch.bfloat16), _opt(lse, "lse", torch.float32),
+                                      ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    return out
+
+
+@_on_tensor_device
+def prefix_attention_partial(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, o_part=None, lse_part=None,
+                             workspace: PrefixWorkspace | None = None, stream=None):
+    """sr_prefix_attention_partial: the prefix's part alone, as combine_partials
+    takes it. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
+    dims, args = _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask)
+    if o_part is None:
+        o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if lse_part is None:
+        lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    _shape(o_part, "o_part", q.shape, q.device)
+    _shape(lse_part, "lse_part", q.shape[:2], q.device)
+    if workspace is None:
+        workspace = PrefixWorkspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, device=q.device)
+    _check("sr_prefix_attention_partial",
+           load().sr_prefix_attention_partial(*args, _dev(o_part, "o_part", torch.float32),
+                                              _dev(lse_part, "lse_part", torch.float32),
+                                              ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    return o_part, lse_part
+
+
 def selftest_bounded_wait(limit_us: int, device="cuda", stream=None):
     """sr_selftest_bounded_wait: a wait on an mbarrier nothing arrives on, with
     a bound of limit_us. Returns (status, waited_ns) after synchronising; the
@@ -422,6 +745,33 @@ class Decoder:
         route_decode_attention(q, k_cache, v_cache, k0, v0, seq_lens, tau, self.out, self.route_mask,
                                self.active_list, n_splits, self.workspace, stream)
         return self.out
+
+
+class QuantDecoder(Decoder):
+    """A Decoder over an 8-bit cache: step() = sr_route then
+    sr_decode_attention_quant, append_step() = sr_rope_append_route_kv then
+    sr_decode_attention_quant. The cache (a QuantCache, or tensors like its
+    parts) is the caller's; k0 and v0 stay bf16."""
+
+    def step(self, q, cache: QuantCache, k0, v0, seq_lens, tau, n_splits: int = 0, stream=None):
+        route(q, k0, tau, self.route_mask, self.active_list, stream)
+        return decode_attention_quant(q, cache.k, cache.v, cache.scales, v0, seq_lens, self.active_list, self.out,
+                                      n_splits, self.workspace, stream)
+
+    def append_step(self, q_in, k_new, v_new, rope_cos, rope_sin, cache: QuantCache, k0, v0, seq_lens, tau,
+                    n_splits: int = 0, device_error=None, stream=None):
+        """A whole decode step from the un-rotated projections; the cache, k0 / v0
+        and seq_lens are updated in place, the rotated query is kept in self.q."""
+        if getattr(self, "q", None) is None or self.q.shape != q_in.shape:
+            self.q = torch.empty_like(q_in)
+        rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, cache.k, cache.v, cache.scales, k0, v0,
+                             tau, q_out=self.q, route_mask=self.route_mask, active_list=self.active_list,
+                             device_error=device_error, stream=stream)
+        return decode_attention_quant(self.q, cache.k, cache.v, cache.scales, v0, seq_lens, self.active_list, self.out,
+                                      n_splits, self.workspace, stream)
+
+    def step_fused(self, *args, **kwargs):
+        raise NotImplementedError("the single-launch step exists for bf16 caches only")
 
 
 class StepGraph:

@@ -1,0 +1,148 @@
+"""Host-side refusals of the 8-bit cache and shared-prefix entry points: nothing is
+launched, so these run without a GPU. Also the binding's own checks of shapes."""
+import ctypes
+
+import pytest
+import torch
+
+from kv_cache_routing_sr_b200 import build, native, shared_prefix
+
+FAKE = 0x10000  # aligned, never dereferenced: validation fails before any launch
+INV, UNS, WS = native.SR_ERR_INVALID_ARG, native.SR_ERR_UNSUPPORTED, native.SR_ERR_WORKSPACE
+BAD_DIMS = [(dict(d=64), UNS), (dict(Hq=24), UNS), (dict(B=4097), UNS), (dict(B=0), INV), (dict(Hq=30), INV),
+            (dict(L=0), INV)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if build.needs_build():
+        build.build()
+    return native.load()
+
+
+def dims(B=1, Hq=32, Hkv=8, d=128, L=4096):
+    return native.Dims(B, Hq, Hkv, d, L)
+
+
+def caller(lib, name, order, fixed):
+    """A call of an entry point with any argument replaced by keyword."""
+    def call(dims=dims(), **kw):
+        args = [kw.get(n, fixed.get(n, FAKE)) for n in order]
+        args = [ctypes.c_float(a) if n == "tau" else ctypes.byref(a) if isinstance(a, ctypes.Structure) else a
+                for n, a in zip(order, args)]
+        return getattr(lib, name)(ctypes.byref(dims), *args, None)
+    return call
+
+
+def strides(b=8, t=8, h=8):
+    return native.RowStrides(b, t, h)
+
+
+def refuses(call, cases):
+    for kw, expect in cases:
+        assert call(**kw) == expect, kw
+
+
+def common(call, pointers, aligned16, aligned4, extra=()):
+    refuses(call, [({n: None}, INV) for n in pointers])
+    refuses(call, [({n: FAKE + 8}, INV) for n in aligned16])
+    refuses(call, [({n: FAKE + 2}, INV) for n in aligned4])
+    refuses(call, [(dict(dims=dims(**d)), e) for d, e in BAD_DIMS])
+    refuses(call, extra)
+
+
+def test_kv_append_quant(lib):
+    call = caller(lib, "sr_kv_append_quant",
+                  ["kv", "T", "k", "ks", "v", "vs", "start", "n", "kc", "vc", "sc", "k0", "v0", "err"],
+                  dict(kv=1, T=4, ks=strides(), vs=strides(), err=None))
+    common(call, ["k", "ks", "v", "vs", "start", "n", "kc", "vc", "sc", "k0", "v0"], ["k", "v", "kc", "vc", "sc", "k0", "v0"],
+           ["start", "n", "err"],
+           [(dict(kv=0), INV), (dict(kv=3), INV), (dict(kv=-1), INV), (dict(T=0), INV), (dict(ks=strides(b=4)), INV),
+            (dict(vs=strides(t=12)), INV), (dict(vs=strides(h=-1)), INV)])
+
+
+def test_kv_dequant(lib):
+    call = caller(lib, "sr_kv_dequant", ["kv", "T", "kc", "vc", "sc", "start", "n", "ko", "vo", "err"],
+                  dict(kv=2, T=4, err=None))
+    common(call, ["kc", "vc", "sc", "start", "n", "ko", "vo"], ["kc", "vc", "sc", "ko", "vo"], ["start", "n", "err"],
+           [(dict(kv=0), INV), (dict(kv=7), INV), (dict(T=0), INV), (dict(T=-5), INV)])
+
+
+def test_rope_append_route_kv(lib):
+    rows = ["q", "kn", "vn", "cos", "sin", "kc", "vc", "k0", "v0", "qo"]
+    call = caller(lib, "sr_rope_append_route_kv",
+                  ["kv", "off", "q", "kn", "vn", "cos", "sin", "mp", "sl", "slo", "kc", "vc", "sc", "k0", "v0", "tau", "qo",
+                   "mask", "act", "err"], dict(kv=1, off=0, mp=64, tau=0.6, err=None))
+    common(call, rows + ["sl", "slo", "mask", "act", "sc"], rows + ["sc"], ["sl", "slo", "act", "err"],
+           [(dict(kv=0), INV), (dict(kv=0, sc=None, mp=0), INV), (dict(kv=5), INV), (dict(off=-1), INV), (dict(mp=0), INV),
+            (dict(tau=float("nan")), INV)])
+
+
+@pytest.mark.parametrize("partial", [False, True])
+def test_decode_attention_quant(lib, partial):
+    outs = ["o", "lse"]
+    call = caller(lib, "sr_decode_attention_quant" + ("_partial" if partial else ""),
+                  ["kv", "q", "kc", "vc", "sc", "v0", "sl", "act", "ns", *outs, "ws", "wsb"], dict(kv=1, ns=0, wsb=1 << 30))
+    need = native.workspace_bytes(1, 32, 8, 4096)
+    common(call, ["q", "kc", "vc", "sc", "v0", "sl", "act", "o"] + (["lse"] if partial else []),
+           ["q", "kc", "vc", "sc", "v0", "o"], ["sl", "act", "lse"],
+           [(dict(kv=0), INV), (dict(kv=9), INV), (dict(ns=-1), INV), (dict(ns=native.SR_MAX_SPLITS + 1), INV),
+            (dict(ws=None), WS), (dict(ws=FAKE + 128), WS), (dict(wsb=need - 1), WS)])
+
+
+@pytest.mark.parametrize("partial", [False, True])
+def test_prefix_attention(lib, partial):
+    order = ["Lp", "q", "k", "v", "v0", "mask"] + ([] if partial else ["os", "ls"]) + ["o", "lse", "ws", "wsb"]
+    call = caller(lib, "sr_prefix_attention" + ("_partial" if partial else ""), order, dict(Lp=100, wsb=1 << 40))
+    need = native.prefix_workspace_bytes(1, 32, 8, 4096)
+    assert need % 256 == 0
+    extra = [(dict(Lp=-1), INV), (dict(Lp=4097), INV), (dict(ws=None), WS), (dict(ws=FAKE + 16), WS),
+             (dict(wsb=need - 1), WS)]
+    if partial:
+        extra.append((dict(lse=None), INV))
+    else:  # both parts of the suffix, or none
+        extra += [(dict(os=None), INV), (dict(ls=None), INV), (dict(os=FAKE + 8), INV), (dict(ls=FAKE + 2), INV)]
+    common(call, ["q", "k", "v", "v0", "mask", "o"], ["q", "k", "v", "v0", "o"], ["lse"], extra)
+    for d, _ in BAD_DIMS:
+        assert lib.sr_prefix_workspace_bytes(ctypes.byref(dims(**d))) == 0
+    assert lib.sr_prefix_workspace_bytes(None) == 0
+
+
+def test_binding_refuses_mismatched_tensors():
+    """The library sees pointers: the binding compares every tensor with the cache
+    (CPU tensors here: nothing reaches the library)."""
+    e, i32, f = torch.float8_e4m3fn, torch.int32, torch.float32
+    k = torch.zeros(2, 4, 9, 128, dtype=torch.uint8).view(e)
+    sc = torch.zeros(2, 4, 9, 2)
+    with pytest.raises(ValueError, match="kv_scales"):
+        native._kv_type(k, k, torch.zeros(2, 4, 9))
+    with pytest.raises(ValueError, match="v_cache"):
+        native._kv_type(k, k[:, :, :8], sc)
+    with pytest.raises(ValueError, match="8-bit"):
+        native._kv_type(k, k, None)
+    with pytest.raises(ValueError, match="k_cache"):
+        native._kv_type(k.view(torch.uint8), k, sc)
+    with pytest.raises(ValueError, match="bfloat16"):
+        native._kv_type(torch.zeros(2, 4, 9, 128, dtype=torch.bfloat16), k, sc)
+    with pytest.raises(ValueError, match="kv_scales"):
+        b = torch.zeros(2, 4, 9, 128, dtype=torch.bfloat16)
+        native._kv_type(b, b, sc, quant_only=False)
+    assert native._kv_type(k, k, sc) == native.SR_KV_E4M3
+    assert native._kv_type(k.view(torch.int8), k.view(torch.int8), sc) == native.SR_KV_INT8
+    with pytest.raises(ValueError, match="8-bit"):
+        native.QuantCache(1, 1, 1, torch.float16, device="cpu")
+    x = torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="k_new"):
+        native._row_strides(x[:, :, :2], "k_new", (2, 3, 4, 128), x.device)
+    with pytest.raises(ValueError, match="CUDA"):
+        native._row_strides(x, "k_new", (2, 3, 4, 128), x.device)
+    with pytest.raises(ValueError, match="v0"):
+        native._prefix_args(torch.zeros(2, 8, 128), torch.zeros(4, 9, 128), torch.zeros(4, 9, 128), 3,
+                            torch.zeros(2, 3, 128), torch.zeros(8))
+    with pytest.raises(ValueError, match="route_mask"):
+        native._prefix_args(torch.zeros(2, 8, 128), torch.zeros(4, 9, 128), torch.zeros(4, 9, 128), 3,
+                            torch.zeros(2, 4, 128), torch.zeros(7))
+    with pytest.raises(ValueError, match="active_list"):
+        native._quant_args(torch.zeros(2, 8, 128), k, k, sc, torch.zeros(2, 4, 128), torch.zeros(2, dtype=i32),
+                           torch.zeros(8, dtype=i32), 0)
+    assert f and shared_prefix.SharedPrefixDecoder

@@ -1,0 +1,601 @@
+"""The 8-bit KV cache on the GPU: bulk writes, reads, the single-token append and
+the routed scan, against their definitions in 64 bits (tests/quant_ref.py) and the
+oracle's rotation.
+
+Bars. Codes and scales are bit-exact. Rows read back are the rounding of code *
+scale. The append's query, position-0 rows, mask and lengths are bit-exact with
+the oracle and sr_route. The scan is inside the elementwise bound of its own
+roundings: softmax weights to fp16 (half a step, 2^-11), output to bf16 (2^-8),
+fp32 logits; a weight below 2^-39 of the largest may vanish (fp16's smallest step
+2^-24 under the scaling by 2^14, half of it lost)."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import oracle
+from kv_cache_routing_sr_b200 import inputs, native
+from tests import gpu_helpers as H
+from tests import quant_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TAU = 0.6
+both = pytest.mark.parametrize("dtype", R.DTYPES, ids=R.IDS)
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def rows(shape, seed):
+    """bf16 rows over many magnitudes, with ties, zeros and a row of zeros among them."""
+    x = torch.randn(shape, generator=gen(seed), device=DEV)
+    x = x * torch.exp2(torch.randint(-12, 13, (*shape[:-1], 1), generator=gen(seed + 1), device=DEV).float())
+    x = x.to(torch.bfloat16)
+    flat = x.view(-1, R.D)
+    n = flat.shape[0]
+    flat[0] = 0
+    if n > 1:  # ties of both formats: top and its halves, odd multiples
+        flat[1] = torch.tensor([127.0, 63.5, 0.5, 1.5, -2.5, -63.5, 254.0 / 2, 17.0] * 16, device=DEV).to(torch.bfloat16)
+    if n > 2:
+        flat[2] = torch.tensor([3.0, 1.5, 0.75, -1.5, 2.0, 1.0, -0.5, 0.25] * 16, device=DEV).to(torch.bfloat16)
+    if n > 3:
+        flat[3] = torch.tensor([448.0, 17.0, 19.0, -21.0, 2.0 ** -9, 3 * 2.0 ** -10, 2.0 ** -10, 0.0] * 16,
+                               device=DEV).to(torch.bfloat16)
+    if n > 4:
+        flat[4] = 3e38
+    if n > 5:
+        flat[5] = 1e-38
+    return x
+
+
+def assert_rows(codes, scales, x, dtype, what):
+    want, ws = R.quantise(x, dtype)
+    assert torch.equal(torch.isnan(scales), torch.isnan(ws)), what
+    ok = ~torch.isnan(ws)
+    assert torch.equal(scales[ok], ws[ok]), f"{what}: scales differ"
+    got = codes.double()
+    if not torch.equal(got, want):
+        bad = (got != want).nonzero()
+        i = tuple(bad[0].tolist())
+        raise AssertionError(f"{what}: {bad.shape[0]} codes differ, first at {i}: {got[i]} for {want[i]}, "
+                             f"x {x[i].item()}, scale {scales[i[:-1]].item()}")
+
+
+def sentinel_cache(B, Hkv, Lmax, dtype):
+    c = native.QuantCache(B, Hkv, Lmax, dtype)
+    for t in (c.k, c.v):
+        t.view(torch.uint8).fill_(0x55)
+    c.scales.fill_(-7.0)
+    return c
+
+
+WRITES = [
+    # B, Hkv, T, Lmax, starts, counts
+    (1, 1, 1, 1, [0], [1]),
+    (1, 8, 5, 9, [0], [5]),
+    (2, 5, 7, 33, [0, 26], [7, 7]),
+    (3, 4, 64, 101, [37, 0, 11], [64, 0, 1]),
+    (4, 32, 33, 64, [31, 0, 1, 0], [33, 2, 32, 33]),
+]
+
+
+@both
+@pytest.mark.parametrize("fused", [False, True], ids=["own", "view"])
+@pytest.mark.parametrize("B,Hkv,T,Lmax,start,count", WRITES, ids=[f"B{w[0]}T{w[2]}" for w in WRITES])
+def test_append_quant_writes_exactly_its_rows(B, Hkv, T, Lmax, start, count, fused, dtype):
+    if fused:
+        p = rows((B, T, 3 * Hkv, R.D), 5)
+        k, v = p[:, :, Hkv:2 * Hkv], p[:, :, 2 * Hkv:]
+    else:
+        k, v = rows((B, T, Hkv, R.D), 5), rows((B, T, Hkv, R.D), 6)
+    c = sentinel_cache(B, Hkv, Lmax, dtype)
+    k0 = torch.full((B, Hkv, R.D), 9.0, device=DEV, dtype=torch.bfloat16)
+    v0 = k0.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    st, n = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (start, count))
+    got = native.kv_append_quant(k, v, st, n, c.k, c.v, c.scales, k0, v0, device_error=err)
+    assert got[0] is c.k and int(err) == 0
+    seen = torch.zeros((B, Hkv, Lmax), dtype=torch.bool, device=DEV)
+    for b in range(B):
+        s, e = start[b], start[b] + count[b]
+        seen[b, :, s:e] = True
+        for new, cache, part in ((k, c.k, 0), (v, c.v, 1)):
+            x = new[b, :count[b]].transpose(0, 1)
+            assert_rows(cache[b, :, s:e], c.scales[b, :, s:e, part], x, dtype, f"sequence {b}")
+        first = start[b] == 0 and count[b] > 0
+        assert torch.equal(k0[b], k[b, 0] if first else torch.full_like(k0[b], 9.0))
+        assert torch.equal(v0[b], v[b, 0] if first else torch.full_like(v0[b], 9.0))
+    for t in (c.k, c.v):
+        assert (t.view(torch.uint8)[~seen] == 0x55).all(), "rows behind the chunk changed"
+    assert (c.scales[~seen] == -7.0).all()
+
+
+@both
+def test_append_quant_covers_every_bf16_ratio(dtype):
+    """Every bf16 significand as the row's largest magnitude against every one as
+    an element, over the exponents that reach a code: all ties, both signs."""
+    tops = torch.arange(128, 256, device=DEV).double() / 128
+    elems = torch.arange(128, 256, device=DEV).double() / 128
+    x = torch.zeros(128, 16, 128, device=DEV, dtype=torch.float64)
+    for e in range(16):
+        x[:, e] = elems * 2.0 ** -e * (1 - 2 * (e % 2))
+    x = torch.where(x.abs() > tops[:, None, None], torch.zeros_like(x), x)
+    x[:, :, 0] = tops[:, None]
+    x = x.to(torch.bfloat16).reshape(1, 2048, 1, R.D)
+    c = native.QuantCache(1, 1, 2048, dtype)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    native.kv_append_quant(x, -x, z, z + 2048, c.k, c.v, c.scales)
+    assert_rows(c.k[0, 0], c.scales[0, 0, :, 0], x[0, :, 0], dtype, "keys")
+    assert_rows(c.v[0, 0], c.scales[0, 0, :, 1], -x[0, :, 0], dtype, "values")
+
+
+@both
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_append_quant_non_finite_rows(dtype, bad):
+    x = rows((1, 8, 2, R.D), 3)
+    y = x.clone()
+    y[0, 6, 1, 77] = bad
+    c = native.QuantCache(1, 2, 8, dtype)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    native.kv_append_quant(y, x, z, z + 8, c.k, c.v, c.scales)
+    assert_rows(c.k[0], c.scales[0, :, :, 0], y[0].transpose(0, 1), dtype, "keys")
+    assert_rows(c.v[0], c.scales[0, :, :, 1], x[0].transpose(0, 1), dtype, "values")
+    k, v = (torch.zeros(1, 2, 8, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    native.kv_dequant(c.k, c.v, c.scales, z, z + 8, k, v)
+    assert torch.isnan(k[0, 1, 6]).all() and torch.isfinite(v).all()
+    assert torch.isnan(k).sum() == R.D
+
+
+@both
+def test_append_quant_reports_bad_slots_and_counts(dtype):
+    B, Hkv, T, Lmax = 6, 2, 4, 10
+    k, v = rows((B, T, Hkv, R.D), 1), rows((B, T, Hkv, R.D), 2)
+    c = sentinel_cache(B, Hkv, Lmax, dtype)
+    #        runs off the end  before 0   past    bad counts       far out
+    start = torch.tensor([8, -2, 10, 1, 2, 2147483647], dtype=torch.int32, device=DEV)
+    count = torch.tensor([4, 4, 1, 5, -3, 4], dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    native.kv_append_quant(k, v, start, count, c.k, c.v, c.scales, device_error=err)
+    assert int(err) == native.SR_DEVERR_APPEND_SLOT | native.SR_DEVERR_ROW_COUNT
+    seen = torch.zeros((B, Lmax), dtype=torch.bool)
+    seen[0, 8:10] = seen[1, 0:2] = seen[3, 1:5] = True
+    written = (c.scales[:, 0, :, 0] != -7.0).cpu()
+    assert torch.equal(written, seen)
+    assert_rows(c.k[0, :, 8:], c.scales[0, :, 8:, 0], k[0, :2].transpose(0, 1), dtype, "clipped")
+    assert_rows(c.k[1, :, :2], c.scales[1, :, :2, 0], k[1, 2:].transpose(0, 1), dtype, "clipped")
+
+
+@both
+@pytest.mark.parametrize("B,Hkv,T,Lmax,start,count", WRITES, ids=[f"B{w[0]}T{w[2]}" for w in WRITES])
+def test_dequant_reads_exactly_its_rows(B, Hkv, T, Lmax, start, count, dtype):
+    c = native.QuantCache(B, Hkv, Lmax, dtype)
+    g = gen(4)
+    for t in (c.k, c.v):
+        x = torch.randint(0, 256, t.shape, generator=g, device=DEV, dtype=torch.int32).to(torch.uint8)
+        t.view(torch.uint8).copy_(x)  # every code, e4m3's NaN among them
+    c.scales.copy_(torch.randn(c.scales.shape, generator=g, device=DEV))
+    st, n = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (start, count))
+    k, v = (torch.full((B, Hkv, T, R.D), 5.0, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    native.kv_dequant(c.k, c.v, c.scales, st, n, k, v, device_error=err)
+    assert int(err) == 0
+    for out, cache, part in ((k, c.k, 0), (v, c.v, 1)):
+        want = torch.full_like(out, 5.0)
+        for b in range(B):
+            s, e = start[b], start[b] + count[b]
+            x = cache[b, :, s:e].float() * c.scales[b, :, s:e, part:part + 1]
+            want[b, :, :count[b]] = x.to(torch.bfloat16)
+        assert torch.equal(torch.isnan(out), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(out), torch.nan_to_num(want))
+
+
+def test_dequant_of_written_e4m3_rows_is_exact_and_int8_within_half_a_step():
+    x = rows((1, 40, 3, R.D), 8)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for dtype in R.DTYPES:
+        c = native.QuantCache(1, 3, 40, dtype)
+        native.kv_append_quant(x, x, z, z + 40, c.k, c.v, c.scales)
+        k, v = (torch.zeros(1, 3, 40, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+        native.kv_dequant(c.k, c.v, c.scales, z, z + 40, k, v)
+        codes, scales = R.quantise(x[0].transpose(0, 1), dtype)
+        want = codes * scales[..., None].double()
+        if dtype == R.E4M3:
+            assert torch.equal(k[0].double(), want)
+        else:
+            assert ((k[0].double() - want).abs() <= (R.HALF_BF16 + R.HALF_F32) * want.abs()).all()
+        assert torch.equal(k, v)
+
+
+# ---- append ------------------------------------------------------------------------------
+
+APPENDS = [
+    # B, Hkv, M, Lmax, positions, sink units, offset
+    (2, 8, 4, 64, [0, 37], (0, 1, 9, 12), 0),
+    (3, 4, 1, 64, [63, 5, 0], (2, 5, 11), 0),
+    (2, 4, 2, 41, [17, 0], (0, 7), 90),
+    (3, 8, 8, 16, [0, 15, 3], (3, 8, 15, 23), 5),
+    (9, 32, 1, 100, [99, 0, 1, 2, 3, 50, 60, 98, 0], tuple(range(0, 288, 7)), 0),
+]
+
+
+def append_case(B, Hkv, M, Lmax, positions, sinks, off, seed=3):
+    """Inputs whose listed units are sinks once rotated (built by rotating the
+    target back with the oracle), and the oracle's state after the step."""
+    g = torch.Generator().manual_seed(seed)
+    q, kn, vn = inputs.make_projections(B, Hkv * M, Hkv, seed=seed)
+    cs, sn = inputs.rope_tables(Lmax + off)
+    k0, v0 = (torch.randn(B, Hkv, R.D, generator=g).to(torch.bfloat16) for _ in range(2))
+    seq = torch.tensor(positions, dtype=torch.int32)
+    dummy = torch.zeros(B, Hkv, Lmax, R.D, dtype=torch.bfloat16)
+    o = oracle.load()
+    run = lambda x, s: o.rope_append(x, kn, vn, cs[off:].contiguous(), s[off:].contiguous(), seq, dummy, dummy, k0, v0)  # noqa: E731
+    after = run(q, sn)
+    k0_after = after[4] if off == 0 else k0
+    v0_after = after[5] if off == 0 else v0
+    target = q.clone()
+    for u in sinks:
+        b, gg = divmod(u, Hkv)
+        for m in range(M):
+            noise = 0.03 * torch.randn(R.D, generator=g) * k0_after[b, gg].float().norm() / 11.3
+            target[b, gg * M + m] = (k0_after[b, gg].float() + noise).to(torch.bfloat16)
+    back = run(target, -sn)[1]
+    for u in sinks:
+        b, gg = divmod(u, Hkv)
+        q[b, gg * M:(gg + 1) * M] = back[b, gg * M:(gg + 1) * M]
+    after = run(q, sn)
+    return dict(q=q, kn=kn, vn=vn, cs=cs, sn=sn, seq=seq, k0=k0, v0=v0), after, k0_after, v0_after
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, *R.DTYPES], ids=["bf16", *R.IDS])
+@pytest.mark.parametrize("separate", [False, True], ids=["inplace", "separate"])
+@pytest.mark.parametrize("B,Hkv,M,Lmax,pos,sinks,off", APPENDS, ids=[f"B{a[0]}Hkv{a[1]}M{a[2]}" for a in APPENDS])
+def test_append_matches_oracle(B, Hkv, M, Lmax, pos, sinks, off, separate, dtype):
+    c, after, k0_ref, v0_ref = append_case(B, Hkv, M, Lmax, pos, sinks, off)
+    d = {k: v.to(DEV) for k, v in c.items()}
+    quant = dtype != torch.bfloat16
+    if quant:
+        cache = sentinel_cache(B, Hkv, Lmax, dtype)
+        kc, vc, sc = cache.k, cache.v, cache.scales
+    else:
+        kc, vc, sc = torch.full((B, Hkv, Lmax, R.D), 3.0, device=DEV, dtype=dtype), None, None
+        vc = kc.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = torch.full_like(d["seq"], -1) if separate else None
+    q_out, mask, active = native.rope_append_route_kv(
+        d["q"], d["kn"], d["vn"], d["cs"], d["sn"], d["seq"], kc, vc, sc, d["k0"], d["v0"], TAU, pos_offset=off,
+        seq_lens_out=lens, device_error=err)
+    assert int(err) == 0
+    bits = lambda t: t.detach().cpu().contiguous().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(q_out), bits(after[1]))
+    assert torch.equal(bits(d["k0"]), bits(k0_ref)) and torch.equal(bits(d["v0"]), bits(v0_ref))
+    assert torch.equal((lens if separate else d["seq"]).cpu(), c["seq"] + 1)
+    if separate:
+        assert torch.equal(d["seq"].cpu(), c["seq"])
+    m2, a2 = native.route(q_out, d["k0"], TAU)
+    H.assert_route_equal(mask.cpu(), active.cpu(), m2.cpu(), a2.cpu())
+    assert all(int(mask[u]) == 1 for u in sinks) and int(mask.sum()) < B * Hkv
+    seen = torch.zeros((B, Hkv, Lmax), dtype=torch.bool)
+    for b in range(B):
+        seen[b, :, pos[b]] = True
+        k_row, v_row = after[2][b, :, pos[b]], after[3][b, :, pos[b]]
+        if quant:
+            assert_rows(kc[b, :, pos[b]].cpu(), sc[b, :, pos[b], 0].cpu(), k_row, dtype, f"key {b}")
+            assert_rows(vc[b, :, pos[b]].cpu(), sc[b, :, pos[b], 1].cpu(), v_row, dtype, f"value {b}")
+        else:
+            assert torch.equal(bits(kc[b, :, pos[b]]), bits(k_row)) and torch.equal(bits(vc[b, :, pos[b]]), bits(v_row))
+    if quant:
+        assert (kc.view(torch.uint8).cpu()[~seen] == 0x55).all() and (vc.view(torch.uint8).cpu()[~seen] == 0x55).all()
+        assert (sc.cpu()[~seen] == -7.0).all()
+    else:
+        assert (kc.cpu()[~seen] == 3.0).all() and (vc.cpu()[~seen] == 3.0).all()
+
+
+@both
+def test_append_bad_slots_leave_their_sequence_alone(dtype):
+    B, Hkv, M, Lmax = 4, 2, 4, 8
+    c, _, _, _ = append_case(B, Hkv, M, Lmax, [1, 2, 3, 4], (), 0)
+    d = {k: v.to(DEV) for k, v in c.items()}
+    d["seq"] = torch.tensor([8, -1, 3, 6], dtype=torch.int32, device=DEV)  # 6 + 3 is behind the tables
+    cache = sentinel_cache(B, Hkv, Lmax, dtype)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = torch.zeros_like(d["seq"])
+    q_out, mask, _ = native.rope_append_route_kv(
+        d["q"], d["kn"], d["vn"], d["cs"], d["sn"], d["seq"], cache.k, cache.v, cache.scales, d["k0"], d["v0"], TAU,
+        pos_offset=3, seq_lens_out=lens, device_error=err)
+    assert int(err) == native.SR_DEVERR_APPEND_SLOT
+    assert lens.tolist() == [8, -1, 4, 6]
+    assert (q_out[[0, 1, 3]] == 0).all() and (q_out[2] != 0).any()
+    wrote = (cache.scales[:, :, :, 0] != -7.0).nonzero().tolist()
+    assert wrote == [[2, 0, 3], [2, 1, 3]]
+
+
+# ---- the scan ----------------------------------------------------------------------------
+
+def filled_cache(B, Hkv, Lmax, lens, dtype, seed, spread=2.0, poison=True):
+    """A cache of random rows whose scales vary by 2^+-spread from row to row, with
+    NaN codes and scales behind every length."""
+    c = native.QuantCache(B, Hkv, Lmax, dtype)
+    z = torch.zeros(B, dtype=torch.int32, device=DEV)
+    shape = (B, Lmax, Hkv, R.D)
+    k, v = (torch.randn(shape, generator=gen(seed + i), device=DEV) *
+            torch.exp2(spread * (2 * torch.rand((*shape[:3], 1), generator=gen(seed + 2 + i), device=DEV) - 1))
+            for i in range(2))
+    native.kv_append_quant(k.to(torch.bfloat16), v.to(torch.bfloat16), z, z + Lmax, c.k, c.v, c.scales)
+    if poison:
+        for b in range(B):
+            for t in (c.k, c.v):
+                t.view(torch.uint8)[b, :, lens[b]:] = 0x7f
+            c.scales[b, :, lens[b]:] = math.nan
+    return c
+
+
+def check_scan(q, c, v0, lens, mask, out, lse, o_f32=None):
+    B, Hkv, _, _ = c.k.shape
+    M = q.shape[1] // Hkv
+    for b in range(B):
+        for g in range(Hkv):
+            h = slice(g * M, (g + 1) * M)
+            if mask[b][g]:
+                assert torch.equal(out[b, h], v0[b, g].expand(M, -1)) and torch.isnan(lse[b, h]).all()
+                continue
+            k, v = (t[b, g, :lens[b]].double() * c.scales[b, g, :lens[b], i:i + 1].double()
+                    for i, t in enumerate((c.k, c.v)))
+            o, z, a, delta = R.attention(q[b, h], k, v, lens[b])
+            under = lens[b] * 2.0 ** -39 * float(v.abs().max())
+            lim = R.bound(o, a, delta, R.HALF_F16, R.HALF_BF16, under)
+            err = (out[b, h].double() - o).abs()
+            assert (err <= lim).all(), f"unit {b},{g}: {float((err / lim).max())} of the bound"
+            assert ((lse[b, h].double() - z).abs() <= R.lse_bound(z, delta)).all(), f"lse of unit {b},{g}"
+            if o_f32 is not None:
+                lim = R.bound(o, a, delta, R.HALF_F16, R.HALF_F32, under)
+                assert ((o_f32[b, h].double() - o).abs() <= lim).all()
+
+
+def scan(q, c, v0, lens, mask, n_splits=0, stream=None):
+    """Both forms of the scan; out, lse and the partials."""
+    B, Hkv, Lmax, _ = c.k.shape
+    units = (mask.reshape(-1) == 0).nonzero().reshape(-1).to(torch.int32)
+    active = torch.full((1 + B * Hkv,), -1, dtype=torch.int32, device=DEV)
+    active[0] = units.numel()
+    active[1:1 + units.numel()] = units
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = native.Workspace(B, q.shape[1], Hkv, Lmax, n_splits)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    torch.cuda.synchronize()
+    out = native.decode_attention_quant(q, c.k, c.v, c.scales, v0, sl, active, n_splits=n_splits, workspace=ws, lse=lse,
+                                        stream=stream)
+    o, z = native.decode_attention_quant_partial(q, c.k, c.v, c.scales, v0, sl, active, n_splits=n_splits, workspace=ws,
+                                                 stream=stream)
+    torch.cuda.synchronize()
+    assert ws.device_error() == 0
+    assert torch.equal(torch.nan_to_num(z, nan=-7.0), torch.nan_to_num(lse, nan=-7.0))
+    return out, lse, o
+
+
+SCANS = [
+    # B, Hkv, M, Lmax, lens, n_splits
+    (1, 1, 1, 1, [1], 0),
+    (1, 1, 8, 129, [129], 0),  # an odd number of scale pairs, the last one read on its own
+    (1, 5, 4, 131, [131], 0),
+    (3, 1, 2, 257, [2, 257, 128], 0),
+    (4, 8, 4, 700, [1, 127, 700, 513], 0),
+    (2, 8, 8, 3001, [3001, 1400], 0),
+    (5, 8, 1, 999, [999, 1, 500, 64, 65], 3),
+    (1, 8, 4, 20011, [20011], 0),
+    (1, 2, 8, 4099, [4099], 37),
+    (40, 2, 2, 67, [1 + (13 * i) % 67 for i in range(40)], 0),  # more than 32 units
+]
+
+
+@both
+@pytest.mark.parametrize("B,Hkv,M,Lmax,lens,ns", SCANS, ids=[f"B{s[0]}Hkv{s[1]}M{s[2]}L{s[3]}s{s[5]}" for s in SCANS])
+def test_scan_against_64_bits(B, Hkv, M, Lmax, lens, ns, dtype):
+    c = filled_cache(B, Hkv, Lmax, lens, dtype, 11)
+    q = torch.randn(B, Hkv * M, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.randn(B, Hkv, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    mask = torch.rand(B, Hkv, generator=gen(3), device=DEV) < 0.3
+    mask[0, 0] = False
+    out, lse, o = scan(q, c, v0, lens, mask, ns)
+    check_scan(q, c, v0, lens, mask.tolist(), out, lse, o)
+
+
+@both
+@pytest.mark.parametrize("all_sinks", [True, False])
+def test_scan_of_all_sinks_and_none(all_sinks, dtype):
+    c = filled_cache(2, 4, 50, [50, 9], dtype, 5)
+    q = torch.randn(2, 16, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.randn(2, 4, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    mask = torch.full((2, 4), all_sinks, device=DEV)
+    out, lse, o = scan(q, c, v0, [50, 9], mask)
+    check_scan(q, c, v0, [50, 9], mask.tolist(), out, lse, o)
+
+
+@both
+@pytest.mark.parametrize("case", ["scales", "tiny_scales", "zero_scales", "huge_q", "tiny_q", "zero_q", "one_hot", "sink_row"])
+def test_scan_extreme_values(case, dtype):
+    B, Hkv, M, Lmax = 1, 2, 4, 400
+    lens = [387]
+    c = filled_cache(B, Hkv, Lmax, lens, dtype, 21)
+    q = torch.randn(B, Hkv * M, R.D, generator=gen(1), device=DEV)
+    n = lens[0]
+    if case == "scales":  # value scales over 2^60, in rising and falling order
+        e = torch.linspace(-40, 20, n, device=DEV)
+        c.scales[0, 0, :n, 1] = torch.exp2(e)
+        c.scales[0, 1, :n, 1] = torch.exp2(e.flip(0))
+    elif case == "tiny_scales":
+        c.scales[0, :, :n, 1] = 2.0 ** -106
+    elif case == "zero_scales":
+        c.scales[0, :, :n, 1] = 0.0
+        c.scales[0, 1, 5, 1] = 1.0
+    elif case == "huge_q":
+        q *= 2.0 ** 100
+        c.scales[0, :, :n, 0] *= 2.0 ** -100
+    elif case == "tiny_q":
+        q *= 2.0 ** -90
+        c.scales[0, :, :n, 0] *= 2.0 ** 90
+    elif case == "zero_q":
+        q.zero_()
+    elif case == "one_hot":  # one element carries the row: the others are far below it
+        q *= 2.0 ** -12
+        q[..., 5] = 3.0
+    elif case == "sink_row":  # one position takes nearly all the weight, late in the scan
+        c.scales[0, :, 380, 0] *= 60.0
+    q = q.to(torch.bfloat16)
+    v0 = torch.zeros(B, Hkv, R.D, device=DEV, dtype=torch.bfloat16)
+    mask = torch.zeros(B, Hkv, dtype=torch.bool, device=DEV)
+    out, lse, o = scan(q, c, v0, lens, mask, 2)
+    check_scan(q, c, v0, lens, mask.tolist(), out, lse, o)
+
+
+@both
+def test_scan_propagates_a_stored_nan_row(dtype):
+    c = filled_cache(1, 2, 64, [64], dtype, 2)
+    c.scales[0, 1, 40] = math.nan
+    q = torch.randn(1, 8, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.zeros(1, 2, R.D, device=DEV, dtype=torch.bfloat16)
+    out, lse, _ = scan(q, c, v0, [64], torch.zeros(1, 2, dtype=torch.bool, device=DEV))
+    assert torch.isfinite(out[0, :4]).all() and torch.isnan(out[0, 4:]).all()
+
+
+@both
+def test_scan_is_deterministic_and_repeats_in_a_graph(dtype):
+    B, Hkv, M, Lmax = 2, 4, 4, 5003
+    lens = [5003, 2600]
+    c = filled_cache(B, Hkv, Lmax, lens, dtype, 9)
+    q = torch.randn(B, Hkv * M, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    k0 = torch.randn(B, Hkv, R.D, generator=gen(4), device=DEV).to(torch.bfloat16)
+    v0 = torch.randn(B, Hkv, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    dec = native.QuantDecoder(B, Hkv * M, Hkv, Lmax)
+    first = dec.step(q, c, k0, v0, sl, TAU).clone()
+    for _ in range(5):
+        assert torch.equal(dec.step(q, c, k0, v0, sl, TAU), first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dec.step(q, c, k0, v0, sl, TAU)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = native.QuantDecoder(B, Hkv * M, Hkv, Lmax)
+    with torch.cuda.stream(side):  # another decoder's calls while the graph replays
+        for _ in range(5):
+            o2 = other.step(q, c, k0, v0, sl, TAU)
+    dec.out.zero_()
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dec.out, first) and torch.equal(o2, first)
+
+
+@both
+def test_scan_reports_bad_lengths_and_lists(dtype):
+    c = filled_cache(2, 2, 30, [30, 30], dtype, 9, poison=False)
+    q = torch.randn(2, 4, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.zeros(2, 2, R.D, device=DEV, dtype=torch.bfloat16)
+    ws = native.Workspace(2, 4, 2, 30)
+    active = torch.tensor([4, 0, 1, 2, 3], dtype=torch.int32, device=DEV)
+    full = native.decode_attention_quant(q, c.k, c.v, c.scales, v0,
+                                         torch.tensor([30, 1], dtype=torch.int32, device=DEV), active, workspace=ws)
+    got = native.decode_attention_quant(q, c.k, c.v, c.scales, v0,
+                                        torch.tensor([77, 0], dtype=torch.int32, device=DEV), active, workspace=ws)
+    assert ws.device_error() == native.SR_DEVERR_SEQ_LEN and torch.equal(got, full)
+    ws.clear_device_error()
+    native.decode_attention_quant(q, c.k, c.v, c.scales, v0, torch.tensor([3, 3], dtype=torch.int32, device=DEV),
+                                  torch.tensor([3, 0, 2, 1, 9], dtype=torch.int32, device=DEV), workspace=ws)
+    assert ws.device_error() == native.SR_DEVERR_ACTIVE_LIST
+
+
+@both
+def test_far_positions_of_a_cache_over_4_gib(dtype):
+    """Rows behind byte offset 2^32 and position 2^24: written, scanned and read
+    back. All other rows are zero keys (logit 0) and zero values."""
+    Lmax, Hkv, M = (1 << 24) + 3, 2, 4
+    c = native.QuantCache(1, Hkv, Lmax, dtype)
+    c.scales.fill_(1.0)
+    x, y = rows((1, 3, Hkv, R.D), 4)[:, :, :, :], torch.randn(1, 3, Hkv, R.D, generator=gen(6), device=DEV)
+    x = torch.randn(1, 3, Hkv, R.D, generator=gen(5), device=DEV).to(torch.bfloat16)
+    y = y.to(torch.bfloat16)
+    st = torch.tensor([Lmax - 3], dtype=torch.int32, device=DEV)
+    native.kv_append_quant(x, y, st, torch.full_like(st, 3), c.k, c.v, c.scales)
+    k, v = (torch.zeros(1, Hkv, 3, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    native.kv_dequant(c.k, c.v, c.scales, st, torch.full_like(st, 3), k, v)
+    kc, ks = R.quantise(x[0].transpose(0, 1), dtype)
+    vc, vs = R.quantise(y[0].transpose(0, 1), dtype)
+    assert torch.equal(c.k[0, :, -3:].double(), kc) and torch.equal(c.v[0, :, -3:].double(), vc)
+    kd, vd = kc * ks[..., None].double(), vc * vs[..., None].double()
+    assert torch.allclose(k[0].double(), kd, rtol=2.0 ** -8, atol=0) and torch.allclose(v[0].double(), vd, rtol=2.0 ** -8, atol=0)
+    # queries along the last keys, so that these hold most of the weight
+    q = (4.0 * kd[:, 2:3] + 0.1 * torch.randn(Hkv, M, R.D, generator=gen(7), device=DEV)).to(torch.bfloat16).reshape(1, Hkv * M, R.D)
+    sl = torch.tensor([Lmax], dtype=torch.int32, device=DEV)
+    active = torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV)
+    lse = torch.zeros(1, Hkv * M, device=DEV)
+    out = native.decode_attention_quant(q, c.k, c.v, c.scales, v[:, :, 0].contiguous(), sl, active, lse=lse)
+    for g in range(Hkv):
+        h = slice(g * M, (g + 1) * M)
+        s = q[0, h].double() @ kd[g].T / math.sqrt(R.D)
+        e = torch.exp(s)
+        tot = e.sum(-1, keepdim=True) + (Lmax - 3)
+        o = e @ vd[g] / tot
+        a = e @ vd[g].abs() / tot
+        delta = 130 * R.HALF_F32 * (q[0, h].double().abs() @ kd[g].abs().T / math.sqrt(R.D)).amax(-1)
+        # the sum of 2^24 ones in fp32: lanes, warps and splits add at most 2^14 of them in a row. Weights far
+        # below the last row's may vanish, as in check_scan: fp16's smallest step is 2^-24, half of it is lost,
+        # and the weights are scaled by 2^14, so three rows can lose 2^-39 of the largest weight each.
+        under = 3 * 2.0 ** -39 * float(vd[g].abs().max())
+        lim = R.bound(o, a, delta, R.HALF_F16, R.HALF_BF16, under) + 2.0 ** -10 * a
+        err = (out[0, h].double() - o).abs()
+        assert bool((err <= lim).all()), float((err / lim).max())
+        assert ((lse[0, h].double() - torch.log(tot[:, 0])).abs() <= R.lse_bound(torch.log(tot[:, 0]), delta) + 2.0 ** -10).all()
+
+
+# ---- together ----------------------------------------------------------------------------
+
+@both
+def test_prefill_then_decode_steps(dtype):
+    """A prompt is written in two chunks, then tokens are appended and attended to,
+    each step against 64 bits on the cache that the definitions give."""
+    B, Hkv, M, Lmax = 2, 4, 4, 96
+    Hq = Hkv * M
+    prompt = [50, 33]
+    k, v = rows((B, 50, Hkv, R.D), 3), torch.randn(B, 50, Hkv, R.D, generator=gen(4), device=DEV).to(torch.bfloat16)
+    k = torch.randn(B, 50, Hkv, R.D, generator=gen(5), device=DEV).to(torch.bfloat16)
+    c = native.QuantCache(B, Hkv, Lmax, dtype)
+    k0, v0 = (torch.zeros(B, Hkv, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    n1 = torch.tensor([30, 30], dtype=torch.int32, device=DEV)
+    n2 = torch.tensor([n - 30 for n in prompt], dtype=torch.int32, device=DEV)
+    native.kv_append_quant(k[:, :30], v[:, :30], torch.zeros_like(n1), n1, c.k, c.v, c.scales, k0, v0)
+    native.kv_append_quant(k[:, 30:], v[:, 30:], n1, n2, c.k, c.v, c.scales, k0, v0)
+    assert torch.equal(k0, k[:, 0]) and torch.equal(v0, v[:, 0])
+    seq = (n1 + n2).clone()
+    cs, sn = inputs.rope_tables(Lmax, device=DEV)
+    dec = native.QuantDecoder(B, Hq, Hkv, Lmax)
+    keys, values = ([[x[b, :prompt[b]].transpose(0, 1)] for b in range(B)] for x in (k, v))
+    o = oracle.load()
+    dummy = torch.zeros(B, Hkv, Lmax, R.D, dtype=torch.bfloat16)
+    for step in range(4):
+        q, kn, vn = inputs.make_projections(B, Hq, Hkv, seed=40 + step, device=DEV)
+        before = seq.cpu()
+        out = dec.append_step(q, kn, vn, cs, sn, c, k0, v0, seq, TAU)
+        ref = o.rope_append(q, kn, vn, cs, sn, before, dummy, dummy, k0, v0)
+        assert torch.equal(dec.q.cpu().view(torch.int16), ref[1].view(torch.int16))
+        assert torch.equal(seq.cpu(), before + 1)
+        for b in range(B):
+            keys[b].append(ref[2][b, :, before[b]].to(DEV)[:, None])
+            values[b].append(vn[b][:, None])
+        mask = dec.route_mask.view(B, Hkv).tolist()
+        for b in range(B):
+            kc, ks = R.quantise(torch.cat(keys[b], 1), dtype)
+            vc, vs = R.quantise(torch.cat(values[b], 1), dtype)
+            for g in range(Hkv):
+                h = slice(g * M, (g + 1) * M)
+                if mask[b][g]:
+                    assert torch.equal(out[b, h], v0[b, g].expand(M, -1))
+                    continue
+                vd = vc[g] * vs[g][:, None].double()
+                oo, _, a, delta = R.attention(dec.q[b, h], kc[g] * ks[g][:, None].double(), vd, vd.shape[0])
+                under = vd.shape[0] * 2.0 ** -39 * float(vd.abs().max())
+                assert ((out[b, h].double() - oo).abs() <= R.bound(oo, a, delta, R.HALF_F16, R.HALF_BF16, under)).all()
+    assert dec.workspace.device_error() == 0

@@ -1,0 +1,265 @@
+"""Attention over a prefix that the batch shares, alone and joined with each
+sequence's suffix, against 64 bits (tests/quant_ref.py).
+
+Bars: sink heads are v0 bit for bit. Active heads are inside the elementwise bound
+of the kernel's roundings: softmax weights to bf16 (half a step, 2^-8), output to
+bf16 (2^-8), fp32 logits, statistics and sums."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import oracle
+from kv_cache_routing_sr_b200 import inputs, native, shared_prefix
+from tests import quant_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TAU = 0.6
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(shape, seed, scale=1.0):
+    return (scale * torch.randn(shape, generator=gen(seed), device=DEV)).to(torch.bfloat16)
+
+
+def check(q, parts_of, v0, mask, out, lse, half_out=R.HALF_BF16):
+    """parts_of(b, g, heads): attention() results whose union the unit attends to."""
+    B, Hq, _ = q.shape
+    Hkv = v0.shape[1]
+    M = Hq // Hkv
+    for b in range(B):
+        for g in range(Hkv):
+            h = slice(g * M, (g + 1) * M)
+            if mask[b][g]:
+                assert torch.equal(out[b, h].float(), v0[b, g].float().expand(M, -1))
+                assert lse is None or torch.isnan(lse[b, h]).all()
+                continue
+            o, z, a, delta = R.join(parts_of(b, g, q[b, h]))
+            if torch.isinf(z).all():
+                assert (out[b, h] == 0).all() and (lse is None or (lse[b, h] == -math.inf).all())
+                continue
+            lim = R.bound(o, a, delta, R.HALF_BF16, half_out)
+            err = (out[b, h].double() - o).abs()
+            assert (err <= lim).all(), f"unit {b},{g}: {float((err / lim).max())} of the bound"
+            if lse is not None:
+                assert ((lse[b, h].double() - z).abs() <= R.lse_bound(z, delta)).all(), f"lse of unit {b},{g}"
+
+
+CASES = [
+    # B, Hkv, M, prefix_len, capacity
+    (1, 1, 1, 1, 1),
+    (1, 8, 4, 0, 5),
+    (2, 8, 4, 127, 130),
+    (3, 32, 1, 577, 577),
+    (5, 4, 2, 128, 128),
+    (7, 3, 8, 129, 400),
+    (33, 2, 4, 1000, 1001),   # 132 rows a KV head
+    (40, 2, 8, 2500, 2500),   # 320 rows
+    (64, 1, 8, 257, 300),     # 512 rows
+    (2, 2, 8, 40000, 40000),  # long, few rows: many splits
+    (129, 3, 1, 384, 384),
+]
+
+
+@pytest.mark.parametrize("B,Hkv,M,Lp,cap", CASES, ids=[f"B{c[0]}Hkv{c[1]}M{c[2]}L{c[3]}" for c in CASES])
+def test_prefix_against_64_bits(B, Hkv, M, Lp, cap):
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, cap, R.D), 3), randn((Hkv, cap, R.D), 4)
+    k[:, Lp:], v[:, Lp:] = math.nan, math.nan  # behind the prefix: never used
+    mask = (torch.rand(B, Hkv, generator=gen(5), device=DEV) < 0.25).to(torch.uint8)
+    mask[0, 0] = 0
+    ws = native.PrefixWorkspace(B, Hkv * M, Hkv, cap)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse, workspace=ws)
+    o, z = native.prefix_attention_partial(q, k, v, Lp, v0, mask.reshape(-1), workspace=ws)
+    assert ws.device_error() == 0
+    assert torch.equal(torch.nan_to_num(z, nan=-7.0), torch.nan_to_num(lse, nan=-7.0))
+    part = lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)]  # noqa: E731
+    check(q, part, v0, mask.tolist(), out, lse)
+    check(q, part, v0, mask.tolist(), o, z, R.HALF_F32)
+
+
+@pytest.mark.parametrize("fill", ["all", "none", "one_group", "one_row"])
+def test_prefix_masks(fill):
+    B, Hkv, M, Lp = 6, 4, 4, 300
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    mask = torch.zeros(B, Hkv, dtype=torch.uint8, device=DEV)
+    if fill == "all":
+        mask[:] = 1
+    elif fill == "one_group":
+        mask[:, 2] = 255  # any value but 0 is a sink
+    elif fill == "one_row":
+        mask[:] = 1
+        mask[5, 1] = 0
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse)
+    check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.tolist(), out, lse)
+
+
+@pytest.mark.parametrize("case", ["late_peak", "early_peak", "rising", "zero_q", "large_v"])
+def test_prefix_extreme_logits(case):
+    """Running maxima that jump late, never, or in every tile."""
+    B, Hkv, M, Lp = 3, 2, 8, 1700
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3, 0.2).float(), randn((Hkv, Lp, R.D), 4)
+    dirn = q[0, 0].float() / q[0, 0].float().norm()
+    if case == "late_peak":
+        k[:, 1650] = 90 * dirn
+    elif case == "early_peak":
+        k[:, 3] = 90 * dirn
+    elif case == "rising":
+        k += torch.linspace(0, 60, Lp, device=DEV)[None, :, None] * dirn
+    elif case == "zero_q":
+        q.zero_()
+    elif case == "large_v":
+        v = (v.float() * 1e30).to(torch.bfloat16)
+    k = k.to(torch.bfloat16)
+    mask = torch.zeros(B * Hkv, dtype=torch.uint8, device=DEV)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = native.prefix_attention(q, k, v, Lp, v0, mask, lse=lse)
+    check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.view(B, Hkv).tolist(), out, lse)
+
+
+def suffix_of(kind, B, Hkv, n, seed):
+    k, v = randn((B, n, Hkv, R.D), seed), randn((B, n, Hkv, R.D), seed + 1)
+    if kind == "bf16":
+        return k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous(), None
+    c = native.QuantCache(B, Hkv, n, R.E4M3 if kind == "e4m3" else R.INT8)
+    z = torch.zeros(B, dtype=torch.int32, device=DEV)
+    native.kv_append_quant(k, v, z, z + n, c.k, c.v, c.scales)
+    return c.k, c.v, c.scales
+
+
+def suffix_rows(k, v, sc, b, g, n):
+    if sc is None:
+        return k[b, g, :n], v[b, g, :n]
+    return tuple(t[b, g, :n].double() * sc[b, g, :n, i:i + 1].double() for i, t in enumerate((k, v)))
+
+
+@pytest.mark.parametrize("kind", ["bf16", *R.IDS])
+@pytest.mark.parametrize("B,Hkv,M,Lp", [(2, 8, 4, 600), (9, 4, 8, 77), (5, 32, 1, 0), (40, 2, 4, 129)])
+def test_shared_prefix_step(B, Hkv, M, Lp, kind):
+    cap, n = max(1, Lp), 90
+    lens = [1 + (31 * b) % n for b in range(B)]
+    k0, v0 = randn((B, Hkv, R.D), 5), randn((B, Hkv, R.D), 6)
+    q = randn((B, Hkv * M, R.D), 1)
+    for b in range(B):  # some sinks
+        g = b % Hkv
+        q[b, g * M:(g + 1) * M] = (k0[b, g].float() + 0.05 * q[b, g * M:(g + 1) * M].float()).to(torch.bfloat16)
+    kp, vp = randn((Hkv, cap, R.D), 3), randn((Hkv, cap, R.D), 4)
+    ks, vs, sc = suffix_of(kind, B, Hkv, n, 7)
+    dec = shared_prefix.SharedPrefixDecoder(B, Hkv * M, Hkv, cap, n)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = dec.step(q, kp, vp, Lp, ks, vs, k0, v0, sl, TAU, kv_scales=sc)
+    mask = dec.route_mask.view(B, Hkv).tolist()
+    assert all(mask[b][b % Hkv] for b in range(B)) and (B * Hkv <= 32 or not all(all(m) for m in mask))
+    parts = lambda b, g, rows: [R.attention(rows, kp[g], vp[g], Lp),  # noqa: E731
+                                R.attention(rows, *suffix_rows(ks, vs, sc, b, g, lens[b]), lens[b])]
+    check(q, parts, v0, mask, out, None)
+    # combine_partials on the two parts gives the same heads
+    o, z = native.prefix_attention_partial(q, kp, vp, Lp, v0, dec.route_mask, workspace=dec.workspace)
+    stride = (o.numel() + 3) // 4 * 4
+    both_o = torch.zeros(2 * stride, device=DEV)
+    both_z = torch.zeros(2 * stride, device=DEV)
+    for i, (x, y) in enumerate(((o, z), (dec.o_suffix, dec.lse_suffix))):
+        both_o[i * stride:i * stride + x.numel()] = x.reshape(-1)
+        both_z[i * stride:i * stride + y.numel()] = y.reshape(-1)
+    joined = native.combine_partials(both_o, both_z, stride, 2, B, Hkv * M)
+    check(q, parts, v0, mask, joined, None)
+
+
+def test_join_with_an_empty_part():
+    """A suffix (or prefix) without a position weighs nothing; both empty give 0."""
+    B, Hkv, M, Lp = 2, 2, 4, 50
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    mask = torch.tensor([0, 1, 0, 0], dtype=torch.uint8, device=DEV)
+    o_s = torch.randn(B, Hkv * M, R.D, generator=gen(8), device=DEV)
+    z_s = torch.full((B, Hkv * M), -math.inf, device=DEV)
+    alone, joined = torch.zeros(B, Hkv * M, device=DEV), torch.zeros(B, Hkv * M, device=DEV)
+    a = native.prefix_attention(q, k, v, Lp, v0, mask, lse=alone)
+    b = native.prefix_attention(q, k, v, Lp, v0, mask, lse=joined, o_suffix=o_s, lse_suffix=z_s)
+    assert torch.equal(a, b)
+    keep = ~torch.isnan(alone)
+    assert torch.equal(torch.isnan(joined), ~keep) and torch.allclose(alone[keep], joined[keep], rtol=1e-6)
+    both = native.prefix_attention(q, k, v, 0, v0, mask, lse=joined, o_suffix=o_s, lse_suffix=z_s)
+    assert (joined[keep] == -math.inf).all() and (both[keep] == 0).all()
+    z_s.fill_(1.5)
+    one = native.prefix_attention(q, k, v, 0, v0, mask, lse=joined, o_suffix=o_s, lse_suffix=z_s)
+    assert torch.equal(one[keep], o_s.to(torch.bfloat16)[keep]) and (joined[keep] == 1.5).all()
+
+
+def test_prefix_repeats_in_a_graph_and_on_a_side_stream():
+    B, Hkv, M, Lp, n = 9, 4, 8, 3000, 64
+    q, k0, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2), randn((B, Hkv, R.D), 3)
+    kp, vp = randn((Hkv, Lp, R.D), 4), randn((Hkv, Lp, R.D), 5)
+    ks, vs, sc = suffix_of("e4m3", B, Hkv, n, 6)
+    sl = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    args = (q, kp, vp, Lp, ks, vs, k0, v0, sl, TAU, sc)
+    dec, other = (shared_prefix.SharedPrefixDecoder(B, Hkv * M, Hkv, Lp, n) for _ in range(2))
+    first = dec.step(*args).clone()
+    for _ in range(5):
+        assert torch.equal(dec.step(*args), first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dec.step(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            o2 = other.step(*args)
+    dec.out.zero_()
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dec.out, first) and torch.equal(o2, first)
+    # new values in the bound tensors: the replay reads them
+    q.copy_(randn(q.shape, 9))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dec.out, other.step(*args))
+
+
+@pytest.mark.parametrize("kind", ["bf16", *R.IDS])
+def test_generation_behind_a_shared_prefix(kind):
+    """An 8-bit context is read back as the shared bf16 prefix; every sequence then
+    appends and attends, token by token, from an empty suffix."""
+    B, Hkv, M, Lp, n = 3, 4, 4, 200, 6
+    Hq = Hkv * M
+    src = native.QuantCache(1, Hkv, Lp, R.E4M3)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    native.kv_append_quant(randn((1, Lp, Hkv, R.D), 1), randn((1, Lp, Hkv, R.D), 2), z, z + Lp, src.k, src.v, src.scales)
+    kp, vp = (torch.zeros(1, Hkv, Lp, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    native.kv_dequant(src.k, src.v, src.scales, z, z + Lp, kp, vp)
+    kp, vp = kp[0], vp[0]
+    k0, v0 = (x[None, :, 0].expand(B, -1, -1).contiguous() for x in (kp, vp))
+    keep0 = k0.clone()
+    if kind == "bf16":
+        kc, vc, sc = (torch.zeros(B, Hkv, n, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2)), None, None
+        kc, vc = kc
+    else:
+        c = native.QuantCache(B, Hkv, n, R.E4M3 if kind == "e4m3" else R.INT8)
+        kc, vc, sc = c.k, c.v, c.scales
+    seq = torch.zeros(B, dtype=torch.int32, device=DEV)
+    cs, sn = inputs.rope_tables(Lp + n, device=DEV)
+    dec = shared_prefix.SharedPrefixDecoder(B, Hq, Hkv, Lp, n)
+    dummy = torch.zeros(B, Hkv, n, R.D, dtype=torch.bfloat16)
+    for step in range(n):
+        q, kn, vn = inputs.make_projections(B, Hq, Hkv, seed=60 + step, device=DEV)
+        out = dec.append_step(q, kn, vn, cs, sn, kp, vp, Lp, kc, vc, k0, v0, seq, TAU, kv_scales=sc)
+        assert seq.tolist() == [step + 1] * B and torch.equal(k0, keep0)
+        ref = oracle.load().rope_append(q, kn, vn, cs[Lp:].contiguous(), sn[Lp:].contiguous(),
+                                        torch.full((B,), step, dtype=torch.int32), dummy, dummy, k0, v0)
+        assert torch.equal(dec.q.cpu().view(torch.int16), ref[1].view(torch.int16))
+        check(dec.q, lambda b, g, rows: [R.attention(rows, kp[g], vp[g], Lp),
+                                         R.attention(rows, *suffix_rows(kc, vc, sc, b, g, step + 1), step + 1)],
+              v0, dec.route_mask.view(B, Hkv).tolist(), out, None)
+        if kind == "bf16":
+            assert torch.equal(kc[:, :, step].cpu().view(torch.int16), ref[2][:, :, step].view(torch.int16))
