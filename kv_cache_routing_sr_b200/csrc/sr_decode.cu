@@ -60,7 +60,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <mutex>
 
 #include "sinkrouter.h"
@@ -1516,40 +1515,6 @@ constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
-// 3-D view [units][Lmax][128] of a cache; a box is 128 bytes of a row (64 bf16
-// values, or all 128 codes; swizzled 128B) by `rows` positions of one unit. Rows
-// past Lmax read as zero.
-bool make_cache_map(CUtensorMap *map, const void *base, int units, int lmax, int rows, bool quant)
-{
-    auto fn = encode_fn();
-    if (!fn)
-        return false;
-    const cuuint64_t row_bytes = quant ? kHeadDim : kHeadDim * 2;
-    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)lmax, (cuuint64_t)units};
-    cuuint64_t strides[2] = {row_bytes, (cuuint64_t)lmax * row_bytes};
-    cuuint32_t box[3] = {quant ? 128u : 64u, (cuuint32_t)rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                          const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 using DecodeCfg = Cfg<SR_DECODE_RB, SR_DECODE_STAGES, 4, SR_KV_BF16>;
 // 8-bit caches: eight consumer warps of one row block each, the same 128 rows a
 // tile, in four 32 KB stages.
@@ -1638,8 +1603,8 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream)
     CUtensorMap tmK, tmV;
     const Variant v = pick(a.kv, a.fused);
     const bool quant = a.kv != SR_KV_BF16;
-    if (!make_cache_map(&tmK, a.k_cache, U, a.max_seq_len, v.rows, quant) ||
-        !make_cache_map(&tmV, a.v_cache, U, a.max_seq_len, v.rows, quant))
+    if (!make_cache_map(&tmK, a.k_cache, U, a.max_seq_len, v.rows, quant, a.max_seq_len) ||
+        !make_cache_map(&tmV, a.v_cache, U, a.max_seq_len, v.rows, quant, a.max_seq_len))
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     Params p;

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "sinkrouter.h"
@@ -138,11 +139,13 @@ cudaError_t launch_position0(int B, int Hq, int Hkv, int Lmax, const void *q, co
                              float *p0, cudaStream_t stream);
 cudaError_t launch_combine(int n_heads, int n_parts, const float *o_parts, const float *lse_parts, int64_t part_stride,
                            void *out, cudaStream_t stream);
+// Tensor map over a cache's first `len` positions of every unit; false on failure.
+bool make_cache_map(CUtensorMap *map, const void *base, int units, int lmax, int rows, bool quant, int len);
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_write(const KvWriteArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t stream);
 cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream);
-// Workspace of the prefix attention (0: no device).
+// Workspace of the prefix attention.
 size_t prefix_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 // Persistent CTAs of the decode kernel on the current device (0 on error).
 int decode_grid_size();

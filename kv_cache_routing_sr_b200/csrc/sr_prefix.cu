@@ -3,119 +3,733 @@
 //
 // Method: the split-K reduction of the SinkRouter README's decode-time procedure
 // list, carried across two caches: softmax attention over a union of position
-// ranges is sum_r exp(lse_r - lse) o_r with lse = log sum_r exp(lse_r).
+// ranges is sum_r exp(lse_r - lse) o_r with lse = log sum_r exp(lse_r). Over the
+// prefix the query heads of every active sequence of a KV head are the rows of
+// one matrix Q_g [rows x 128], so S = Q_g K_g^T and O = P V_g are matrix products,
+// and every prefix tile is read once for up to 256 rows.
 //
-// One CTA of 128 threads per query row: 128 positions at a time, each thread
-// takes one position's logit and then one output column, with a running maximum
-// and sum in fp32.
+// Three launches:
+//  * plan: one CTA lists the active sequences of each KV head and cuts each head's
+//    rows into items of up to 256.
+//  * scan: one persistent CTA per SM takes a contiguous share of the (item, tile
+//    of 128 positions) sequence and leaves one partial (m, l, O) a row for every
+//    item its share touches.
+//  * join: one warp a query head combines its partials, and the suffix's.
+//
+// scan, per CTA: two softmax warpgroups (a thread a row), a copy warp and an MMA
+// warp around two streams, each with its logits S (128 x 128, fp32) and its output O
+// in TMEM (all 512 columns). With more than 128 rows the streams are the item's two
+// halves over the same tiles; with fewer they are the same rows over alternate
+// tiles, and leave a partial each. While a warpgroup turns S into P (bf16, written
+// over S), the tensor cores work for the other stream: the issue order is P0 V, S0
+// of the next tile, P1 V, S1 of the next tile. The completion of S also means that
+// the stream's O is complete, so a warpgroup may rescale O before it hands over P;
+// it does so only when a row's maximum has grown by more than 2^8 since the
+// reference it uses (the weights stay below 2^8 of their row's sum, far inside bf16
+// and fp32).
+//
+// Every wait is bounded in time; a timeout sets a device error bit, and the CTA
+// leaves once its own copies and MMAs have landed.
+#include <climits>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <mutex>
 
 #include "sinkrouter.h"
 #include "sr_internal.h"
 #include "sr_ptx.cuh"
+#include "sr_tc.cuh"
 
 namespace sr {
 namespace {
 
-constexpr float kScale = 0.08838834764831845f; // 1 / sqrt(128)
+constexpr uint64_t kWaitLimitNs = 2000000000ull; // 2 s: far above any legitimate wait
+constexpr float kScaleLog2 = 0.12751743082459868f; // log2(e) / sqrt(128)
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr unsigned kFull = 0xffffffffu;
 
-template <typename Op> __device__ __forceinline__ float block_reduce(float x, float *sm, Op op)
+constexpr int kTile = 128;           // positions a tile, rows a stream
+constexpr int kItemRows = 2 * kTile; // rows an item
+constexpr int kGridCap = 256;        // persistent CTAs never exceed this (sizes the workspace)
+constexpr int kStages = 5;
+constexpr int kHalfBytes = kTile * 128;       // [128 rows x 64 bf16], 128B swizzle
+constexpr int kTileBytes = 2 * kHalfBytes;    // [128 x 128]
+constexpr int kThreads = 384;                 // two softmax warpgroups, one for copies and MMAs
+constexpr int kSoftmaxThreads = 256;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
+constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffBar = kOffRing + kStages * kTileBytes;
+constexpr int kSmem = kOffBar + 256 + 1024; // and room to align the base to 1024 B
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+// Workspace: [error word | n_items | active count, first item of each KV head | active
+// sequences of each head | rank of each unit | items | (m, l) | O]
+struct Layout {
+    size_t count, first, list, rank, items, ml, o, total;
+    int row_cap; // rows of a stream's partial
+    long long max_items, slots;
+};
+
+Layout layout(int B, int Hq, int Hkv)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        sm[threadIdx.x >> 5] = x;
-    __syncthreads();
-    return op(op(sm[0], sm[1]), op(sm[2], sm[3]));
+    Layout w;
+    const long long rows = (long long)B * (Hq / Hkv);
+    const size_t U = (size_t)B * Hkv;
+    w.row_cap = rows < kTile ? (int)((rows + 7) / 8 * 8) : kTile;
+    w.max_items = Hkv * ((rows + kItemRows - 1) / kItemRows);
+    w.slots = kGridCap + w.max_items;
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at = align_up(at + bytes, 256);
+        return here;
+    };
+    w.count = take(4 * (size_t)Hkv);
+    w.first = take(4 * (size_t)Hkv);
+    w.list = take(4 * U);
+    w.rank = take(4 * U);
+    w.items = take(16 * (size_t)w.max_items);
+    w.ml = take(8 * 2 * (size_t)w.slots * w.row_cap);
+    w.o = take(4 * 2 * (size_t)w.slots * w.row_cap * kHeadDim);
+    w.total = at;
+    return w;
 }
 
-__global__ void __launch_bounds__(kHeadDim) prefix_rows_kernel(PrefixArgs a)
+struct Params {
+    const __nv_bfloat16 *q, *v0;
+    const uint8_t *mask;
+    int32_t *err;
+    int32_t *n_items; // word 1 of the workspace
+    int32_t *count, *first, *list, *rank;
+    int4 *items; // KV head, first row of the head's rows, rows
+    float2 *ml;  // [slot][stream][row] (m in log2 units, l)
+    float *o;    // [slot][stream][16][row][8]
+    const float *o_suffix, *lse_suffix;
+    __nv_bfloat16 *out;
+    float *out_f32, *lse;
+    int B, Hq, Hkv, M, prefix_len, row_cap, grid;
+};
+
+// ---- plan -------------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params p)
 {
-    __shared__ float qs[kHeadDim], ps[kHeadDim], red[4];
+    __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ int carry;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row = blockIdx.x, t = threadIdx.x; // row = b * Hq + h
-    const int M = a.n_q_heads / a.n_kv_heads;
-    const int b = row / a.n_q_heads, g = (row - b * a.n_q_heads) / M;
-    const int u = b * a.n_kv_heads + g;
-    const __nv_bfloat16 *v0 = static_cast<const __nv_bfloat16 *>(a.v0) + (size_t)u * kHeadDim;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-    const size_t at = (size_t)row * kHeadDim + t;
-    if (a.mask[u]) {
-        if (a.out_f32)
-            a.out_f32[at] = __bfloat162float(v0[t]);
-        else
-            out[at] = v0[t];
-        if (a.lse && t == 0)
-            a.lse[row] = __int_as_float(0x7fc00000);
-        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // A warp a KV head: ranks of its active sequences, in order.
+    for (int g = warp; g < p.Hkv; g += kPlanThreads / 32) {
+        int n = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            const bool act = b < p.B && p.mask[(size_t)b * p.Hkv + g] == 0;
+            const unsigned ball = __ballot_sync(kFull, act);
+            const int r = n + __popc(ball & ((1u << lane) - 1u));
+            if (act)
+                p.list[(size_t)g * p.B + r] = b;
+            if (b < p.B)
+                p.rank[(size_t)b * p.Hkv + g] = act ? r : -1;
+            n += __popc(ball);
+        }
+        if (lane == 0)
+            p.count[g] = n;
     }
-    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k_prefix) + (size_t)g * a.max_seq_len * kHeadDim;
-    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_prefix) + (size_t)g * a.max_seq_len * kHeadDim;
-    qs[t] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[at]) * kScale;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int p0 = 0; p0 < a.prefix_len; p0 += kHeadDim) {
-        const int n = min(kHeadDim, a.prefix_len - p0);
+    if (threadIdx.x == 0)
+        carry = 0;
+    __syncthreads();
+    for (int g0 = 0; g0 < p.Hkv; g0 += kPlanThreads) {
+        const int g = g0 + (int)threadIdx.x;
+        const int rows = g < p.Hkv ? p.count[g] * p.M : 0;
+        const int n = (rows + kItemRows - 1) / kItemRows;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        if (lane == 31)
+            warp_sum[warp] = incl;
         __syncthreads();
-        float s = -INFINITY;
-        if (t < n) {
-            s = 0.f;
-            const __nv_bfloat162 *kr = reinterpret_cast<const __nv_bfloat162 *>(k + (size_t)(p0 + t) * kHeadDim);
-            for (int i = 0; i < kHeadDim / 2; ++i) {
-                const float2 x = __bfloat1622float2(kr[i]);
-                s = fmaf(qs[2 * i], x.x, s);
-                s = fmaf(qs[2 * i + 1], x.y, s);
-            }
+        int before = carry, all = 0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            before += w < warp ? warp_sum[w] : 0;
+            all += warp_sum[w];
         }
-        const float mn = fmaxf(m, block_reduce(s, red, [](float x, float y) { return fmaxf(x, y); }));
-        const float w = t < n ? expf(s - mn) : 0.f, keep = expf(m - mn);
-        ps[t] = w;
-        l = l * keep + block_reduce(w, red, [](float x, float y) { return x + y; });
-        o *= keep;
+        const int first = before + incl - n;
+        if (g < p.Hkv)
+            p.first[g] = first;
         for (int i = 0; i < n; ++i)
-            o = fmaf(ps[i], __bfloat162float(v[(size_t)(p0 + i) * kHeadDim + t]), o);
-        m = mn;
+            p.items[first + i] = make_int4(g, i * kItemRows, min(kItemRows, rows - i * kItemRows), 0);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            carry += all;
+        __syncthreads();
     }
-    float lse = l > 0.f ? m + logf(l) : (l == 0.f ? -INFINITY : l);
-    o = l == 0.f ? 0.f : o / l;
-    if (a.o_suffix) {
-        const float ls = a.lse_suffix[row], top = fmaxf(lse, ls);
-        if (top == -INFINITY) {
-            o = 0.f;
-        } else {
-            const float wp = expf(lse - top), ws = expf(ls - top);
-            o = (wp * o + ws * a.o_suffix[at]) / (wp + ws);
-            lse = top + logf(wp + ws);
-        }
-    }
-    if (a.out_f32)
-        a.out_f32[at] = o;
-    else
-        out[at] = __float2bfloat16_rn(o);
-    if (a.lse && t == 0)
-        a.lse[row] = lse;
+    if (threadIdx.x == 0)
+        *p.n_items = carry;
 }
 
-} // namespace
+// ---- scan -------------------------------------------------------------------------------
 
-size_t prefix_workspace_bytes(int, int, int) { return 256; }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*abort_flag)
+            return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
 
-cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
+// A CTA's part of one item: tiles [j0, j1).
+struct Segment {
+    int item, j0, j1;
+};
+
+// Share of CTA c of n_items x nt tiles: [c * share, (c + 1) * share).
+__device__ __forceinline__ long long share_of(long long tiles, int grid) { return (tiles + grid - 1) / grid; }
+
+struct Walk {
+    long long at, end;
+    int nt;
+    __device__ __forceinline__ bool next(Segment &s)
+    {
+        if (at >= end)
+            return false;
+        s.item = (int)(at / nt);
+        s.j0 = (int)(at - (long long)s.item * nt);
+        s.j1 = (int)min((long long)nt, s.j0 + (end - at));
+        at += s.j1 - s.j0;
+        return true;
+    }
+};
+
+// How a segment of n tiles runs on the two streams.
+struct Streams {
+    bool two; // the streams are two row tiles over the same tiles; else alternate tiles of one
+    int n;
+    __device__ __forceinline__ int steps(int s) const { return two ? n : (n + 1 - s) / 2; }
+    __device__ __forceinline__ int tile(int s, int t) const { return two ? t : 2 * t + s; }
+    // Places of tile j's keys and values in the segment's sequence of copies, which
+    // is the order of their first use.
+    __device__ __forceinline__ int key_at(int j) const { return two ? 2 * j : (j ? 2 * j - 1 : 0); }
+    __device__ __forceinline__ int value_at(int j) const { return two ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], q_full, s_full[2], p_full[2], o_full[2], seg_done, drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+static_assert(sizeof(Shared) <= 256, "barrier block");
+
+__global__ void __launch_bounds__(kThreads, 1)
+scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared *sh = reinterpret_cast<Shared *>(smem + kOffBar);
+    volatile int *abort_flag = &sh->abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty), q_full = smem_u32(&sh->q_full);
+    const uint32_t s_full = smem_u32(sh->s_full), p_full = smem_u32(sh->p_full), o_full = smem_u32(sh->o_full);
+    const uint32_t seg_done = smem_u32(&sh->seg_done);
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(q_full, kSoftmaxThreads);
+        mbar_init(seg_done, kSoftmaxThreads);
+        mbar_init(smem_u32(&sh->drain), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full + 8 * s, 1);
+            mbar_init(p_full + 8 * s, kTile);
+            mbar_init(o_full + 8 * s, 1);
+        }
+        sh->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc(smem_u32(&sh->tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    const int nt = (p.prefix_len + kTile - 1) / kTile;
+    Walk walk;
+    walk.nt = nt;
+    {
+        const long long tiles = (long long)__ldcg(p.n_items) * nt;
+        const long long share = share_of(tiles, gridDim.x);
+        walk.at = min((long long)blockIdx.x * share, tiles);
+        walk.end = min(walk.at + share, tiles);
+    }
+    Segment seg;
+    bool ok = true;
+
+    if (warp >= 8) {
+        regs_dec<56>();
+        if (warp == kCopyWarp && lane == 0) {
+            // ------------------------------------------------------------ copies
+            uint32_t pos = 0; // copies issued
+            auto copy = [&](const CUtensorMap *map, int g, int j) -> bool {
+                const uint32_t st = pos % kStages;
+                if (!wait_bar(empty0 + 8 * st, ((pos / kStages) & 1) ^ 1, abort_flag))
+                    return false;
+                const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem + kOffRing + st * kTileBytes);
+                mbar_arrive_expect_tx(fb, kTileBytes);
+                tma_load_3d_plain(dst, map, fb, 0, j * kTile, g);
+                tma_load_3d_plain(dst + kHalfBytes, map, fb, 64, j * kTile, g);
+                ++pos;
+                return true;
+            };
+            while (ok && walk.next(seg)) {
+                const int4 it = __ldcg(p.items + seg.item);
+                const int n = seg.j1 - seg.j0;
+                if (it.z > kTile) {
+                    for (int j = 0; ok && j < n; ++j)
+                        ok = copy(&tmK, it.x, seg.j0 + j) && copy(&tmV, it.x, seg.j0 + j);
+                } else {
+                    ok = copy(&tmK, it.x, seg.j0);
+                    for (int j = 0; ok && j < n; ++j)
+                        ok = (j + 1 >= n || copy(&tmK, it.x, seg.j0 + j + 1)) && copy(&tmV, it.x, seg.j0 + j);
+                }
+            }
+            // Copies in flight land before the CTA can leave.
+            volatile int never = 0;
+            if (!ok)
+                for (uint32_t i = pos > kStages ? pos - kStages : 0; i < pos; ++i)
+                    (void)wait_bar(full0 + 8 * (i % kStages), (i / kStages) & 1, &never);
+        } else if (warp == kMmaWarp && lane == 0) {
+            // -------------------------------------------------------------- MMAs
+            constexpr uint32_t kIdescS = bf16_idesc(kTile, kTile, false), kIdescO = bf16_idesc(kTile, kHeadDim, true);
+            uint32_t base = 0, nseg = 0; // copies of earlier segments; segments
+            uint32_t np[2] = {0, 0};     // P tiles consumed by each stream
+            auto ring = [&](uint32_t at) { return smem_u32(smem + kOffRing + (at % kStages) * kTileBytes); };
+            auto full = [&](uint32_t at) { return wait_bar(full0 + 8 * (at % kStages), (at / kStages) & 1, abort_flag); };
+            while (ok && walk.next(seg)) {
+                const int4 it = __ldcg(p.items + seg.item);
+                const Streams st{it.z > kTile, seg.j1 - seg.j0};
+                if (!(ok = wait_bar(q_full, nseg & 1, abort_flag)))
+                    break;
+                tc_fence_after();
+                // S of stream s, step t
+                auto logits = [&](int s, int t) -> bool {
+                    const uint32_t at = base + st.key_at(st.tile(s, t));
+                    if (!full(at))
+                        return false;
+                    const uint64_t a = smem_desc_sw128(smem_u32(smem + kOffQ + (st.two ? s : 0) * kTileBytes), 16, 1024);
+                    const uint64_t b = smem_desc_sw128(ring(at), 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) { // 16 of the 128 dimensions each
+                        const uint64_t off = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+                        mma_ss(tmem + s * 128, a + off, b + off, kIdescS, k > 0);
+                    }
+                    mma_commit(s_full + 8 * s);
+                    if (!st.two || s == 1)
+                        mma_commit(empty0 + 8 * (at % kStages));
+                    return true;
+                };
+                // O of stream s += P V, step t
+                auto output = [&](int s, int t) -> bool {
+                    const uint32_t at = base + st.value_at(st.tile(s, t));
+                    if (!full(at) || !wait_bar(p_full + 8 * s, np[s] & 1, abort_flag))
+                        return false;
+                    ++np[s];
+                    tc_fence_after();
+                    const uint64_t b = smem_desc_sw128(ring(at), kHalfBytes, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) // 16 positions each
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, b + k * (2048 >> 4), kIdescO, t > 0 || k > 0);
+                    if (!st.two || s == 1)
+                        mma_commit(empty0 + 8 * (at % kStages));
+                    if (t + 1 == st.steps(s))
+                        mma_commit(o_full + 8 * s);
+                    return true;
+                };
+                ok = logits(0, 0) && (st.steps(1) == 0 || logits(1, 0));
+                for (int t = 0; ok && t < st.steps(0); ++t) {
+                    ok = output(0, t) && (t + 1 >= st.steps(0) || logits(0, t + 1));
+                    if (ok && t < st.steps(1))
+                        ok = output(1, t) && (t + 1 >= st.steps(1) || logits(1, t + 1));
+                }
+                base += 2 * (uint32_t)st.n;
+                ++nseg;
+            }
+            if (!ok) { // MMAs in flight finish before TMEM is given back
+                volatile int never = 0;
+                mma_commit(smem_u32(&sh->drain));
+                (void)wait_bar(smem_u32(&sh->drain), 0, &never);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        regs_inc<224>();
+        const int s = warp >> 2, row = tid & (kTile - 1); // stream, row of its tile
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21; // this warp's TMEM lanes
+        const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
+        uint32_t ns = 0, no = 0, nseg = 0; // S tiles, O results and segments consumed
+        while (walk.next(seg)) {
+            const int4 it = __ldcg(p.items + seg.item);
+            const Streams st{it.z > kTile, seg.j1 - seg.j0};
+            // Every earlier MMA that read Q is complete (both groups have met below).
+            const int qrow = (st.two ? s * kTile : 0) + row; // row of the item
+            if (st.two || s == 0) {
+                uint4 *dst = reinterpret_cast<uint4 *>(smem + kOffQ + s * kTileBytes);
+                const uint4 *src = nullptr;
+                if (qrow < it.z) {
+                    const int r = it.y + qrow, a = r / p.M;
+                    const int b = __ldcg(p.list + (size_t)it.x * p.B + a);
+                    src = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.Hq + (size_t)it.x * p.M + (r - a * p.M)) *
+                                                                    kHeadDim);
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 x = src ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    dst[(c >> 3) * (kHalfBytes / 16) + row * 8 + ((c & 7) ^ (row & 7))] = x;
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(q_full);
+
+            float m = -INFINITY, l = 0.f; // m in the logits' units
+            const int steps = st.steps(s);
+            for (int t = 0; t < steps; ++t) {
+                if (!__all_sync(kFull, wait_bar(s_full + 8 * s, ns & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(x[c], tS + 32 * c);
+                tmem_wait_ld();
+                const int left = p.prefix_len - (seg.j0 + st.tile(s, t)) * kTile;
+                if (left < kTile) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i >= left)
+                                x[c][i] = 0xff800000u; // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                    for (int i = 1; i < 32; ++i)
+                        mx[c] = fmaxf(mx[c], __uint_as_float(x[c][i]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (t == 0) {
+                    m = top;
+                } else if (__any_sync(kFull, (top - m) * kScaleLog2 > kGrowth)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = exp2_approx((m - mn) * kScaleLog2);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o, tO + 32 * c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tO + 32 * c, o);
+                    }
+                }
+                const float sub = m * kScaleLog2;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t(&src)[32] = x[2 * h + (i >> 4)];
+                        const float a = exp2_approx(fmaf(__uint_as_float(src[(2 * i) & 31]), kScaleLog2, -sub));
+                        const float b = exp2_approx(fmaf(__uint_as_float(src[(2 * i + 1) & 31]), kScaleLog2, -sub));
+                        sum[i & 1] += a;
+                        sum[2 + (i & 1)] += b;
+                        w[i] = pack_bf16x2(a, b);
+                    }
+                    tmem_st32(tS + 32 * h, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + 8 * s);
+            }
+            if (!ok)
+                break;
+            // ---- the segment's partial of this row
+            const size_t slot = (size_t)blockIdx.x + seg.item;
+            const size_t part = (slot * 2 + s) * p.row_cap;
+            const bool mine = qrow < it.z;
+            if (steps > 0) {
+                if (!__all_sync(kFull, wait_bar(o_full + 8 * s, no & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                ++no;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o, tO + 32 * c);
+                    tmem_wait_ld();
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) // eight elements a row and block of 16
+                            __stcg(reinterpret_cast<float4 *>(p.o + part * kHeadDim +
+                                                              ((size_t)(4 * c + (i >> 1)) * p.row_cap + row) * 8 + (i & 1) * 4),
+                                   make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
+                    }
+                }
+            }
+            if (mine)
+                __stcg(p.ml + part + row, make_float2(m * kScaleLog2, l));
+            // Both groups are done with the segment's Q, S and O.
+            mbar_arrive(seg_done);
+            if (!__all_sync(kFull, wait_bar(seg_done, nseg & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            ++nseg;
+        }
+    }
+    if (!ok && lane == 0)
+        atomicOr(p.err, SR_DEVERR_TIMEOUT);
+    __syncthreads();
+    __syncwarp();
+    if (warp == kMmaWarp)
+        tmem_dealloc(tmem, 512);
+}
+
+// ---- join -------------------------------------------------------------------------------
+
+constexpr int kJoinWarps = 8;
+
+// One warp a query head; lane c owns elements 4c .. 4c + 3.
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); // b * Hq + h
+    if (row >= (long long)p.B * p.Hq)
+        return;
+    const int b = (int)(row / p.Hq), h = (int)(row - (long long)b * p.Hq), g = h / p.M;
+    const size_t u = (size_t)b * p.Hkv + g;
+    const int rank = __ldcg(p.rank + u);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lse = __int_as_float(0x7fc00000); // sink heads
+    if (rank < 0) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v0 + u * kHeadDim) + lane);
+        acc = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                          __uint_as_float(v.y & 0xffff0000u));
+    } else {
+        float m = -INFINITY, l = 0.f;
+        const int nt = (p.prefix_len + kTile - 1) / kTile;
+        if (nt > 0) {
+            const int r = rank * p.M + (h - g * p.M);
+            const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
+            const bool two = __ldcg(p.count + g) * p.M - (r - ir) > kTile;
+            const long long share = share_of((long long)__ldcg(p.n_items) * nt, p.grid);
+            const int c0 = (int)((long long)item * nt / share);
+            const int c1 = (int)(((long long)(item + 1) * nt - 1) / share);
+            // Partials k: of CTA c0 + k, or of its two streams
+            const int n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
+            auto part = [&](int k) -> size_t {
+                const size_t slot = (size_t)(c0 + (two ? k : k >> 1)) + item;
+                return (slot * 2 + (two ? ir / kTile : k & 1)) * p.row_cap;
+            };
+            const int pr = ir % kTile;
+            for (int k0 = 0; k0 < n; k0 += 32) {
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (k0 + lane < n)
+                    ml = __ldcg(p.ml + part(k0 + lane) + pr);
+                float mb = ml.y == 0.f ? -INFINITY : ml.x; // a stream without a tile has l = 0
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o));
+                const float mn = fmaxf(m, mb);
+                const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - mn);
+                float ls = ml.y * w;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    ls += __shfl_xor_sync(kFull, ls, o);
+                l = l * keep + ls;
+                acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+                const int nb = min(32, n - k0);
+#pragma unroll 8
+                for (int k = 0; k < nb; ++k) {
+                    const float wk = __shfl_sync(kFull, w, k);
+                    if (wk != 0.f) { // its O was written
+                        const float4 o = __ldcg(reinterpret_cast<const float4 *>(
+                            p.o + part(k0 + k) * kHeadDim + ((size_t)(lane >> 1) * p.row_cap + pr) * 8 + (lane & 1) * 4));
+                        acc.x = fmaf(o.x, wk, acc.x);
+                        acc.y = fmaf(o.y, wk, acc.y);
+                        acc.z = fmaf(o.z, wk, acc.z);
+                        acc.w = fmaf(o.w, wk, acc.w);
+                    }
+                }
+                m = mn;
+            }
+        }
+        // acc and l are in units of 2^m; join the suffix's normalised part
+        lse = nt > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+        float wp = nt > 0 ? 1.f / l : 0.f, ws = 0.f;
+        float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.o_suffix) {
+            const float ls = __ldg(p.lse_suffix + row), top = fmaxf(lse, ls);
+            if (ls != -INFINITY) {
+                os = __ldg(reinterpret_cast<const float4 *>(p.o_suffix + (size_t)row * kHeadDim) + lane);
+                const float ep = expf(lse - top), es = expf(ls - top), tot = ep + es;
+                wp *= ep / tot;
+                ws = es / tot;
+                lse = top + logf(tot);
+            }
+        }
+        acc.x = acc.x * wp + os.x * ws;
+        acc.y = acc.y * wp + os.y * ws;
+        acc.z = acc.z * wp + os.z * ws;
+        acc.w = acc.w * wp + os.w * ws;
+    }
+    if (p.lse && lane == 0)
+        p.lse[row] = lse;
+    if (p.out_f32)
+        reinterpret_cast<float4 *>(p.out_f32 + (size_t)row * kHeadDim)[lane] = acc;
+    else
+        reinterpret_cast<uint2 *>(p.out + (size_t)row * kHeadDim)[lane] =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// ---- host side ------------------------------------------------------------------------
+
+cudaError_t grid_of(int *grid)
+{
+    static std::mutex mu;
+    static int known[64]; // 0: not configured
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!known[dev]) {
+        int sms = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        known[dev] = sms < kGridCap ? sms : kGridCap;
+    }
+    *grid = known[dev];
+    return cudaSuccess;
+}
+
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                   const Args &...args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.batch * a.n_q_heads));
-    cfg.blockDim = dim3(kHeadDim);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_rows_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+} // namespace
+
+size_t prefix_workspace_bytes(int batch, int n_q_heads, int n_kv_heads)
+{
+    return layout(batch, n_q_heads, n_kv_heads).total;
+}
+
+cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
+{
+    Params p;
+    cudaError_t e = grid_of(&p.grid);
+    if (e != cudaSuccess)
+        return e;
+    const Layout w = layout(a.batch, a.n_q_heads, a.n_kv_heads);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    p.q = static_cast<const __nv_bfloat16 *>(a.q);
+    p.v0 = static_cast<const __nv_bfloat16 *>(a.v0);
+    p.mask = a.mask;
+    p.err = reinterpret_cast<int32_t *>(ws);
+    p.n_items = p.err + 1;
+    p.count = reinterpret_cast<int32_t *>(ws + w.count);
+    p.first = reinterpret_cast<int32_t *>(ws + w.first);
+    p.list = reinterpret_cast<int32_t *>(ws + w.list);
+    p.rank = reinterpret_cast<int32_t *>(ws + w.rank);
+    p.items = reinterpret_cast<int4 *>(ws + w.items);
+    p.ml = reinterpret_cast<float2 *>(ws + w.ml);
+    p.o = reinterpret_cast<float *>(ws + w.o);
+    p.o_suffix = a.o_suffix;
+    p.lse_suffix = a.lse_suffix;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.out_f32 = a.out_f32;
+    p.lse = a.lse;
+    p.B = a.batch;
+    p.Hq = a.n_q_heads;
+    p.Hkv = a.n_kv_heads;
+    p.M = a.n_q_heads / a.n_kv_heads;
+    p.prefix_len = a.prefix_len;
+    p.row_cap = w.row_cap;
+
+    e = launch(plan_kernel, 1, kPlanThreads, 0, stream, p);
+    if (e == cudaSuccess && a.prefix_len > 0) {
+        CUtensorMap tmK, tmV;
+        if (!make_cache_map(&tmK, a.k_prefix, a.n_kv_heads, a.max_seq_len, kTile, false, a.prefix_len) ||
+            !make_cache_map(&tmV, a.v_prefix, a.n_kv_heads, a.max_seq_len, kTile, false, a.prefix_len))
+            return cudaErrorInvalidValue;
+        e = launch(scan_kernel, (unsigned)p.grid, kThreads, kSmem, stream, tmK, tmV, p);
+    }
+    if (e == cudaSuccess) {
+        const long long rows = (long long)a.batch * a.n_q_heads;
+        e = launch(join_kernel, (unsigned)((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream, p);
+    }
+    return e;
 }
 
 } // namespace sr
