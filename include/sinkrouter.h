@@ -90,8 +90,8 @@ typedef enum sr_status {
  *   active_list out int32 [1 + B*Hkv]: [0] = number of active units n, then
  *               their flat indices in ascending order; entries past 1+n are
  *               left untouched
- * One launch; no workspace. Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED,
- * SR_ERR_CUDA.
+ * One launch, two for more than 192 query rows; no workspace. Errors: SR_ERR_INVALID_ARG,
+ * SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
  */
 sr_status sr_route(const sr_dims *dims, const void *q, const void *k0, float tau,
                    uint8_t *route_mask, int32_t *active_list, void *stream);
@@ -132,10 +132,10 @@ sr_status sr_route(const sr_dims *dims, const void *q, const void *k0, float tau
  *               max_pos)) -- its cache, k0/v0 and length are left untouched,
  *               its q_out rows are zero and its groups are routed from those
  *               rows (so the mask still equals sr_route(q_out, k0, tau))
- * One launch of one CTA; no workspace. It waits for the preceding kernel in the
- * stream before reading anything and lets the next one (sr_decode_attention,
- * which reads all of its inputs after its own wait) launch early. Errors:
- * SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
+ * One launch of a cluster of CTAs, or two launches for many units; no workspace.
+ * It waits for the preceding kernel in the stream before reading anything and lets
+ * the next one (sr_decode_attention, which reads all of its inputs after its own
+ * wait) launch early. Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
  */
 sr_status sr_rope_append_route(const sr_dims *dims, const void *q_in, const void *k_new,
                                const void *v_new, const float *rope_cos, const float *rope_sin,
@@ -442,7 +442,7 @@ sr_status sr_kv_dequant(const sr_dims *dims, int32_t kv_type, int32_t n_rows, co
  *   seq_lens    int32 [B]: the slot to write
  *   seq_lens_out out int32 [B]: seq_lens[b] + 1, or seq_lens[b] where nothing was
  *               appended; may be seq_lens itself
- * One launch. Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
+ * Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
  */
 sr_status sr_rope_append_route_kv(const sr_dims *dims, int32_t kv_type, int32_t pos_offset, const void *q_in,
                                   const void *k_new, const void *v_new, const float *rope_cos,

@@ -11,6 +11,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,18 +33,24 @@ def nvcc() -> str:
 
 def build(output: str = LIBRARY, defines=(), verbose_ptxas: bool = False, quiet: bool = True) -> str:
     """Compile every source into ``output`` (a shared library) and return its path."""
-    flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
-             "--cudart", "static", f"-I{INCLUDE}", f"-I{CSRC}", *[f"-D{d}" for d in defines]]
+    flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}", f"-I{CSRC}",
+             *[f"-D{d}" for d in defines]]
     if verbose_ptxas:
         flags += ["-Xptxas", "-v"]
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+        return r.stdout + r.stderr
+
     tmp = output + ".tmp"
-    cmd = [nvcc(), *flags, *srcs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(len(SOURCES)) as pool:
+        objs = [os.path.join(objects, s + ".o") for s in SOURCES]  # one compiler a source, side by side
+        said = list(pool.map(run, [[nvcc(), *flags, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]))
+        said.append(run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "--cudart", "static", *objs, "-o", tmp]))
     if not quiet or verbose_ptxas:
-        sys.stderr.write(r.stdout + r.stderr)
+        sys.stderr.write("".join(said))
     os.replace(tmp, output)
     return output
 

@@ -82,10 +82,10 @@
 
 // 8-bit caches: row blocks of 16 per consumer warp and tile, stages, consumer warps.
 #ifndef SR_QUANT_RB
-#define SR_QUANT_RB 1
+#define SR_QUANT_RB 2
 #endif
 #ifndef SR_QUANT_STAGES
-#define SR_QUANT_STAGES 4
+#define SR_QUANT_STAGES 2
 #endif
 #ifndef SR_QUANT_CW
 #define SR_QUANT_CW 8
@@ -1331,7 +1331,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             // Partial of the split, one float4 column per thread: the warps'
             // states weighted by 2^(m_w - max_w m_w) (0 for a warp that saw no
             // row of this split).
+            // A split that is its whole unit needs no partial: its state is the
+            // merge's result, bit for bit (the only weight is 2^0).
             float *po = p.part_o + (size_t)h.slot * M * kHeadDim;
+            const bool whole = h.nseg == 1;
             for (int idx = ctid; idx < M * 32; idx += 32 * kCWarps) {
                 const int head = idx >> 5, d4 = (idx & 31) * 4;
                 float2 ml[kCWarps];
@@ -1354,6 +1357,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                     acc.w = fmaf(x.w, f, acc.w);
                     Lh = fmaf(ml[ww].y, f, Lh);
                 }
+                if (whole) {
+                    const int b = h.unit / p.Hkv, gg = h.unit - b * p.Hkv;
+                    if (p.lse && d4 == 0)
+                        p.lse[(size_t)b * p.Hq + (size_t)gg * M + head] = (Mh + log2f(Lh)) * kLn2;
+                    store_out(b, gg, head, d4, acc, 1.f / Lh);
+                    continue;
+                }
                 __stcg(reinterpret_cast<float4 *>(po + head * kHeadDim + d4), acc);
                 if (d4 == 0)
                     __stcg(p.part_ml + (size_t)h.slot * M + head, make_float2(Mh, Lh));
@@ -1370,6 +1380,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             // loads. No separate fences.
             if (!(ok = cbar_sync()))
                 break;
+            if (whole) {
+                if (++stage == STAGES) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+                continue;
+            }
             if (ctid == 0)
                 SR_STAMP(tl_decode, 8);
             if (ctid == 0)
@@ -1516,8 +1533,12 @@ DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
 using DecodeCfg = Cfg<SR_DECODE_RB, SR_DECODE_STAGES, 4, SR_KV_BF16>;
-// 8-bit caches: eight consumer warps of one row block each, the same 128 rows a
-// tile, in four 32 KB stages.
+// 8-bit caches: eight consumer warps of two row blocks each, 256 rows in two 64 KB
+// stages. Measured back to back (128K with 4 of 8 groups active; four 64K..128K
+// sequences, M = 8): 29.0 and 101.6 us; 128 rows in four 32 KB stages take 31.9 and
+// 122.9 with eight warps, 31.2 and 129.3 with four; 256 rows on four warps 28.3 and
+// 104.5; 64 rows in eight stages 42.6 and 168.6. What a tile costs beside its bytes
+// (barriers, maxima, the scales' copy) is paid half as often.
 template <int KV> using QuantCfg = Cfg<SR_QUANT_RB, SR_QUANT_STAGES, SR_QUANT_CW, KV>;
 
 // One kernel of the family: its launch shape.

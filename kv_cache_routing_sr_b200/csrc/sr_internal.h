@@ -128,7 +128,18 @@ struct PrefixArgs {
     int batch, n_q_heads, n_kv_heads, max_seq_len, prefix_len;
 };
 
+// Active list of a mask; with seq_lens, also the append step's length update.
+struct CompactArgs {
+    const uint8_t *mask;
+    int32_t *active;
+    int units;
+    const int32_t *seq_lens;
+    int32_t *seq_lens_out;
+    int batch, max_seq_len, max_pos, pos_offset;
+};
+
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream);
 cudaError_t launch_rope_append_route(const PrestepArgs &a, cudaStream_t stream);
 // Self-test of the bounded wait (sr_selftest_bounded_wait).
 cudaError_t launch_bounded_wait_selftest(int32_t limit_us, int32_t *status, unsigned long long *waited_ns,

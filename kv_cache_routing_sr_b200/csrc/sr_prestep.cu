@@ -25,9 +25,11 @@
 // correctly rounded bf16 rotation first and is quantised from that, by the
 // eight lanes that hold it, so the position-0 key is the bf16 row in either case.
 //
-// Layout: one CTA of 512 threads, or a cluster of eight with a share of the
-// units each, walking its units in chunks whose rows fit in
-// shared memory. Per chunk, in one pass where each thread takes its own item:
+// Layout: a cluster of eight CTAs of 512 threads with a share of the units each,
+// whose sink flags go to CTA 0's shared memory for the compaction; launches of
+// more than kClusterItems items a CTA use as many CTAs as give every item a
+// thread, and the routing kernel's compaction launch, which then also advances the
+// lengths. Per CTA, in one pass where each thread takes its own item:
 // eight threads per new key rotate it (each takes 8 elements and their 8
 // partners), write the cache slot, and stage the group's position-0 key (the
 // captured one at slot 0, else the stored k0); eight threads per query row
@@ -35,7 +37,6 @@
 // routine (one warp per GQA group), so the decision equals sr_route on
 // (q_out, k0) bit for bit. Lengths advance after every read of
 // them; the compaction is the routing kernel's.
-#include <atomic>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,11 +53,15 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowBudget = 160 * 1024; // shared bytes for staged q / k0 rows
 constexpr int kClusterCtas = 8;
-constexpr int kOneCtaUnits = 16; // launches of at most this many units use one CTA
-
-template <int M> __host__ __device__ constexpr int chunk_units() { return kRowBudget / ((M + 1) * 256); }
+// Items (eight per query row and per new key) of one of eight CTAs, 512 threads:
+// beyond this, one chunk of 512 items a CTA and a second launch. Measured back to
+// back, cluster of eight against two launches: 3.7 us against 6.5 at 32 units (M =
+// 4), 6.0 / 6.6 at 128, 8.3 / 6.6 at 256, 25.9 / 6.8 at 1024; M = 8: 6.1 / 7.7 at 64
+// units, 8.1 / 7.8 at 128; M = 1: 5.0 / 6.5 at 256, 7.3 / 6.6 at 512. Fewer CTAs than
+// eight are no faster where they would give every item a thread (32 units, M = 1: 4.6
+// us on one, 3.3 on eight): the fp64 rotations spread over more SMs.
+constexpr int kClusterItems = 768;
 
 struct PrestepParams {
     const __nv_bfloat16 *q_in, *k_new, *v_new;
@@ -159,24 +164,23 @@ __device__ __forceinline__ void load_table8(const float *tab, int pos, int j, fl
     v[1] = __ldg(t + 1);
 }
 
-template <int M, int KV, bool CLUSTER>
+template <int M, int KV, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepParams p, int cu)
 {
-    extern __shared__ __align__(128) uint8_t dsm[]; // [cu*(M+1)*256 staged rows][B*Hkv sink flags]
+    extern __shared__ __align__(128) uint8_t dsm[]; // [cu*(M+1)*256 staged rows][cluster: B*Hkv sink flags]
     __shared__ int32_t warp_cnt[kWarps];
     __shared__ int32_t warp_off[kWarps + 1];
 
     const int U = p.B * p.Hkv;
-    // This CTA's units [ub, ue): all of them, or its share of the cluster's.
-    const int per = CLUSTER ? (U + kClusterCtas - 1) / kClusterCtas : U;
-    const int ub = CLUSTER ? min((int)blockIdx.x * per, U) : 0;
-    const int ue = CLUSTER ? min(ub + per, U) : U;
+    // This CTA's units
+    const int u0 = min((int)blockIdx.x * cu, U);
+    const int nu = min(cu, U - u0);
     uint4 *rows = reinterpret_cast<uint4 *>(dsm);
     uint8_t *sink_flag = dsm + (size_t)cu * (M + 1) * 256;
     uint8_t *all_flags = sink_flag; // CTA 0's, which compacts the active list
-    if constexpr (CLUSTER) {
+    if constexpr (!WIDE) {
         all_flags = cooperative_groups::this_cluster().map_shared_rank(sink_flag, 0);
-        cooperative_groups::this_cluster().sync(); // CTA 0 runs: its shared memory may be written
+        cooperative_groups::this_cluster().barrier_arrive();
     }
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
@@ -187,9 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // Query row item `it` of the chunk starting at unit u0: rotate into q_out and
-    // the staged rows; a sequence with no valid slot gets a zero query.
-    auto query_item = [&](int it, int u0) {
+    // Query row item `it`: rotate into q_out and the staged rows; a sequence with no
+    // valid slot gets a zero query.
+    auto query_item = [&](int it) {
         const int r = it >> 3, j = it & 7;
         const int u = u0 + r / M;
         const size_t row = ((size_t)u0 * M + r) * kHeadDim;
@@ -213,100 +217,86 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     };
 
     bool bad_slot = false;
-    for (int u0 = ub; u0 < ue; u0 += cu) {
-        const int nu = (ue - u0) < cu ? (ue - u0) : cu;
-        uint4 *krows = rows + (size_t)nu * M * 16;
-        // One pass over the chunk's items, each thread on its own item (at the
-        // 8B shape every item has a thread), so that no thread takes a key and
-        // a query row one after the other: items [0, nu*8) are the new keys,
-        // the rest the query rows.
-        for (int it = threadIdx.x; it < nu * 8 + nu * M * 8; it += kThreads) {
-            if (it >= nu * 8) {
-                query_item(it - nu * 8, u0);
-                continue;
-            }
-            // New key: rotate, append, capture or stage k0. New value: append.
-            const int lu = it >> 3, j = it & 7;
-            const int u = u0 + lu;
-            // The new key and value do not depend on the slot: load them in the
-            // same round trip as the slot itself.
-            const uint4 *kn = reinterpret_cast<const uint4 *>(p.k_new + (size_t)u * kHeadDim);
-            const uint4 *vn = reinterpret_cast<const uint4 *>(p.v_new + (size_t)u * kHeadDim);
-            const uint4 klo = __ldg(kn + j), khi = __ldg(kn + j + 8);
-            const uint4 vlo = __ldg(vn + j), vhi = __ldg(vn + j + 8);
-            const int pos = slot_of(p, u / p.Hkv);
-            uint4 *ks = krows + lu * 16;
-            uint4 *k0g = reinterpret_cast<uint4 *>(p.k0 + (size_t)u * kHeadDim);
-            if (pos < 0) {
-                bad_slot = true;
-                ks[j] = k0g[j];
-                ks[j + 8] = k0g[j + 8];
-                continue;
-            }
-            float4 c[2], s[2];
-            load_table8(p.rope_cos, pos + p.pos_offset, j, c);
-            load_table8(p.rope_sin, pos + p.pos_offset, j, s);
-            uint4 lo, hi;
-            rope8(klo, khi, c, s, lo, hi);
-            const size_t slot = (size_t)u * p.Lmax + pos;
-            const float sk = store_row<KV>(p.k_cache, slot, j, lo, hi);
-            const float sv = store_row<KV>(p.v_cache, slot, j, vlo, vhi);
-            if (KV != SR_KV_BF16 && j == 0)
-                p.scales[slot] = make_float2(sk, sv);
-            if (pos + p.pos_offset == 0) {
-                uint4 *v0g = reinterpret_cast<uint4 *>(p.v0 + (size_t)u * kHeadDim);
-                k0g[j] = lo;
-                k0g[j + 8] = hi;
-                v0g[j] = vlo;
-                v0g[j + 8] = vhi;
-                ks[j] = lo;
-                ks[j + 8] = hi;
-            } else {
-                ks[j] = k0g[j];
-                ks[j + 8] = k0g[j + 8];
-            }
+    uint4 *krows = rows + (size_t)nu * M * 16;
+    // One pass over the items, each thread on its own item (at the 8B shape every
+    // item has a thread), so that no thread takes a key and a query row one after
+    // the other: items [0, nu*8) are the new keys, the rest the query rows.
+    for (int it = threadIdx.x; it < nu * 8 + nu * M * 8; it += kThreads) {
+        if (it >= nu * 8) {
+            query_item(it - nu * 8);
+            continue;
         }
-        __syncthreads();
-        route_units_warp<M, false>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
-            all_flags[u0 + lu] = sink ? 1 : 0;
-            p.mask[u0 + lu] = sink ? 1 : 0;
-        });
-        __syncthreads(); // the rows are overwritten by the next chunk
+        // New key: rotate, append, capture or stage k0. New value: append.
+        const int lu = it >> 3, j = it & 7;
+        const int u = u0 + lu;
+        // The new key and value do not depend on the slot: load them in the
+        // same round trip as the slot itself.
+        const uint4 *kn = reinterpret_cast<const uint4 *>(p.k_new + (size_t)u * kHeadDim);
+        const uint4 *vn = reinterpret_cast<const uint4 *>(p.v_new + (size_t)u * kHeadDim);
+        const uint4 klo = __ldg(kn + j), khi = __ldg(kn + j + 8);
+        const uint4 vlo = __ldg(vn + j), vhi = __ldg(vn + j + 8);
+        const int pos = slot_of(p, u / p.Hkv);
+        uint4 *ks = krows + lu * 16;
+        uint4 *k0g = reinterpret_cast<uint4 *>(p.k0 + (size_t)u * kHeadDim);
+        if (pos < 0) {
+            bad_slot = true;
+            ks[j] = k0g[j];
+            ks[j + 8] = k0g[j + 8];
+            continue;
+        }
+        float4 c[2], s[2];
+        load_table8(p.rope_cos, pos + p.pos_offset, j, c);
+        load_table8(p.rope_sin, pos + p.pos_offset, j, s);
+        uint4 lo, hi;
+        rope8(klo, khi, c, s, lo, hi);
+        const size_t slot = (size_t)u * p.Lmax + pos;
+        const float sk = store_row<KV>(p.k_cache, slot, j, lo, hi);
+        const float sv = store_row<KV>(p.v_cache, slot, j, vlo, vhi);
+        if (KV != SR_KV_BF16 && j == 0)
+            p.scales[slot] = make_float2(sk, sv);
+        if (pos + p.pos_offset == 0) {
+            uint4 *v0g = reinterpret_cast<uint4 *>(p.v0 + (size_t)u * kHeadDim);
+            k0g[j] = lo;
+            k0g[j + 8] = hi;
+            v0g[j] = vlo;
+            v0g[j + 8] = vhi;
+            ks[j] = lo;
+            ks[j + 8] = hi;
+        } else {
+            ks[j] = k0g[j];
+            ks[j + 8] = k0g[j + 8];
+        }
     }
+    __syncthreads();
+    if constexpr (!WIDE)
+        cooperative_groups::this_cluster().barrier_wait(); // CTA 0 runs: its shared memory may be written
+    route_units_warp<M, false>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
+        if constexpr (!WIDE)
+            all_flags[u0 + lu] = sink ? 1 : 0;
+        p.mask[u0 + lu] = sink ? 1 : 0;
+    });
+    __syncthreads(); // every read of the lengths is done
 
     if (p.error && __syncthreads_or(bad_slot) && threadIdx.x == 0)
         atomicOr(p.error, SR_DEVERR_APPEND_SLOT);
-    if constexpr (CLUSTER) {
-        cooperative_groups::this_cluster().sync();
-        if (blockIdx.x != 0)
-            return;
-    }
+    if constexpr (WIDE)
+        return;
+    cooperative_groups::this_cluster().sync();
+    if (blockIdx.x != 0)
+        return;
     // Every other read of seq_lens, and every flag, is behind the barriers above.
     for (int b = threadIdx.x; b < p.B; b += kThreads)
         p.seq_lens_out[b] = p.seq_lens[b] + (slot_of(p, b) >= 0 ? 1 : 0);
     compact_active<kThreads>(sink_flag, U, p.active, warp_cnt, warp_off);
 }
 
-template <int M, int KV, bool CLUSTER>
+template <int M, int KV, bool WIDE>
 cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
 {
     const int U = a.batch * a.n_kv_heads;
-    const int per = CLUSTER ? (U + kClusterCtas - 1) / kClusterCtas : U;
-    const int cu = per < chunk_units<M>() ? per : chunk_units<M>();
-    const size_t smem = (size_t)cu * (M + 1) * 256 + (size_t)U;
-    static std::atomic<bool> configured[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-        e = cudaFuncSetAttribute(rope_append_route_kernel<M, KV, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)((size_t)chunk_units<M>() * (M + 1) * 256 + SR_MAX_UNITS));
-        if (e != cudaSuccess)
-            return e;
-        if (dev >= 0 && dev < 64)
-            configured[dev].store(true);
-    }
+    // Units a CTA. Wide: one thread an item (8 a row, M + 1 rows a unit).
+    const int cu = WIDE ? kThreads / (8 * (M + 1)) : (U + kClusterCtas - 1) / kClusterCtas;
+    const size_t smem = (size_t)cu * (M + 1) * 256 + (WIDE ? 0 : (size_t)U);
     PrestepParams p;
     p.q_in = static_cast<const __nv_bfloat16 *>(a.q_in);
     p.k_new = static_cast<const __nv_bfloat16 *>(a.k_new);
@@ -332,7 +322,7 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     p.pos_offset = a.pos_offset;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CLUSTER ? kClusterCtas : 1);
+    cfg.gridDim = dim3(WIDE ? (unsigned)((U + cu - 1) / cu) : (unsigned)kClusterCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -344,13 +334,28 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CLUSTER ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M, KV, CLUSTER>, p, cu);
+    cfg.numAttrs = WIDE ? 1 : 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M, KV, WIDE>, p, cu);
+    if (e != cudaSuccess || !WIDE)
+        return e;
+    CompactArgs c{};
+    c.mask = a.mask;
+    c.active = a.active;
+    c.units = U;
+    c.seq_lens = a.seq_lens;
+    c.seq_lens_out = a.seq_lens_out;
+    c.batch = a.batch;
+    c.max_seq_len = a.max_seq_len;
+    c.max_pos = a.max_pos;
+    c.pos_offset = a.pos_offset;
+    return launch_compact(c, stream);
 }
 
 template <int M, int KV> cudaError_t launch_kv(const PrestepArgs &a, cudaStream_t stream)
 {
-    return a.batch * a.n_kv_heads > kOneCtaUnits ? launch_m<M, KV, true>(a, stream) : launch_m<M, KV, false>(a, stream);
+    const int cluster_units = (a.batch * a.n_kv_heads + kClusterCtas - 1) / kClusterCtas;
+    return cluster_units * 8 * (M + 1) > kClusterItems ? launch_m<M, KV, true>(a, stream)
+                                                       : launch_m<M, KV, false>(a, stream);
 }
 
 template <int M> cudaError_t launch_group(const PrestepArgs &a, cudaStream_t stream)

@@ -146,6 +146,9 @@ def _on_tensor_device(fn):
     must be that device's."""
     @functools.wraps(fn)
     def wrapper(t, *args, **kwargs):
+        d = t.get_device()  # -1 for a CPU tensor, which the context below refuses
+        if d >= 0 and d == torch.cuda.current_device():
+            return fn(t, *args, **kwargs)
         with torch.cuda.device(t.device):
             return fn(t, *args, **kwargs)
     return wrapper
@@ -156,9 +159,14 @@ def _check(fn: str, status: int):
         raise SinkRouterError(fn, status, load())
 
 
+# The current stream's handle without a Stream object around it (0.1 us in place
+# of 3 us, a sixth of a short call); a torch that lacks it takes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream=None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(stream.cuda_stream if stream is not None else _raw_stream(torch.cuda.current_device()))
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
@@ -171,33 +179,29 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     return t.data_ptr()
 
 
-def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype) -> int | None:
-    return None if t is None else _dev(t, name, dtype)
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """Pointer of a contiguous CUDA tensor of exactly this dtype, shape and device:
+    the library sees pointers only, and would read another size out of bounds."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} must have shape {tuple(shape)} on cuda:{device}, got {tuple(t.shape)} on {t.device}")
 
 
-def _shape(t: torch.Tensor, name: str, shape, device) -> None:
-    """The library sees pointers only: a tensor of another size or device would
-    be read out of bounds."""
-    if t is not None and (t.shape != shape or t.device != device):
-        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int | None:
+    return None if t is None else _arg(t, name, dtype, shape, device)
 
 
-def _kv_type(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales, quant_only: bool = True) -> int:
-    """sr_kv_type of a cache [B, Hkv, Lmax, 128] after checking its parts against each other."""
+def _kv_type(k_cache: torch.Tensor, kv_scales, quant_only: bool = True) -> int:
+    """sr_kv_type of a cache [B, Hkv, Lmax, 128], and whether scales belong to it."""
     kv = KV_TYPES.get(k_cache.dtype)
     if kv is None or (quant_only and kv == SR_KV_BF16):
         raise ValueError(f"k_cache must be float8_e4m3fn or int8{'' if quant_only else ' or bfloat16'}, "
                          f"got {k_cache.dtype}")
     if k_cache.dim() != 4 or k_cache.shape[3] != HEAD_DIM:
         raise ValueError(f"k_cache must be [B, Hkv, Lmax, {HEAD_DIM}], got {tuple(k_cache.shape)}")
-    _shape(v_cache, "v_cache", k_cache.shape, k_cache.device)
-    if kv == SR_KV_BF16:
-        if kv_scales is not None:
-            raise ValueError("a bfloat16 cache has no kv_scales")
-    elif kv_scales is None:
-        raise ValueError("an 8-bit cache needs kv_scales")
-    else:
-        _shape(kv_scales, "kv_scales", (*k_cache.shape[:3], 2), k_cache.device)
+    if (kv == SR_KV_BF16) != (kv_scales is None):
+        raise ValueError("a bfloat16 cache has no kv_scales" if kv == SR_KV_BF16 else "an 8-bit cache needs kv_scales")
     return kv
 
 
@@ -444,13 +448,14 @@ class QuantCache:
         self.scales = torch.zeros((*shape[:3], 2), dtype=torch.float32, device=device)
 
 
-def _row_strides(t: torch.Tensor, name: str, shape, device) -> RowStrides:
+def _row_strides(t: torch.Tensor, name: str, shape: tuple, device: int) -> RowStrides:
     """Strides of a bf16 [B, T, Hkv, 128] tensor, which may be a view."""
-    _shape(t, name, shape, device)
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor with a contiguous last dimension")
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device or st[3] != 1:
+        raise ValueError(f"{name} must be a bfloat16 tensor {shape} on cuda:{device} with a contiguous last dimension, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     # the stride of a dimension of one entry is never used
-    return RowStrides(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+    return RowStrides(*(x if n > 1 else 0 for x, n in zip(st, shape[:3])))
 
 
 @_on_tensor_device
@@ -460,26 +465,22 @@ def kv_append_quant(k_new, v_new, start, n_new, k_cache, v_cache, kv_scales, k0=
     [B, T, Hkv, 128], views allowed) into slots start[b] + t of the 8-bit cache.
     k0 / v0 (both or neither) receive the bf16 rows that land in slot 0. Updates
     k_cache, v_cache, kv_scales, k0 and v0 in place and returns the first three."""
-    kv = _kv_type(k_cache, v_cache, kv_scales)
-    B, Hkv, Lmax, d = k_cache.shape
-    dev = k_cache.device
+    kv = _kv_type(k_cache, kv_scales)
+    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
+    dev, i32, cache = k_cache.get_device(), torch.int32, k_cache.dtype
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B, T, Hkv, 128]")
     T = k_new.shape[1]
+    rows, row0 = (B, T, Hkv, d), (B, Hkv, d)
+    ks, vs = _row_strides(k_new, "k_new", rows, dev), _row_strides(v_new, "v_new", rows, dev)
     if T < 1:
         return k_cache, v_cache, kv_scales
-    ks, vs = (_row_strides(t, n, (B, T, Hkv, d), dev) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
-    _shape(start, "start", (B,), dev)
-    _shape(n_new, "n_new", (B,), dev)
-    _shape(k0, "k0", (B, Hkv, d), dev)
-    _shape(v0, "v0", (B, Hkv, d), dev)
-    dims = dims_of(B, Hkv, Hkv, Lmax, d)
     st = load().sr_kv_append_quant(
-        ctypes.byref(dims), kv, T, k_new.data_ptr(), ctypes.byref(ks), v_new.data_ptr(), ctypes.byref(vs),
-        _dev(start, "start", torch.int32), _dev(n_new, "n_new", torch.int32), _dev(k_cache, "k_cache", k_cache.dtype),
-        _dev(v_cache, "v_cache", k_cache.dtype), _dev(kv_scales, "kv_scales", torch.float32),
-        _opt(k0, "k0", torch.bfloat16), _opt(v0, "v0", torch.bfloat16),
-        _opt(device_error, "device_error", torch.int32), _stream(stream))
+        Dims(B, Hkv, Hkv, d, Lmax), kv, T, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        _arg(start, "start", i32, (B,), dev), _arg(n_new, "n_new", i32, (B,), dev),
+        _arg(k_cache, "k_cache", cache, full, dev), _arg(v_cache, "v_cache", cache, full, dev),
+        _arg(kv_scales, "kv_scales", torch.float32, (B, Hkv, Lmax, 2), dev), _opt(k0, "k0", torch.bfloat16, row0, dev),
+        _opt(v0, "v0", torch.bfloat16, row0, dev), _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
     _check("sr_kv_append_quant", st)
     return k_cache, v_cache, kv_scales
 
@@ -489,24 +490,21 @@ def kv_dequant(k_cache, v_cache, kv_scales, start, n, k_out, v_out, device_error
     """sr_kv_dequant: positions start[b] .. start[b] + n[b] - 1 of the 8-bit cache
     as bf16 rows 0 .. n[b] - 1 of k_out / v_out [B, Hkv, T, 128]; the other rows
     stay. Returns (k_out, v_out)."""
-    kv = _kv_type(k_cache, v_cache, kv_scales)
-    B, Hkv, Lmax, d = k_cache.shape
-    dev = k_cache.device
+    kv = _kv_type(k_cache, kv_scales)
+    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
+    dev, i32, cache = k_cache.get_device(), torch.int32, k_cache.dtype
     if k_out.dim() != 4:
         raise ValueError("k_out must be [B, Hkv, T, 128]")
     T = k_out.shape[2]
-    _shape(k_out, "k_out", (B, Hkv, T, d), dev)
-    _shape(v_out, "v_out", (B, Hkv, T, d), dev)
-    _shape(start, "start", (B,), dev)
-    _shape(n, "n", (B,), dev)
+    rows = (B, Hkv, T, d)
+    ko, vo = _arg(k_out, "k_out", torch.bfloat16, rows, dev), _arg(v_out, "v_out", torch.bfloat16, rows, dev)
     if T < 1:
         return k_out, v_out
-    dims = dims_of(B, Hkv, Hkv, Lmax, d)
     st = load().sr_kv_dequant(
-        ctypes.byref(dims), kv, T, _dev(k_cache, "k_cache", k_cache.dtype), _dev(v_cache, "v_cache", k_cache.dtype),
-        _dev(kv_scales, "kv_scales", torch.float32), _dev(start, "start", torch.int32), _dev(n, "n", torch.int32),
-        _dev(k_out, "k_out", torch.bfloat16), _dev(v_out, "v_out", torch.bfloat16),
-        _opt(device_error, "device_error", torch.int32), _stream(stream))
+        Dims(B, Hkv, Hkv, d, Lmax), kv, T, _arg(k_cache, "k_cache", cache, full, dev),
+        _arg(v_cache, "v_cache", cache, full, dev), _arg(kv_scales, "kv_scales", torch.float32, (B, Hkv, Lmax, 2), dev),
+        _arg(start, "start", i32, (B,), dev), _arg(n, "n", i32, (B,), dev), ko, vo,
+        _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
     _check("sr_kv_dequant", st)
     return k_out, v_out
 
@@ -519,55 +517,49 @@ def rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cac
     (kv_scales None for bf16) whose slot 0 holds position pos_offset. seq_lens
     advances in place, or into seq_lens_out when that is given. Returns (q_out,
     route_mask, active_list); q_out may be q_in."""
-    kv = _kv_type(k_cache, v_cache, kv_scales, quant_only=False)
-    B, Hkv, Lmax, d = k_cache.shape
-    dev = k_cache.device
-    Hq = q_in.shape[1]
+    kv = _kv_type(k_cache, kv_scales, quant_only=False)
+    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
+    dev, i32, f32, bf16, cache = k_cache.get_device(), torch.int32, torch.float32, torch.bfloat16, k_cache.dtype
+    Hq, U, max_pos = q_in.shape[1], B * Hkv, rope_cos.shape[0]
+    qs, kvs, table = (B, Hq, d), (B, Hkv, d), (max_pos, d // 2)
+    q_ptr = _arg(q_in, "q_in", bf16, qs, dev)
     if q_out is None:
         q_out = torch.empty_like(q_in)
     if route_mask is None:
-        route_mask = torch.empty(B * Hkv, dtype=torch.uint8, device=dev)
+        route_mask = torch.empty(U, dtype=torch.uint8, device=q_in.device)
     if active_list is None:
-        active_list = torch.empty(1 + B * Hkv, dtype=torch.int32, device=dev)
-    if seq_lens_out is None:
-        seq_lens_out = seq_lens
-    if rope_cos.shape != rope_sin.shape or rope_cos.dim() != 2 or rope_cos.shape[1] != d // 2:
-        raise ValueError("rope_cos / rope_sin must both be [max_pos, head_dim / 2]")
-    for t, name, shape in ((q_in, "q_in", (B, Hq, d)), (q_out, "q_out", (B, Hq, d)), (k_new, "k_new", (B, Hkv, d)),
-                           (v_new, "v_new", (B, Hkv, d)), (k0, "k0", (B, Hkv, d)), (v0, "v0", (B, Hkv, d)),
-                           (seq_lens, "seq_lens", (B,)), (seq_lens_out, "seq_lens_out", (B,)),
-                           (route_mask, "route_mask", (B * Hkv,)), (active_list, "active_list", (1 + B * Hkv,))):
-        _shape(t, name, shape, dev)
-    dims = dims_of(B, Hq, Hkv, Lmax, d)
+        active_list = torch.empty(1 + U, dtype=i32, device=q_in.device)
+    lens = _arg(seq_lens, "seq_lens", i32, (B,), dev)
     st = load().sr_rope_append_route_kv(
-        ctypes.byref(dims), kv, int(pos_offset), _dev(q_in, "q_in", torch.bfloat16),
-        _dev(k_new, "k_new", torch.bfloat16), _dev(v_new, "v_new", torch.bfloat16),
-        _dev(rope_cos, "rope_cos", torch.float32), _dev(rope_sin, "rope_sin", torch.float32), int(rope_cos.shape[0]),
-        _dev(seq_lens, "seq_lens", torch.int32), _dev(seq_lens_out, "seq_lens_out", torch.int32),
-        _dev(k_cache, "k_cache", k_cache.dtype), _dev(v_cache, "v_cache", k_cache.dtype),
-        _opt(kv_scales, "kv_scales", torch.float32), _dev(k0, "k0", torch.bfloat16), _dev(v0, "v0", torch.bfloat16),
-        float(tau), _dev(q_out, "q_out", torch.bfloat16), _dev(route_mask, "route_mask", torch.uint8),
-        _dev(active_list, "active_list", torch.int32), _opt(device_error, "device_error", torch.int32),
-        _stream(stream))
+        Dims(B, Hq, Hkv, d, Lmax), kv, pos_offset, q_ptr, _arg(k_new, "k_new", bf16, kvs, dev),
+        _arg(v_new, "v_new", bf16, kvs, dev), _arg(rope_cos, "rope_cos", f32, table, dev),
+        _arg(rope_sin, "rope_sin", f32, table, dev), max_pos, lens,
+        lens if seq_lens_out is None else _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev),
+        _arg(k_cache, "k_cache", cache, full, dev), _arg(v_cache, "v_cache", cache, full, dev),
+        _opt(kv_scales, "kv_scales", f32, (B, Hkv, Lmax, 2), dev), _arg(k0, "k0", bf16, kvs, dev),
+        _arg(v0, "v0", bf16, kvs, dev), tau, _arg(q_out, "q_out", bf16, qs, dev),
+        _arg(route_mask, "route_mask", torch.uint8, (U,), dev), _arg(active_list, "active_list", i32, (1 + U,), dev),
+        _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
     _check("sr_rope_append_route_kv", st)
     return q_out, route_mask, active_list
 
 
-def _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits):
-    """Checked arguments that both forms of the 8-bit scan share, and their dims."""
-    kv = _kv_type(k_cache, v_cache, kv_scales)
-    B, Hkv, Lmax, d = k_cache.shape
-    dev = k_cache.device
+def _decode_quant(fn, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out, lse, out_dtype,
+                  workspace, stream):
+    """Both forms of the 8-bit scan: they differ in the entry point and the outputs' type."""
+    kv = _kv_type(k_cache, kv_scales)
+    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
+    dev, i32, f32, bf16, cache = k_cache.get_device(), torch.int32, torch.float32, torch.bfloat16, k_cache.dtype
     Hq = q.shape[1]
-    _shape(q, "q", (B, Hq, d), dev)
-    _shape(v0, "v0", (B, Hkv, d), dev)
-    _shape(seq_lens, "seq_lens", (B,), dev)
-    _shape(active_list, "active_list", (1 + B * Hkv,), dev)
-    dims = dims_of(B, Hq, Hkv, Lmax, d)
-    return dims, (ctypes.byref(dims), kv, _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", k_cache.dtype),
-                  _dev(v_cache, "v_cache", k_cache.dtype), _dev(kv_scales, "kv_scales", torch.float32),
-                  _dev(v0, "v0", torch.bfloat16), _dev(seq_lens, "seq_lens", torch.int32),
-                  _dev(active_list, "active_list", torch.int32), int(n_splits))
+    qs = (B, Hq, d)
+    args = (Dims(B, Hq, Hkv, d, Lmax), kv, _arg(q, "q", bf16, qs, dev), _arg(k_cache, "k_cache", cache, full, dev),
+            _arg(v_cache, "v_cache", cache, full, dev), _arg(kv_scales, "kv_scales", f32, (B, Hkv, Lmax, 2), dev),
+            _arg(v0, "v0", bf16, (B, Hkv, d), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
+            _arg(active_list, "active_list", i32, (1 + B * Hkv,), dev), n_splits,
+            _arg(out, "out" if out_dtype is bf16 else "o_part", out_dtype, qs, dev), _opt(lse, "lse", f32, (B, Hq), dev))
+    if workspace is None:
+        workspace = Workspace(B, Hq, Hkv, Lmax, n_splits, device=q.device)
+    _check(fn, getattr(load(), fn)(*args, workspace.ptr, workspace.nbytes, _stream(stream)))
 
 
 @_on_tensor_device
@@ -576,16 +568,10 @@ def decode_attention_quant(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_
     """sr_decode_attention_quant: decode_attention over an 8-bit cache. Returns
     out bf16 [B, Hq, 128]; ``lse`` (fp32 [B, Hq]) receives the per-head
     log-sum-exp (NaN for sink heads)."""
-    dims, args = _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits)
     if out is None:
         out = torch.empty_like(q)
-    _shape(out, "out", q.shape, q.device)
-    _shape(lse, "lse", q.shape[:2], q.device)
-    if workspace is None:
-        workspace = Workspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, n_splits, device=q.device)
-    _check("sr_decode_attention_quant",
-           load().sr_decode_attention_quant(*args, _dev(out, "out", torch.bfloat16), _opt(lse, "lse", torch.float32),
-                                            ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    _decode_quant("sr_decode_attention_quant", q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out,
+                  lse, torch.bfloat16, workspace, stream)
     return out
 
 
@@ -594,25 +580,17 @@ def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens,
                                    lse_part=None, n_splits: int = 0, workspace: Workspace | None = None, stream=None):
     """sr_decode_attention_quant_partial: decode_attention_partial over an 8-bit
     cache. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    dims, args = _quant_args(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits)
     if o_part is None:
         o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     if lse_part is None:
         lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _shape(o_part, "o_part", q.shape, q.device)
-    _shape(lse_part, "lse_part", q.shape[:2], q.device)
-    if workspace is None:
-        workspace = Workspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, n_splits, device=q.device)
-    _check("sr_decode_attention_quant_partial",
-           load().sr_decode_attention_quant_partial(*args, _dev(o_part, "o_part", torch.float32),
-                                                    _dev(lse_part, "lse_part", torch.float32),
-                                                    ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    _decode_quant("sr_decode_attention_quant_partial", q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list,
+                  n_splits, o_part, lse_part, torch.float32, workspace, stream)
     return o_part, lse_part
 
 
 def prefix_workspace_bytes(batch, n_q_heads, n_kv_heads, max_prefix_len) -> int:
-    d = dims_of(batch, n_q_heads, n_kv_heads, max_prefix_len)
-    n = load().sr_prefix_workspace_bytes(ctypes.byref(d))
+    n = load().sr_prefix_workspace_bytes(dims_of(batch, n_q_heads, n_kv_heads, max_prefix_len))
     if n == 0:
         raise ValueError("unsupported dims for the prefix workspace")
     return int(n)
@@ -626,22 +604,23 @@ class PrefixWorkspace(Workspace):
         self._allocate(prefix_workspace_bytes(batch, n_q_heads, n_kv_heads, max_prefix_len), device)
 
 
-def _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask):
-    """Checked arguments that both forms of the prefix attention share, and their dims."""
+def _prefix(fn, q, k_prefix, v_prefix, prefix_len, v0, route_mask, suffix, out, lse, out_dtype, workspace, stream):
+    """Both forms of the prefix attention; suffix: (o_suffix, lse_suffix), or () for the partial form."""
     if k_prefix.dim() != 3 or k_prefix.shape[2] != HEAD_DIM or q.dim() != 3:
         raise ValueError("q must be [B, Hq, 128] and k_prefix [Hkv, max_prefix_len, 128]")
-    Hkv, Lmax, d = k_prefix.shape
-    B, Hq, _ = q.shape
-    dev = q.device
-    _shape(q, "q", (B, Hq, d), dev)
-    _shape(k_prefix, "k_prefix", (Hkv, Lmax, d), dev)
-    _shape(v_prefix, "v_prefix", (Hkv, Lmax, d), dev)
-    _shape(v0, "v0", (B, Hkv, d), dev)
-    _shape(route_mask, "route_mask", (B * Hkv,), dev)
-    dims = dims_of(B, Hq, Hkv, Lmax, d)
-    return dims, (ctypes.byref(dims), int(prefix_len), _dev(q, "q", torch.bfloat16),
-                  _dev(k_prefix, "k_prefix", torch.bfloat16), _dev(v_prefix, "v_prefix", torch.bfloat16),
-                  _dev(v0, "v0", torch.bfloat16), _dev(route_mask, "route_mask", torch.uint8))
+    Hkv, Lmax, d = pre = tuple(k_prefix.shape)
+    B, Hq = q.shape[:2]
+    dev, f32, bf16 = q.get_device(), torch.float32, torch.bfloat16
+    qs, hs = (B, Hq, d), (B, Hq)
+    args = (Dims(B, Hq, Hkv, d, Lmax), prefix_len, _arg(q, "q", bf16, qs, dev),
+            _arg(k_prefix, "k_prefix", bf16, pre, dev), _arg(v_prefix, "v_prefix", bf16, pre, dev),
+            _arg(v0, "v0", bf16, (B, Hkv, d), dev), _arg(route_mask, "route_mask", torch.uint8, (B * Hkv,), dev))
+    if suffix:
+        args += (_opt(suffix[0], "o_suffix", f32, qs, dev), _opt(suffix[1], "lse_suffix", f32, hs, dev))
+    args += (_arg(out, "out" if out_dtype is bf16 else "o_part", out_dtype, qs, dev), _opt(lse, "lse", f32, hs, dev))
+    if workspace is None:
+        workspace = PrefixWorkspace(B, Hq, Hkv, Lmax, device=q.device)
+    _check(fn, getattr(load(), fn)(*args, workspace.ptr, workspace.nbytes, _stream(stream)))
 
 
 @_on_tensor_device
@@ -652,19 +631,10 @@ def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out
     prefix_len positions of it), joined with each sequence's suffix when o_suffix
     and lse_suffix (decode_attention_partial's) are given. Returns out bf16 [B, Hq,
     128]; ``lse`` (fp32 [B, Hq]) receives the log-sum-exp (NaN for sink heads)."""
-    dims, args = _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask)
     if out is None:
         out = torch.empty_like(q)
-    for t, name, shape in ((out, "out", q.shape), (lse, "lse", q.shape[:2]), (o_suffix, "o_suffix", q.shape),
-                           (lse_suffix, "lse_suffix", q.shape[:2])):
-        _shape(t, name, shape, q.device)
-    if workspace is None:
-        workspace = PrefixWorkspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, device=q.device)
-    _check("sr_prefix_attention",
-           load().sr_prefix_attention(*args, _opt(o_suffix, "o_suffix", torch.float32),
-                                      _opt(lse_suffix, "lse_suffix", torch.float32),
-                                      _dev(out, "out", torch.bfloat16), _opt(lse, "lse", torch.float32),
-                                      ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    _prefix("sr_prefix_attention", q, k_prefix, v_prefix, prefix_len, v0, route_mask, (o_suffix, lse_suffix), out, lse,
+            torch.bfloat16, workspace, stream)
     return out
 
 
@@ -673,19 +643,12 @@ def prefix_attention_partial(q, k_prefix, v_prefix, prefix_len: int, v0, route_m
                              workspace: PrefixWorkspace | None = None, stream=None):
     """sr_prefix_attention_partial: the prefix's part alone, as combine_partials
     takes it. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    dims, args = _prefix_args(q, k_prefix, v_prefix, prefix_len, v0, route_mask)
     if o_part is None:
         o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     if lse_part is None:
         lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _shape(o_part, "o_part", q.shape, q.device)
-    _shape(lse_part, "lse_part", q.shape[:2], q.device)
-    if workspace is None:
-        workspace = PrefixWorkspace(dims.batch, dims.n_q_heads, dims.n_kv_heads, dims.max_seq_len, device=q.device)
-    _check("sr_prefix_attention_partial",
-           load().sr_prefix_attention_partial(*args, _dev(o_part, "o_part", torch.float32),
-                                              _dev(lse_part, "lse_part", torch.float32),
-                                              ctypes.c_void_p(workspace.ptr), workspace.nbytes, _stream(stream)))
+    _prefix("sr_prefix_attention_partial", q, k_prefix, v_prefix, prefix_len, v0, route_mask, (), o_part, lse_part,
+            torch.float32, workspace, stream)
     return o_part, lse_part
 
 

@@ -551,6 +551,34 @@ def test_far_positions_of_a_cache_over_4_gib(dtype):
         assert ((lse[0, h].double() - torch.log(tot[:, 0])).abs() <= R.lse_bound(torch.log(tot[:, 0]), delta) + 2.0 ** -10).all()
 
 
+def test_binding_refusals_on_the_gpu():
+    """Every tensor's shape, type, layout and device is held against the cache's."""
+    c = native.QuantCache(2, 4, 9)
+    q = torch.zeros(2, 8, R.D, device=DEV, dtype=torch.bfloat16)
+    v0 = torch.zeros(2, 4, R.D, device=DEV, dtype=torch.bfloat16)
+    sl = torch.ones(2, dtype=torch.int32, device=DEV)
+    act = torch.zeros(9, dtype=torch.int32, device=DEV)
+    good = dict(q=q, k_cache=c.k, v_cache=c.v, kv_scales=c.scales, v0=v0, seq_lens=sl, active_list=act)
+    native.decode_attention_quant(*good.values())
+    bad = dict(q=[q[:1], q.float(), q.cpu(), q[:, :7]], v_cache=[c.v[:, :, :8], c.v.view(torch.int8), c.v.cpu()],
+               kv_scales=[c.scales[..., :1], c.scales.double(), c.scales.transpose(0, 1)], v0=[v0[:, :3], v0.float()],
+               seq_lens=[sl[:1], sl.long()], active_list=[act[:8], act.float()])
+    for name, tensors in bad.items():
+        for t in tensors:
+            with pytest.raises((ValueError, native.SinkRouterError)):
+                native.decode_attention_quant(*(t if n == name else x for n, x in good.items()))
+    x = torch.zeros(2, 3, 4, R.D, device=DEV, dtype=torch.bfloat16)
+    wide = torch.zeros(2, 3, 4, R.D + 4, device=DEV, dtype=torch.bfloat16)[..., :R.D]  # rows not 16-byte aligned
+    for k_new in (x[:, :, :3], x.float(), x.transpose(1, 2), wide):
+        with pytest.raises((ValueError, native.SinkRouterError)):
+            native.kv_append_quant(k_new, x, sl, sl, c.k, c.v, c.scales)
+    with pytest.raises(native.SinkRouterError):
+        native.kv_append_quant(x, x, sl, sl, c.k, c.v, c.scales, k0=v0)  # k0 without v0
+    assert native.kv_append_quant(x[:, :0], x[:, :0], sl, sl, c.k, c.v, c.scales)[0] is c.k  # no token: nothing to do
+    torch.cuda.synchronize()
+    assert not c.scales.any()
+
+
 # ---- together ----------------------------------------------------------------------------
 
 @both
