@@ -12,8 +12,9 @@
 //  * plan: one CTA lists the active sequences of each KV head and cuts each head's
 //    rows into items of up to 256.
 //  * scan: one persistent CTA per SM takes a contiguous share of the (item, tile
-//    of 128 positions) sequence and leaves one partial (m, l, O) a row for every
-//    item its share touches.
+//    of 128 positions) sequence, in which a tile weighs 2 for an item of more than
+//    128 rows and 1 for a smaller one, and leaves one partial (m, l, O) a row for
+//    every item its share touches.
 //  * join: one warp a query head combines its partials, and the suffix's.
 //
 // scan, per CTA: two softmax warpgroups (a thread a row), a copy warp and an MMA
@@ -59,15 +60,19 @@ constexpr int kTileBytes = 2 * kHalfBytes;    // [128 x 128]
 constexpr int kThreads = 384;                 // two softmax warpgroups, one for copies and MMAs
 constexpr int kSoftmaxThreads = 256;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
+#ifndef SR_PREFIX_POLY
+#define SR_PREFIX_POLY 2
+#endif
+constexpr int kPolyOf8 = SR_PREFIX_POLY; // pairs of 8 whose 2^x is a polynomial
 constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
 constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffBar = kOffRing + kStages * kTileBytes;
 constexpr int kSmem = kOffBar + 256 + 1024; // and room to align the base to 1024 B
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
-// Workspace: [error word | n_items | active count, first item of each KV head | active
-// sequences of each head | rank of each unit | items | (m, l) | O]
+// Workspace: [error word | total weight | active count, first item of each KV head | active
+// sequences of each head | rank of each unit | items | item at each weight | (m, l) | O]
 struct Layout {
-    size_t count, first, list, rank, items, ml, o, total;
+    size_t count, first, list, rank, items, item_of, ml, o, total;
     int row_cap; // rows of a stream's partial
     long long max_items, slots;
 };
@@ -91,6 +96,7 @@ Layout layout(int B, int Hq, int Hkv)
     w.list = take(4 * U);
     w.rank = take(4 * U);
     w.items = take(16 * (size_t)w.max_items);
+    w.item_of = take(4 * 2 * (size_t)w.max_items);
     w.ml = take(8 * 2 * (size_t)w.slots * w.row_cap);
     w.o = take(4 * 2 * (size_t)w.slots * w.row_cap * kHeadDim);
     w.total = at;
@@ -101,9 +107,10 @@ struct Params {
     const __nv_bfloat16 *q, *v0;
     const uint8_t *mask;
     int32_t *err;
-    int32_t *n_items; // word 1 of the workspace
+    int32_t *weight; // word 1 of the workspace: sum of the items' weights
     int32_t *count, *first, *list, *rank;
-    int4 *items; // KV head, first row of the head's rows, rows
+    int4 *items;      // KV head, first row of the head's rows, rows, weights before it
+    int32_t *item_of; // item at each unit of weight
     float2 *ml;  // [slot][stream][row] (m in log2 units, l)
     float *o;    // [slot][stream][16][row][8]
     const float *o_suffix, *lse_suffix;
@@ -112,14 +119,27 @@ struct Params {
     int B, Hq, Hkv, M, prefix_len, row_cap, grid;
 };
 
+// An item's weight: its tiles take two row tiles' products or one.
+__device__ __forceinline__ int weight_of(int rows) { return rows > kTile ? 2 : 1; }
+
+// Cost of n tiles of weight 1, even, so that with even shares no tile of weight 2
+// lies across two shares.
+__device__ __forceinline__ long long item_cost(int nt) { return (nt + 1) & ~1; }
+
+// Cost that one CTA takes of `weight` items of weight 1.
+__device__ __forceinline__ long long share_of(int weight, int nt, int grid)
+{
+    return max(((long long)weight * item_cost(nt) + grid - 1) / grid + 1 & ~1ll, 2ll);
+}
+
 // ---- plan -------------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 512;
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params p)
 {
-    __shared__ int warp_sum[kPlanThreads / 32];
-    __shared__ int carry;
+    __shared__ int2 warp_sum[kPlanThreads / 32];
+    __shared__ int2 carry; // items, weight
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -141,39 +161,51 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params p)
             p.count[g] = n;
     }
     if (threadIdx.x == 0)
-        carry = 0;
+        carry = make_int2(0, 0);
     __syncthreads();
     for (int g0 = 0; g0 < p.Hkv; g0 += kPlanThreads) {
         const int g = g0 + (int)threadIdx.x;
         const int rows = g < p.Hkv ? p.count[g] * p.M : 0;
-        const int n = (rows + kItemRows - 1) / kItemRows;
-        int incl = n;
+        const int n = (rows + kItemRows - 1) / kItemRows, last = rows - (n - 1) * kItemRows;
+        const int2 mine = make_int2(n, n ? 2 * (n - 1) + weight_of(last) : 0);
+        int2 incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o)
-                incl += y;
+            const int y = __shfl_up_sync(kFull, incl.x, o), z = __shfl_up_sync(kFull, incl.y, o);
+            if (lane >= o) {
+                incl.x += y;
+                incl.y += z;
+            }
         }
         if (lane == 31)
             warp_sum[warp] = incl;
         __syncthreads();
-        int before = carry, all = 0;
+        int2 before = carry, all = make_int2(0, 0);
         for (int w = 0; w < kPlanThreads / 32; ++w) {
-            before += w < warp ? warp_sum[w] : 0;
-            all += warp_sum[w];
+            const int2 x = warp_sum[w];
+            if (w < warp) {
+                before.x += x.x;
+                before.y += x.y;
+            }
+            all.x += x.x;
+            all.y += x.y;
         }
-        const int first = before + incl - n;
+        const int first = before.x + incl.x - mine.x, weight = before.y + incl.y - mine.y;
         if (g < p.Hkv)
             p.first[g] = first;
-        for (int i = 0; i < n; ++i)
-            p.items[first + i] = make_int4(g, i * kItemRows, min(kItemRows, rows - i * kItemRows), 0);
+        for (int i = 0; i < n; ++i) {
+            p.items[first + i] = make_int4(g, i * kItemRows, min(kItemRows, rows - i * kItemRows), weight + 2 * i);
+            p.item_of[weight + 2 * i] = first + i;
+            if (i + 1 < n || weight_of(last) == 2)
+                p.item_of[weight + 2 * i + 1] = first + i;
+        }
         __syncthreads();
         if (threadIdx.x == 0)
-            carry += all;
+            carry = make_int2(carry.x + all.x, carry.y + all.y);
         __syncthreads();
     }
     if (threadIdx.x == 0)
-        *p.n_items = carry;
+        *p.weight = carry.y;
 }
 
 // ---- scan -------------------------------------------------------------------------------
@@ -195,26 +227,76 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// The same for a whole warp: true in every lane or in none.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(kFull, wait_bar(bar, parity, abort_flag));
+}
+
+// Largest of three, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^y of a pair without the special-function unit: y = n + f with n the nearest
+// integer (added and taken off as 1.5 2^23 + n), 2^f on [-1/2, 1/2] by the degree-4
+// polynomial of least largest relative error (2.7e-6, mean 4e-8; Remez exchange), n
+// added to its exponent. y below -126 counts as -126; y must be below 127.
+__device__ __forceinline__ void exp2_poly2(uint64_t y2, float &a, float &b)
+{
+    unpack2(y2, a, b);
+    y2 = pack2(a < -126.f ? -126.f : a, b < -126.f ? -126.f : b);
+    const uint64_t t = add2(y2, pack2(12582912.f, 12582912.f));
+    const uint64_t f = sub2(y2, add2(t, pack2(-12582912.f, -12582912.f)));
+    uint64_t r = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
+                      pack2(0.05591785907745361f, 0.05591785907745361f));
+    r = fma2(r, f, pack2(0.240247443318367f, 0.240247443318367f));
+    r = fma2(r, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+    r = fma2(r, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+    float ta, tb, ra, rb;
+    unpack2(t, ta, tb);
+    unpack2(r, ra, rb);
+    a = __uint_as_float(__float_as_uint(ra) + (__float_as_uint(ta) << 23));
+    b = __uint_as_float(__float_as_uint(rb) + (__float_as_uint(tb) << 23));
+}
+
 // A CTA's part of one item: tiles [j0, j1).
 struct Segment {
     int item, j0, j1;
+    int4 it;
 };
 
-// Share of CTA c of n_items x nt tiles: [c * share, (c + 1) * share).
-__device__ __forceinline__ long long share_of(long long tiles, int grid) { return (tiles + grid - 1) / grid; }
-
+// The segments of a share: costs [at, end) of the items' sequence.
 struct Walk {
-    long long at, end;
+    const Params &p;
+    long long at, end, cost;
     int nt;
+    __device__ __forceinline__ Walk(const Params &p_) : p(p_)
+    {
+        nt = (p.prefix_len + kTile - 1) / kTile;
+        cost = item_cost(nt);
+        const int weight = __ldcg(p.weight);
+        const long long share = share_of(weight, nt, gridDim.x);
+        at = min((long long)blockIdx.x * share, weight * cost);
+        end = min(at + share, weight * cost);
+    }
     __device__ __forceinline__ bool next(Segment &s)
     {
-        if (at >= end)
-            return false;
-        s.item = (int)(at / nt);
-        s.j0 = (int)(at - (long long)s.item * nt);
-        s.j1 = (int)min((long long)nt, s.j0 + (end - at));
-        at += s.j1 - s.j0;
-        return true;
+        while (at < end) {
+            s.item = __ldcg(p.item_of + at / cost);
+            s.it = __ldcg(p.items + s.item);
+            const int w = weight_of(s.it.z);
+            const long long begin = s.it.w * cost;
+            s.j0 = (int)((at - begin) / w);
+            s.j1 = (int)min((long long)nt, (end - begin) / w);
+            at = min(end, begin + w * cost);
+            if (s.j0 < s.j1) // else only the padding of an odd number of tiles
+                return true;
+        }
+        return false;
     }
 };
 
@@ -231,7 +313,7 @@ struct Streams {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], q_full, s_full[2], p_full[2], o_full[2], seg_done, drain;
+    uint64_t full[kStages], empty[kStages], q_full, s_full[2], p_full[2][2], o_full[2], seg_done, drain;
     uint32_t tmem;
     int abort_flag;
 };
@@ -244,7 +326,7 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Shared *sh = reinterpret_cast<Shared *>(smem + kOffBar);
     volatile int *abort_flag = &sh->abort_flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty), q_full = smem_u32(&sh->q_full);
     const uint32_t s_full = smem_u32(sh->s_full), p_full = smem_u32(sh->p_full), o_full = smem_u32(sh->o_full);
     const uint32_t seg_done = smem_u32(&sh->seg_done);
@@ -259,7 +341,8 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         mbar_init(smem_u32(&sh->drain), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 1);
-            mbar_init(p_full + 8 * s, kTile);
+            mbar_init(p_full + 16 * s, kTile);
+            mbar_init(p_full + 16 * s + 8, kTile);
             mbar_init(o_full + 8 * s, 1);
         }
         sh->abort_flag = 0;
@@ -278,36 +361,34 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const int nt = (p.prefix_len + kTile - 1) / kTile;
-    Walk walk;
-    walk.nt = nt;
-    {
-        const long long tiles = (long long)__ldcg(p.n_items) * nt;
-        const long long share = share_of(tiles, gridDim.x);
-        walk.at = min((long long)blockIdx.x * share, tiles);
-        walk.end = min(walk.at + share, tiles);
-    }
+    Walk walk(p);
     Segment seg;
     bool ok = true;
 
     if (warp >= 8) {
-        regs_dec<56>();
-        if (warp == kCopyWarp && lane == 0) {
+        regs_dec<88>();
+        // Both warps run converged and elect the issuing lane at each issue: the
+        // instructions take their descriptors from uniform registers, which code
+        // under a divergent branch has to fill one by one.
+        if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             uint32_t pos = 0; // copies issued
             auto copy = [&](const CUtensorMap *map, int g, int j) -> bool {
                 const uint32_t st = pos % kStages;
-                if (!wait_bar(empty0 + 8 * st, ((pos / kStages) & 1) ^ 1, abort_flag))
+                if (!wait_warp(empty0 + 8 * st, ((pos / kStages) & 1) ^ 1, abort_flag))
                     return false;
                 const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem + kOffRing + st * kTileBytes);
-                mbar_arrive_expect_tx(fb, kTileBytes);
-                tma_load_3d_plain(dst, map, fb, 0, j * kTile, g);
-                tma_load_3d_plain(dst + kHalfBytes, map, fb, 64, j * kTile, g);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(fb, kTileBytes);
+                    tma_load_3d_plain(dst, map, fb, 0, j * kTile, g);
+                    tma_load_3d_plain(dst + kHalfBytes, map, fb, 64, j * kTile, g);
+                }
+                __syncwarp();
                 ++pos;
                 return true;
             };
             while (ok && walk.next(seg)) {
-                const int4 it = __ldcg(p.items + seg.item);
+                const int4 it = seg.it;
                 const int n = seg.j1 - seg.j0;
                 if (it.z > kTile) {
                     for (int j = 0; ok && j < n; ++j)
@@ -323,17 +404,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             if (!ok)
                 for (uint32_t i = pos > kStages ? pos - kStages : 0; i < pos; ++i)
                     (void)wait_bar(full0 + 8 * (i % kStages), (i / kStages) & 1, &never);
-        } else if (warp == kMmaWarp && lane == 0) {
+        } else if (warp == kMmaWarp) {
             // -------------------------------------------------------------- MMAs
             constexpr uint32_t kIdescS = bf16_idesc(kTile, kTile, false), kIdescO = bf16_idesc(kTile, kHeadDim, true);
             uint32_t base = 0, nseg = 0; // copies of earlier segments; segments
-            uint32_t np[2] = {0, 0};     // P tiles consumed by each stream
+            uint32_t np0 = 0, np1 = 0;       // P tiles consumed by each stream
             auto ring = [&](uint32_t at) { return smem_u32(smem + kOffRing + (at % kStages) * kTileBytes); };
-            auto full = [&](uint32_t at) { return wait_bar(full0 + 8 * (at % kStages), (at / kStages) & 1, abort_flag); };
+            auto full = [&](uint32_t at) { return wait_warp(full0 + 8 * (at % kStages), (at / kStages) & 1, abort_flag); };
             while (ok && walk.next(seg)) {
-                const int4 it = __ldcg(p.items + seg.item);
+                const int4 it = seg.it;
                 const Streams st{it.z > kTile, seg.j1 - seg.j0};
-                if (!(ok = wait_bar(q_full, nseg & 1, abort_flag)))
+                if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
                     break;
                 tc_fence_after();
                 // S of stream s, step t
@@ -341,33 +422,47 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     const uint32_t at = base + st.key_at(st.tile(s, t));
                     if (!full(at))
                         return false;
-                    const uint64_t a = smem_desc_sw128(smem_u32(smem + kOffQ + (st.two ? s : 0) * kTileBytes), 16, 1024);
+                    const uint64_t a = smem_desc_sw128(smem_u32(smem + kOffQ + s * kTileBytes), 16, 1024);
                     const uint64_t b = smem_desc_sw128(ring(at), 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) { // 16 of the 128 dimensions each
-                        const uint64_t off = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-                        mma_ss(tmem + s * 128, a + off, b + off, kIdescS, k > 0);
+                        for (int k = 0; k < 8; ++k) { // 16 of the 128 dimensions each
+                            const uint64_t off = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+                            mma_ss(tmem + s * 128, a + off, b + off, kIdescS, k > 0);
+                        }
+                        mma_commit(s_full + 8 * s);
+                        if (!st.two || s == 1)
+                            mma_commit(empty0 + 8 * (at % kStages));
                     }
-                    mma_commit(s_full + 8 * s);
-                    if (!st.two || s == 1)
-                        mma_commit(empty0 + 8 * (at % kStages));
+                    __syncwarp();
                     return true;
                 };
                 // O of stream s += P V, step t
                 auto output = [&](int s, int t) -> bool {
                     const uint32_t at = base + st.value_at(st.tile(s, t));
-                    if (!full(at) || !wait_bar(p_full + 8 * s, np[s] & 1, abort_flag))
+                    if (!full(at))
                         return false;
-                    ++np[s];
-                    tc_fence_after();
                     const uint64_t b = smem_desc_sw128(ring(at), kHalfBytes, 1024);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) // 16 positions each
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, b + k * (2048 >> 4), kIdescO, t > 0 || k > 0);
-                    if (!st.two || s == 1)
-                        mma_commit(empty0 + 8 * (at % kStages));
-                    if (t + 1 == st.steps(s))
-                        mma_commit(o_full + 8 * s);
+                    for (int h = 0; h < 2; ++h) { // P comes in two halves
+                        if (!wait_warp(p_full + 16 * s + 8 * h, (s ? np1 : np0) & 1, abort_flag))
+                            return false;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 4 * h; k < 4 * h + 4; ++k) // 16 positions each
+                                mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
+                                       t > 0 || k > 0);
+                            if (h == 1) {
+                                if (!st.two || s == 1)
+                                    mma_commit(empty0 + 8 * (at % kStages));
+                                if (t + 1 == st.steps(s))
+                                    mma_commit(o_full + 8 * s);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    ++(s ? np1 : np0);
                     return true;
                 };
                 ok = logits(0, 0) && (st.steps(1) == 0 || logits(1, 0));
@@ -381,26 +476,34 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             }
             if (!ok) { // MMAs in flight finish before TMEM is given back
                 volatile int never = 0;
-                mma_commit(smem_u32(&sh->drain));
+                if (elect_one())
+                    mma_commit(smem_u32(&sh->drain));
+                __syncwarp();
                 (void)wait_bar(smem_u32(&sh->drain), 0, &never);
             }
         }
     } else {
         // ------------------------------------------------------------ softmax
-        regs_inc<224>();
+        regs_inc<208>();
         const int s = warp >> 2, row = tid & (kTile - 1); // stream, row of its tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // this warp's TMEM lanes
         const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
         uint32_t ns = 0, no = 0, nseg = 0; // S tiles, O results and segments consumed
         while (walk.next(seg)) {
-            const int4 it = __ldcg(p.items + seg.item);
+            const int4 it = seg.it;
             const Streams st{it.z > kTile, seg.j1 - seg.j0};
+            // Row of the item in this thread's lane. With at most 64 rows the second
+            // stream's start at lane 64, so that the streams' rows fall to different
+            // schedulers.
+            const int turn = !st.two && it.z <= kTile / 2 ? s * (kTile / 2) : 0;
+            const int qrow = st.two ? s * kTile + row : (row + kTile - turn) % kTile;
+            const bool mine = qrow < it.z;
+            const bool busy = __any_sync(kFull, mine); // a warp without a row only keeps the barriers' count
             // Every earlier MMA that read Q is complete (both groups have met below).
-            const int qrow = (st.two ? s * kTile : 0) + row; // row of the item
-            if (st.two || s == 0) {
+            {
                 uint4 *dst = reinterpret_cast<uint4 *>(smem + kOffQ + s * kTileBytes);
                 const uint4 *src = nullptr;
-                if (qrow < it.z) {
+                if (mine) {
                     const int r = it.y + qrow, a = r / p.M;
                     const int b = __ldcg(p.list + (size_t)it.x * p.B + a);
                     src = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.Hq + (size_t)it.x * p.M + (r - a * p.M)) *
@@ -419,11 +522,16 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             float m = -INFINITY, l = 0.f; // m in the logits' units
             const int steps = st.steps(s);
             for (int t = 0; t < steps; ++t) {
-                if (!__all_sync(kFull, wait_bar(s_full + 8 * s, ns & 1, abort_flag))) {
+                if (!wait_warp(s_full + 8 * s, ns & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 ++ns;
+                if (!busy) {
+                    mbar_arrive(p_full + 16 * s);
+                    mbar_arrive(p_full + 16 * s + 8);
+                    continue;
+                }
                 tc_fence_after();
                 uint32_t x[4][32];
 #pragma unroll
@@ -442,59 +550,74 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = __uint_as_float(x[c][0]);
+                    mx[c] = max_nan(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
 #pragma unroll
-                    for (int i = 1; i < 32; ++i)
-                        mx[c] = fmaxf(mx[c], __uint_as_float(x[c][i]));
+                    for (int i = 3; i < 31; i += 2)
+                        mx[c] = max_nan(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float top = max_nan(mx[0], mx[1], __uint_as_float(x[0][31]));
+                top = max_nan(top, mx[2], __uint_as_float(x[1][31]));
+                top = max_nan(top, mx[3], __uint_as_float(x[2][31]));
+                top = max_nan(top, top, __uint_as_float(x[3][31]));
                 if (t == 0) {
                     m = top;
-                } else if (__any_sync(kFull, (top - m) * kScaleLog2 > kGrowth)) {
-                    const float mn = fmaxf(m, top);
-                    const float f = exp2_approx((m - mn) * kScaleLog2);
+                } else if (__any_sync(kFull, !((top - m) * kScaleLog2 <= kGrowth))) { // also for a NaN
+                    const float mn = max_nan(m, top, top);
+                    const float f = mn == m ? 1.f : exp2_approx((m - mn) * kScaleLog2);
                     m = mn;
                     l *= f;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o, tO + 32 * c);
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(o, tO + 16 * c);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(tO + 32 * c, o);
+                        tmem_st16(tO + 16 * c, o);
                     }
                 }
-                const float sub = m * kScaleLog2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // A row without a finite logit yet keeps weights of 0; an infinite
+                // maximum makes them NaN.
+                const float sub = m == -INFINITY ? 0.f : fmaf(m, kScaleLog2, m - m);
+                const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), sub2 = pack2(-sub, -sub);
+                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const uint32_t(&src)[32] = x[2 * h + (i >> 4)];
-                        const float a = exp2_approx(fmaf(__uint_as_float(src[(2 * i) & 31]), kScaleLog2, -sub));
-                        const float b = exp2_approx(fmaf(__uint_as_float(src[(2 * i + 1) & 31]), kScaleLog2, -sub));
-                        sum[i & 1] += a;
-                        sum[2 + (i & 1)] += b;
+                        const uint64_t y = fma2(pack2(__uint_as_float(src[(2 * i) & 31]),
+                                                      __uint_as_float(src[(2 * i + 1) & 31])), scale2, sub2);
+                        float a, b;
+                        if ((i & 7) < kPolyOf8) {
+                            exp2_poly2(y, a, b);
+                        } else {
+                            unpack2(y, a, b);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                        }
+                        sum[i & 1] = add2(sum[i & 1], pack2(a, b));
                         w[i] = pack_bf16x2(a, b);
                     }
                     tmem_st32(tS + 32 * h, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full + 16 * s + 8 * h);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_full + 8 * s);
+                float s0, s1;
+                unpack2(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
             if (!ok)
                 break;
             // ---- the segment's partial of this row
             const size_t slot = (size_t)blockIdx.x + seg.item;
             const size_t part = (slot * 2 + s) * p.row_cap;
-            const bool mine = qrow < it.z;
+            const int prow = qrow % kTile;
             if (steps > 0) {
-                if (!__all_sync(kFull, wait_bar(o_full + 8 * s, no & 1, abort_flag))) {
+                if (!wait_warp(o_full + 8 * s, no & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -509,17 +632,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
                         for (int i = 0; i < 8; ++i) // eight elements a row and block of 16
                             __stcg(reinterpret_cast<float4 *>(p.o + part * kHeadDim +
-                                                              ((size_t)(4 * c + (i >> 1)) * p.row_cap + row) * 8 + (i & 1) * 4),
+                                                              ((size_t)(4 * c + (i >> 1)) * p.row_cap + prow) * 8 + (i & 1) * 4),
                                    make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
                     }
                 }
             }
             if (mine)
-                __stcg(p.ml + part + row, make_float2(m * kScaleLog2, l));
+                __stcg(p.ml + part + prow, make_float2(m * kScaleLog2, l));
             // Both groups are done with the segment's Q, S and O.
             mbar_arrive(seg_done);
-            if (!__all_sync(kFull, wait_bar(seg_done, nseg & 1, abort_flag))) {
+            if (!wait_warp(seg_done, nseg & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -562,10 +685,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
         if (nt > 0) {
             const int r = rank * p.M + (h - g * p.M);
             const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
-            const bool two = __ldcg(p.count + g) * p.M - (r - ir) > kTile;
-            const long long share = share_of((long long)__ldcg(p.n_items) * nt, p.grid);
-            const int c0 = (int)((long long)item * nt / share);
-            const int c1 = (int)(((long long)(item + 1) * nt - 1) / share);
+            const int4 it = __ldcg(p.items + item);
+            const bool two = it.z > kTile;
+            const long long share = share_of(__ldcg(p.weight), nt, p.grid), begin = it.w * item_cost(nt);
+            const int c0 = (int)(begin / share);
+            const int c1 = (int)((begin + (long long)(nt - 1) * weight_of(it.z)) / share);
             // Partials k: of CTA c0 + k, or of its two streams
             const int n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
             auto part = [&](int k) -> size_t {
@@ -697,12 +821,13 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
     p.v0 = static_cast<const __nv_bfloat16 *>(a.v0);
     p.mask = a.mask;
     p.err = reinterpret_cast<int32_t *>(ws);
-    p.n_items = p.err + 1;
+    p.weight = p.err + 1;
     p.count = reinterpret_cast<int32_t *>(ws + w.count);
     p.first = reinterpret_cast<int32_t *>(ws + w.first);
     p.list = reinterpret_cast<int32_t *>(ws + w.list);
     p.rank = reinterpret_cast<int32_t *>(ws + w.rank);
     p.items = reinterpret_cast<int4 *>(ws + w.items);
+    p.item_of = reinterpret_cast<int32_t *>(ws + w.item_of);
     p.ml = reinterpret_cast<float2 *>(ws + w.ml);
     p.o = reinterpret_cast<float *>(ws + w.o);
     p.o_suffix = a.o_suffix;
