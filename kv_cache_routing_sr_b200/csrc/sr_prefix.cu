@@ -12,22 +12,23 @@
 //  * plan: one CTA lists the active sequences of each KV head and cuts each head's
 //    rows into items of up to 256.
 //  * scan: one persistent CTA per SM takes a contiguous share of the (item, tile
-//    of 128 positions) sequence, in which a tile weighs 2 for an item of more than
+//    of 64 positions) sequence, in which a tile weighs 2 for an item of more than
 //    128 rows and 1 for a smaller one, and leaves one partial (m, l, O) a row for
 //    every item its share touches.
 //  * join: one warp a query head combines its partials, and the suffix's.
 //
-// scan, per CTA: two softmax warpgroups (a thread a row), a copy warp and an MMA
-// warp around two streams, each with its logits S (128 x 128, fp32) and its output O
-// in TMEM (all 512 columns). With more than 128 rows the streams are the item's two
-// halves over the same tiles; with fewer they are the same rows over alternate
-// tiles, and leave a partial each. While a warpgroup turns S into P (bf16, written
-// over S), the tensor cores work for the other stream: the issue order is P0 V, S0
-// of the next tile, P1 V, S1 of the next tile. The completion of S also means that
-// the stream's O is complete, so a warpgroup may rescale O before it hands over P;
-// it does so only when a row's maximum has grown by more than 2^8 since the
-// reference it uses (the weights stay below 2^8 of their row's sum, far inside bf16
-// and fp32).
+// scan, per CTA: two streams, each with a softmax warpgroup (a thread a row), an MMA
+// warp, two buffers for its logits S (128 x 64, fp32) and its output O (128 x 128,
+// fp32), which fill the 512 columns of TMEM; and one copy warp for both. With more
+// than 128 rows the streams are the item's two halves over the same tiles; with
+// fewer they are the same rows over alternate tiles, and leave a partial each. An MMA
+// warp issues S of two tiles and then, tile by tile, O += P V and S of the tile after
+// next, so a warpgroup that hands over P (bf16, written over S) finds the next S
+// ready, and a copied tile is used as soon as it has landed: the ring's ten 16 KB
+// stages are in flight rather than waiting. A warpgroup rescales O only when a
+// row's maximum has grown by more than 2^8 since the reference it uses (the weights
+// stay below 2^8 of their row's sum, far inside bf16 and fp32), after the previous
+// tile's product is complete.
 //
 // Every wait is bounded in time; a timeout sets a device error bit, and the CTA
 // leaves once its own copies and MMAs have landed.
@@ -51,22 +52,24 @@ constexpr float kScaleLog2 = 0.12751743082459868f; // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kFull = 0xffffffffu;
 
-constexpr int kTile = 128;           // positions a tile, rows a stream
-constexpr int kItemRows = 2 * kTile; // rows an item
+constexpr int kTile = 64;            // positions a tile
+constexpr int kRows = 128;           // rows a stream
+constexpr int kItemRows = 2 * kRows; // rows an item
 constexpr int kGridCap = 256;        // persistent CTAs never exceed this (sizes the workspace)
-constexpr int kStages = 5;
-constexpr int kHalfBytes = kTile * 128;       // [128 rows x 64 bf16], 128B swizzle
-constexpr int kTileBytes = 2 * kHalfBytes;    // [128 x 128]
+constexpr int kStages = 10;
+constexpr int kHalfBytes = kTile * 128;       // [64 positions x 64 bf16], 128B swizzle
+constexpr int kTileBytes = 2 * kHalfBytes;    // [64 x 128]
+constexpr int kQHalfBytes = kRows * 128, kQBytes = 2 * kQHalfBytes;
 constexpr int kThreads = 384;                 // two softmax warpgroups, one for copies and MMAs
-constexpr int kSoftmaxThreads = 256;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;    // and 10: one a stream
 #ifndef SR_PREFIX_POLY
-#define SR_PREFIX_POLY 2
+#define SR_PREFIX_POLY 0
 #endif
 constexpr int kPolyOf8 = SR_PREFIX_POLY; // pairs of 8 whose 2^x is a polynomial
 constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
-constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffBar = kOffRing + kStages * kTileBytes;
-constexpr int kSmem = kOffBar + 256 + 1024; // and room to align the base to 1024 B
+constexpr int kOffQ = 0, kOffRing = 2 * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
+constexpr int kSmem = kOffBar + 512 + 1024; // and room to align the base to 1024 B
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 // Workspace: [error word | total weight | active count, first item of each KV head | active
@@ -82,7 +85,7 @@ Layout layout(int B, int Hq, int Hkv)
     Layout w;
     const long long rows = (long long)B * (Hq / Hkv);
     const size_t U = (size_t)B * Hkv;
-    w.row_cap = rows < kTile ? (int)((rows + 7) / 8 * 8) : kTile;
+    w.row_cap = rows < kRows ? (int)((rows + 7) / 8 * 8) : kRows;
     w.max_items = Hkv * ((rows + kItemRows - 1) / kItemRows);
     w.slots = kGridCap + w.max_items;
     size_t at = 256;
@@ -120,7 +123,7 @@ struct Params {
 };
 
 // An item's weight: its tiles take two row tiles' products or one.
-__device__ __forceinline__ int weight_of(int rows) { return rows > kTile ? 2 : 1; }
+__device__ __forceinline__ int weight_of(int rows) { return rows > kRows ? 2 : 1; }
 
 // Cost of n tiles of weight 1, even, so that with even shares no tile of weight 2
 // lies across two shares.
@@ -306,18 +309,39 @@ struct Streams {
     int n;
     __device__ __forceinline__ int steps(int s) const { return two ? n : (n + 1 - s) / 2; }
     __device__ __forceinline__ int tile(int s, int t) const { return two ? t : 2 * t + s; }
-    // Places of tile j's keys and values in the segment's sequence of copies, which
-    // is the order of their first use.
-    __device__ __forceinline__ int key_at(int j) const { return two ? 2 * j : (j ? 2 * j - 1 : 0); }
-    __device__ __forceinline__ int value_at(int j) const { return two ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
 };
 
+// Copies come in the order of their first use: the keys of a stream's first two
+// steps, then each step's values and the keys of the step after next. Places of
+// step t's keys and values in that sequence of 2 * steps copies.
+__device__ __forceinline__ int key_at(int t) { return t < 2 ? t : 2 * t - 1; }
+__device__ __forceinline__ int value_at(int t, int steps) { return min(2, steps) + t + min(t, max(steps - 2, 0)); }
+
+// The stages form two rings of kRing. Streams over the same tiles share one
+// sequence, whose copies alternate between the rings; streams over alternate tiles
+// have a ring each. So whoever waits for a ring waits for its copies in order, and a
+// barrier's parity is never two phases off.
+constexpr int kRing = kStages / 2;
+
+struct Place {
+    uint32_t stage, parity;
+};
+
+__device__ __forceinline__ Place place_of(bool two, int s, int at, uint32_t used0, uint32_t used1)
+{
+    const int ring = two ? at & 1 : s;
+    const uint32_t i = (ring ? used1 : used0) + (two ? at >> 1 : at);
+    return {ring * kRing + i % kRing, (i / kRing) & 1};
+}
+
 struct Shared {
-    uint64_t full[kStages], empty[kStages], q_full, s_full[2], p_full[2][2], o_full[2], seg_done, drain;
+    uint64_t full[kStages], empty[kStages];
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2]; // stream, step parity
+    uint64_t q_full, seg_done, drain[2];
     uint32_t tmem;
     int abort_flag;
 };
-static_assert(sizeof(Shared) <= 256, "barrier block");
+static_assert(sizeof(Shared) <= 512, "barrier block");
 
 __global__ void __launch_bounds__(kThreads, 1)
 scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
@@ -334,17 +358,17 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 2); // one arrival a stream, or two of the one that used the tile
         }
-        mbar_init(q_full, kSoftmaxThreads);
-        mbar_init(seg_done, kSoftmaxThreads);
-        mbar_init(smem_u32(&sh->drain), 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(s_full + 8 * s, 1);
-            mbar_init(p_full + 16 * s, kTile);
-            mbar_init(p_full + 16 * s + 8, kTile);
-            mbar_init(o_full + 8 * s, 1);
+        mbar_init(q_full, kSoftmaxWarps);
+        mbar_init(seg_done, kSoftmaxWarps);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, kSoftmaxWarps / 2);
+            mbar_init(o_full + 8 * i, 1);
         }
+        mbar_init(smem_u32(&sh->drain[0]), 1);
+        mbar_init(smem_u32(&sh->drain[1]), 1);
         sh->abort_flag = 0;
         fence_mbar_init();
     }
@@ -366,16 +390,16 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     bool ok = true;
 
     if (warp >= 8) {
-        regs_dec<88>();
+        regs_dec<120>();
         // Both warps run converged and elect the issuing lane at each issue: the
         // instructions take their descriptors from uniform registers, which code
         // under a divergent branch has to fill one by one.
         if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
-            uint32_t pos = 0; // copies issued
-            auto copy = [&](const CUtensorMap *map, int g, int j) -> bool {
-                const uint32_t st = pos % kStages;
-                if (!wait_warp(empty0 + 8 * st, ((pos / kStages) & 1) ^ 1, abort_flag))
+            uint32_t used0 = 0, used1 = 0; // copies issued to each ring
+            auto copy = [&](const CUtensorMap *map, int ring, int g, int j) -> bool {
+                const uint32_t i = ring ? used1 : used0, st = ring * kRing + i % kRing;
+                if (!wait_warp(empty0 + 8 * st, ((i / kRing) & 1) ^ 1, abort_flag))
                     return false;
                 const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem + kOffRing + st * kTileBytes);
                 if (elect_one()) {
@@ -384,124 +408,128 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     tma_load_3d_plain(dst + kHalfBytes, map, fb, 64, j * kTile, g);
                 }
                 __syncwarp();
-                ++pos;
+                ++(ring ? used1 : used0);
                 return true;
             };
             while (ok && walk.next(seg)) {
-                const int4 it = seg.it;
-                const int n = seg.j1 - seg.j0;
-                if (it.z > kTile) {
-                    for (int j = 0; ok && j < n; ++j)
-                        ok = copy(&tmK, it.x, seg.j0 + j) && copy(&tmV, it.x, seg.j0 + j);
-                } else {
-                    ok = copy(&tmK, it.x, seg.j0);
-                    for (int j = 0; ok && j < n; ++j)
-                        ok = (j + 1 >= n || copy(&tmK, it.x, seg.j0 + j + 1)) && copy(&tmV, it.x, seg.j0 + j);
+                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+                const int g = seg.it.x, lead = st.two ? 2 : 4;
+                // Shared sequence: copy i goes to ring i % 2 (keys 0, keys 1, then values
+                // j and keys j + 2: rings 0 and 1). Alternate tiles: tile j to ring j % 2.
+                for (int j = 0; ok && j < min(lead, st.n); ++j)
+                    ok = copy(&tmK, j & 1, g, seg.j0 + j);
+                for (int j = 0; ok && j < st.n; ++j) {
+                    const int at = value_at(j, st.n);
+                    ok = copy(&tmV, (st.two ? at : j) & 1, g, seg.j0 + j) &&
+                         (j + lead >= st.n || copy(&tmK, (st.two ? at + 1 : j) & 1, g, seg.j0 + j + lead));
                 }
             }
             // Copies in flight land before the CTA can leave.
             volatile int never = 0;
             if (!ok)
-                for (uint32_t i = pos > kStages ? pos - kStages : 0; i < pos; ++i)
-                    (void)wait_bar(full0 + 8 * (i % kStages), (i / kStages) & 1, &never);
-        } else if (warp == kMmaWarp) {
+                for (int ring = 0; ring < 2; ++ring) {
+                    const uint32_t n = ring ? used1 : used0;
+                    for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
+                        (void)wait_bar(full0 + 8 * (ring * kRing + i % kRing), (i / kRing) & 1, &never);
+                }
+        } else if (warp <= kMmaWarp + 1) {
             // -------------------------------------------------------------- MMAs
-            constexpr uint32_t kIdescS = bf16_idesc(kTile, kTile, false), kIdescO = bf16_idesc(kTile, kHeadDim, true);
-            uint32_t base = 0, nseg = 0; // copies of earlier segments; segments
-            uint32_t np0 = 0, np1 = 0;       // P tiles consumed by each stream
-            auto ring = [&](uint32_t at) { return smem_u32(smem + kOffRing + (at % kStages) * kTileBytes); };
-            auto full = [&](uint32_t at) { return wait_warp(full0 + 8 * (at % kStages), (at / kStages) & 1, abort_flag); };
+            constexpr uint32_t kIdescS = bf16_idesc(kRows, kTile, false), kIdescO = bf16_idesc(kRows, kHeadDim, true);
+            const int s = warp - kMmaWarp;
+            const uint32_t tO = tmem + 256 + s * 128, sq = smem_u32(smem + kOffQ + s * kQBytes);
+            const uint32_t drain = smem_u32(&sh->drain[s]);
+            uint32_t used0 = 0, used1 = 0, nseg = 0; // copies of earlier segments in each ring; segments
+            uint32_t done0 = 0, done1 = 0; // steps of earlier segments, by their parity
             while (ok && walk.next(seg)) {
-                const int4 it = seg.it;
-                const Streams st{it.z > kTile, seg.j1 - seg.j0};
+                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+                const int steps = st.steps(s);
                 if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
                     break;
                 tc_fence_after();
-                // S of stream s, step t
-                auto logits = [&](int s, int t) -> bool {
-                    const uint32_t at = base + st.key_at(st.tile(s, t));
-                    if (!full(at))
+                // S of step t into its buffer
+                auto logits = [&](int t) -> bool {
+                    const auto [stage, parity] = place_of(st.two, s, key_at(t), used0, used1);
+                    const uint64_t a = smem_desc_sw128(sq, 16, 1024);
+                    const uint64_t b = smem_desc_sw128(smem_u32(smem + kOffRing + stage * kTileBytes), 16, 1024);
+                    const uint32_t d = tmem + s * 128 + (t & 1) * 64, sf = s_full + 16 * s + 8 * (t & 1);
+                    if (!wait_warp(full0 + 8 * stage, parity, abort_flag))
                         return false;
-                    const uint64_t a = smem_desc_sw128(smem_u32(smem + kOffQ + s * kTileBytes), 16, 1024);
-                    const uint64_t b = smem_desc_sw128(ring(at), 16, 1024);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) { // 16 of the 128 dimensions each
-                            const uint64_t off = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-                            mma_ss(tmem + s * 128, a + off, b + off, kIdescS, k > 0);
-                        }
-                        mma_commit(s_full + 8 * s);
-                        if (!st.two || s == 1)
-                            mma_commit(empty0 + 8 * (at % kStages));
+                        for (int k = 0; k < 8; ++k) // 16 of the 128 dimensions each
+                            mma_ss(d, a + (k >> 2) * (kQHalfBytes >> 4) + (k & 3) * 2,
+                                   b + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2, kIdescS, k > 0);
+                        mma_commit(sf);
+                        mma_commit(empty0 + 8 * stage);
+                        if (!st.two)
+                            mma_commit(empty0 + 8 * stage);
                     }
                     __syncwarp();
                     return true;
                 };
-                // O of stream s += P V, step t
-                auto output = [&](int s, int t) -> bool {
-                    const uint32_t at = base + st.value_at(st.tile(s, t));
-                    if (!full(at))
-                        return false;
-                    const uint64_t b = smem_desc_sw128(ring(at), kHalfBytes, 1024);
+                ok = (steps < 1 || logits(0)) && (steps < 2 || logits(1));
+                for (int t = 0; ok && t < steps; ++t) {
+                    // O += P V of step t
+                    const auto [stage, parity] = place_of(st.two, s, value_at(t, steps), used0, used1);
+                    const uint64_t b = smem_desc_sw128(smem_u32(smem + kOffRing + stage * kTileBytes), kHalfBytes, 1024);
+                    const uint32_t a = tmem + s * 128 + (t & 1) * 64, bars = 16 * s + 8 * (t & 1);
+                    if (!(ok = wait_warp(full0 + 8 * stage, parity, abort_flag) &&
+                               wait_warp(p_full + bars, (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)))
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) { // P comes in two halves
-                        if (!wait_warp(p_full + 16 * s + 8 * h, (s ? np1 : np0) & 1, abort_flag))
-                            return false;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 4 * h; k < 4 * h + 4; ++k) // 16 positions each
-                                mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, b + k * (2048 >> 4), kIdescO,
-                                       t > 0 || k > 0);
-                            if (h == 1) {
-                                if (!st.two || s == 1)
-                                    mma_commit(empty0 + 8 * (at % kStages));
-                                if (t + 1 == st.steps(s))
-                                    mma_commit(o_full + 8 * s);
-                            }
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < kTile / 16; ++k) // 16 positions each
+                            mma_ts(tO, a + k * 8, b + k * (2048 >> 4), kIdescO, t > 0 || k > 0);
+                        mma_commit(o_full + bars);
+                        mma_commit(empty0 + 8 * stage);
+                        if (!st.two)
+                            mma_commit(empty0 + 8 * stage);
                     }
-                    ++(s ? np1 : np0);
-                    return true;
-                };
-                ok = logits(0, 0) && (st.steps(1) == 0 || logits(1, 0));
-                for (int t = 0; ok && t < st.steps(0); ++t) {
-                    ok = output(0, t) && (t + 1 >= st.steps(0) || logits(0, t + 1));
-                    if (ok && t < st.steps(1))
-                        ok = output(1, t) && (t + 1 >= st.steps(1) || logits(1, t + 1));
+                    __syncwarp();
+                    if (t + 2 < steps)
+                        ok = logits(t + 2);
                 }
-                base += 2 * (uint32_t)st.n;
+                used0 += (uint32_t)(st.two ? st.n : 2 * st.steps(0));
+                used1 += (uint32_t)(st.two ? st.n : 2 * st.steps(1));
+                done0 += (steps + 1) / 2;
+                done1 += steps / 2;
                 ++nseg;
             }
             if (!ok) { // MMAs in flight finish before TMEM is given back
                 volatile int never = 0;
                 if (elect_one())
-                    mma_commit(smem_u32(&sh->drain));
+                    mma_commit(drain);
                 __syncwarp();
-                (void)wait_bar(smem_u32(&sh->drain), 0, &never);
+                (void)wait_bar(drain, 0, &never);
             }
         }
     } else {
         // ------------------------------------------------------------ softmax
-        regs_inc<208>();
-        const int s = warp >> 2, row = tid & (kTile - 1); // stream, row of its tile
+        regs_inc<192>();
+        const int s = warp >> 2, row = tid & (kRows - 1); // stream, row of its tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // this warp's TMEM lanes
-        const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
-        uint32_t ns = 0, no = 0, nseg = 0; // S tiles, O results and segments consumed
+        const uint32_t tO = tmem + 256 + s * 128 + lanes;
+        uint32_t done0 = 0, done1 = 0, nseg = 0; // steps of earlier segments, by their parity; segments
+        auto arrive = [&](uint32_t bar) { // one arrival a warp, behind every lane's work
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
         while (walk.next(seg)) {
             const int4 it = seg.it;
-            const Streams st{it.z > kTile, seg.j1 - seg.j0};
+            const Streams st{it.z > kRows, seg.j1 - seg.j0};
             // Row of the item in this thread's lane. With at most 64 rows the second
             // stream's start at lane 64, so that the streams' rows fall to different
             // schedulers.
-            const int turn = !st.two && it.z <= kTile / 2 ? s * (kTile / 2) : 0;
-            const int qrow = st.two ? s * kTile + row : (row + kTile - turn) % kTile;
+            const int turn = !st.two && it.z <= kRows / 2 ? s * (kRows / 2) : 0;
+            const int qrow = st.two ? s * kRows + row : (row + kRows - turn) % kRows;
             const bool mine = qrow < it.z;
             const bool busy = __any_sync(kFull, mine); // a warp without a row only keeps the barriers' count
             // Every earlier MMA that read Q is complete (both groups have met below).
             {
-                uint4 *dst = reinterpret_cast<uint4 *>(smem + kOffQ + s * kTileBytes);
+                uint4 *dst = reinterpret_cast<uint4 *>(smem + kOffQ + s * kQBytes);
                 const uint4 *src = nullptr;
                 if (mine) {
                     const int r = it.y + qrow, a = r / p.M;
@@ -512,36 +540,35 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint4 x = src ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    dst[(c >> 3) * (kHalfBytes / 16) + row * 8 + ((c & 7) ^ (row & 7))] = x;
+                    dst[(c >> 3) * (kQHalfBytes / 16) + row * 8 + ((c & 7) ^ (row & 7))] = x;
                 }
                 fence_proxy_async_smem();
             }
-            tc_fence_before();
-            mbar_arrive(q_full);
+            arrive(q_full);
 
             float m = -INFINITY, l = 0.f; // m in the logits' units
             const int steps = st.steps(s);
             for (int t = 0; t < steps; ++t) {
-                if (!wait_warp(s_full + 8 * s, ns & 1, abort_flag)) {
+                const uint32_t bars = 16 * s + 8 * (t & 1);
+                const uint32_t tS = tmem + s * 128 + (t & 1) * 64 + lanes;
+                if (!wait_warp(s_full + bars, (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                ++ns;
                 if (!busy) {
-                    mbar_arrive(p_full + 16 * s);
-                    mbar_arrive(p_full + 16 * s + 8);
+                    arrive(p_full + bars);
                     continue;
                 }
                 tc_fence_after();
-                uint32_t x[4][32];
+                uint32_t x[2][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
                     tmem_ld32(x[c], tS + 32 * c);
                 tmem_wait_ld();
                 const int left = p.prefix_len - (seg.j0 + st.tile(s, t)) * kTile;
                 if (left < kTile) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i >= left)
@@ -550,62 +577,65 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = max_nan(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+                    const uint32_t *q = &x[c >> 1][(c & 1) * 16];
+                    mx[c] = max_nan(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]));
 #pragma unroll
-                    for (int i = 3; i < 31; i += 2)
-                        mx[c] = max_nan(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                    for (int i = 3; i < 15; i += 2)
+                        mx[c] = max_nan(mx[c], __uint_as_float(q[i]), __uint_as_float(q[i + 1]));
+                    mx[c] = max_nan(mx[c], mx[c], __uint_as_float(q[15]));
                 }
-                float top = max_nan(mx[0], mx[1], __uint_as_float(x[0][31]));
-                top = max_nan(top, mx[2], __uint_as_float(x[1][31]));
-                top = max_nan(top, mx[3], __uint_as_float(x[2][31]));
-                top = max_nan(top, top, __uint_as_float(x[3][31]));
+                const float top = max_nan(max_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
                 if (t == 0) {
                     m = top;
                 } else if (__any_sync(kFull, !((top - m) * kScaleLog2 <= kGrowth))) { // also for a NaN
+                    // The buffer's S means that the product before the last is
+                    // complete; wait for the last one.
+                    const uint32_t prev = 16 * s + 8 * ((t - 1) & 1);
+                    if (!wait_warp(o_full + prev, ((((t - 1) & 1) ? done1 : done0) + ((t - 1) >> 1)) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     const float mn = max_nan(m, top, top);
                     const float f = mn == m ? 1.f : exp2_approx((m - mn) * kScaleLog2);
                     m = mn;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16(o, tO + 16 * c);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o, tO + 32 * c);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < 32; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st16(tO + 16 * c, o);
+                        tmem_st32(tO + 32 * c, o);
                     }
                 }
                 // A row without a finite logit yet keeps weights of 0; an infinite
                 // maximum makes them NaN.
                 const float sub = m == -INFINITY ? 0.f : fmaf(m, kScaleLog2, m - m);
-                const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), sub2 = pack2(-sub, -sub);
+                const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), nsub2 = pack2(-sub, -sub);
                 uint64_t sum[2] = {0ull, 0ull};
+                uint32_t w[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const uint32_t(&src)[32] = x[2 * h + (i >> 4)];
-                        const uint64_t y = fma2(pack2(__uint_as_float(src[(2 * i) & 31]),
-                                                      __uint_as_float(src[(2 * i + 1) & 31])), scale2, sub2);
-                        float a, b;
-                        if ((i & 7) < kPolyOf8) {
-                            exp2_poly2(y, a, b);
-                        } else {
-                            unpack2(y, a, b);
-                            a = exp2_approx(a);
-                            b = exp2_approx(b);
-                        }
-                        sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-                        w[i] = pack_bf16x2(a, b);
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t(&src)[32] = x[i >> 4];
+                    const uint64_t y = fma2(pack2(__uint_as_float(src[(2 * i) & 31]),
+                                                  __uint_as_float(src[(2 * i + 1) & 31])), scale2, nsub2);
+                    float a, b;
+                    if ((i & 7) < kPolyOf8) {
+                        exp2_poly2(y, a, b);
+                    } else {
+                        unpack2(y, a, b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
                     }
-                    tmem_st32(tS + 32 * h, w);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_full + 16 * s + 8 * h);
+                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+                    w[i] = pack_bf16x2(a, b);
                 }
+                tmem_st32(tS, w);
+                tmem_wait_st();
+                arrive(p_full + bars);
                 float s0, s1;
                 unpack2(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
@@ -615,13 +645,13 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             // ---- the segment's partial of this row
             const size_t slot = (size_t)blockIdx.x + seg.item;
             const size_t part = (slot * 2 + s) * p.row_cap;
-            const int prow = qrow % kTile;
+            const int prow = qrow % kRows;
             if (steps > 0) {
-                if (!wait_warp(o_full + 8 * s, no & 1, abort_flag)) {
+                const int t = steps - 1;
+                if (!wait_warp(o_full + 16 * s + 8 * (t & 1), (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                ++no;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -641,7 +671,9 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             if (mine)
                 __stcg(p.ml + part + prow, make_float2(m * kScaleLog2, l));
             // Both groups are done with the segment's Q, S and O.
-            mbar_arrive(seg_done);
+            done0 += (steps + 1) / 2;
+            done1 += steps / 2;
+            arrive(seg_done);
             if (!wait_warp(seg_done, nseg & 1, abort_flag)) {
                 ok = false;
                 break;
@@ -660,14 +692,69 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 // ---- join -------------------------------------------------------------------------------
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinBatch = 8; // partials in flight a thread
 
-// One warp a query head; lane c owns elements 4c .. 4c + 3.
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
+// (m, l, acc) += parts k0, k0 + step, ... below n of `part`, lane c holding columns
+// 4c .. 4c + 3: lane i fetches the batch's i-th (m, l), and the weights reach the
+// other lanes by shuffles. A part with l = 0 has no O.
+template <typename Part>
+__device__ __forceinline__ void add_parts(const Params &p, Part &&part, int pr, int k0, int step, int n, int lane, float &m,
+                                          float &l, float4 &acc)
 {
+    for (; k0 < n; k0 += step * 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (k0 + lane * step < n)
+            ml = __ldcg(p.ml + part(k0 + lane * step) + pr);
+        float mb = ml.y == 0.f ? -INFINITY : ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o));
+        const float mn = fmaxf(m, mb);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - mn);
+        float ls = ml.y * w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            ls += __shfl_xor_sync(kFull, ls, o);
+        l = l * keep + ls;
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+        const int nb = min(32, (n - k0 + step - 1) / step);
+        for (int i0 = 0; i0 < nb; i0 += kJoinBatch) {
+            float4 o[kJoinBatch];
+            float wi[kJoinBatch];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                wi[i] = __shfl_sync(kFull, w, (i0 + i) & 31);
+                if (i0 + i >= nb)
+                    wi[i] = 0.f;
+                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wi[i] != 0.f)
+                    o[i] = __ldcg(reinterpret_cast<const float4 *>(
+                        p.o + part(k0 + (i0 + i) * step) * kHeadDim + ((size_t)(lane >> 1) * p.row_cap + pr) * 8 +
+                        (lane & 1) * 4));
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                acc.x = fmaf(o[i].x, wi[i], acc.x);
+                acc.y = fmaf(o[i].y, wi[i], acc.y);
+                acc.z = fmaf(o[i].z, wi[i], acc.z);
+                acc.w = fmaf(o[i].w, wi[i], acc.w);
+            }
+        }
+        m = mn;
+    }
+}
+
+// One warp a query head, or (kWhole) a CTA of eight, each with every eighth
+// partial; lane c owns elements 4c .. 4c + 3.
+template <bool kWhole> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
+{
+    __shared__ float4 sh_acc[kJoinWarps][32];
+    __shared__ float2 sh_ml[kJoinWarps];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); // b * Hq + h
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = kWhole ? (long long)blockIdx.x : (long long)blockIdx.x * kJoinWarps + warp; // b * Hq + h
     if (row >= (long long)p.B * p.Hq)
         return;
     const int b = (int)(row / p.Hq), h = (int)(row - (long long)b * p.Hq), g = h / p.M;
@@ -686,7 +773,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
             const int r = rank * p.M + (h - g * p.M);
             const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
             const int4 it = __ldcg(p.items + item);
-            const bool two = it.z > kTile;
+            const bool two = it.z > kRows;
             const long long share = share_of(__ldcg(p.weight), nt, p.grid), begin = it.w * item_cost(nt);
             const int c0 = (int)(begin / share);
             const int c1 = (int)((begin + (long long)(nt - 1) * weight_of(it.z)) / share);
@@ -694,45 +781,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
             const int n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
             auto part = [&](int k) -> size_t {
                 const size_t slot = (size_t)(c0 + (two ? k : k >> 1)) + item;
-                return (slot * 2 + (two ? ir / kTile : k & 1)) * p.row_cap;
+                return (slot * 2 + (two ? ir / kRows : k & 1)) * p.row_cap;
             };
-            const int pr = ir % kTile;
-            for (int k0 = 0; k0 < n; k0 += 32) {
-                float2 ml = make_float2(-INFINITY, 0.f);
-                if (k0 + lane < n)
-                    ml = __ldcg(p.ml + part(k0 + lane) + pr);
-                float mb = ml.y == 0.f ? -INFINITY : ml.x; // a stream without a tile has l = 0
+            add_parts(p, part, ir % kRows, kWhole ? warp : 0, kWhole ? kJoinWarps : 1, n, lane, m, l, acc);
+        }
+        if constexpr (kWhole) {
+            sh_acc[warp][lane] = acc;
+            if (lane == 0)
+                sh_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            m = -INFINITY;
+            l = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o));
-                const float mn = fmaxf(m, mb);
-                const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
-                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - mn);
-                float ls = ml.y * w;
+            for (int w = 0; w < kJoinWarps; ++w)
+                m = fmaxf(m, sh_ml[w].x);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    ls += __shfl_xor_sync(kFull, ls, o);
-                l = l * keep + ls;
-                acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-                const int nb = min(32, n - k0);
-#pragma unroll 8
-                for (int k = 0; k < nb; ++k) {
-                    const float wk = __shfl_sync(kFull, w, k);
-                    if (wk != 0.f) { // its O was written
-                        const float4 o = __ldcg(reinterpret_cast<const float4 *>(
-                            p.o + part(k0 + k) * kHeadDim + ((size_t)(lane >> 1) * p.row_cap + pr) * 8 + (lane & 1) * 4));
-                        acc.x = fmaf(o.x, wk, acc.x);
-                        acc.y = fmaf(o.y, wk, acc.y);
-                        acc.z = fmaf(o.z, wk, acc.z);
-                        acc.w = fmaf(o.w, wk, acc.w);
-                    }
-                }
-                m = mn;
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float2 ml = sh_ml[w];
+                const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+                const float4 o = sh_acc[w][lane];
+                l = fmaf(ml.y, f, l);
+                acc.x = fmaf(o.x, f, acc.x);
+                acc.y = fmaf(o.y, f, acc.y);
+                acc.z = fmaf(o.z, f, acc.z);
+                acc.w = fmaf(o.w, f, acc.w);
             }
         }
         // acc and l are in units of 2^m; join the suffix's normalised part
-        lse = nt > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-        float wp = nt > 0 ? 1.f / l : 0.f, ws = 0.f;
+        lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        float wp = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
         float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.o_suffix) {
             const float ls = __ldg(p.lse_suffix + row), top = fmaxf(lse, ls);
@@ -749,6 +827,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
         acc.z = acc.z * wp + os.z * ws;
         acc.w = acc.w * wp + os.w * ws;
     }
+    if (kWhole && warp != 0)
+        return;
     if (p.lse && lane == 0)
         p.lse[row] = lse;
     if (p.out_f32)
@@ -783,6 +863,8 @@ cudaError_t grid_of(int *grid)
     *grid = known[dev];
     return cudaSuccess;
 }
+
+constexpr long long kWholeRows = 1024;
 
 template <typename... Args>
 cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
@@ -851,8 +933,14 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
         e = launch(scan_kernel, (unsigned)p.grid, kThreads, kSmem, stream, tmK, tmV, p);
     }
     if (e == cudaSuccess) {
+        // Few rows have many partials each (the grid is spread over few items): a
+        // CTA a row. 128K prefix, 8 sequences, 74 partials a row: 32 us with a warp a
+        // row, @@ with a CTA.
         const long long rows = (long long)a.batch * a.n_q_heads;
-        e = launch(join_kernel, (unsigned)((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream, p);
+        if (rows <= kWholeRows)
+            e = launch(join_kernel<true>, (unsigned)rows, 32 * kJoinWarps, 0, stream, p);
+        else
+            e = launch(join_kernel<false>, (unsigned)((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream, p);
     }
     return e;
 }
