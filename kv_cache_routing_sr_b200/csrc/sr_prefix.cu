@@ -12,23 +12,29 @@
 //  * plan: one CTA lists the active sequences of each KV head and cuts each head's
 //    rows into items of up to 256.
 //  * scan: one persistent CTA per SM takes a contiguous share of the (item, tile
-//    of 64 positions) sequence, in which a tile weighs 2 for an item of more than
-//    128 rows and 1 for a smaller one, and leaves one partial (m, l, O) a row for
-//    every item its share touches.
-//  * join: one warp a query head combines its partials, and the suffix's.
+//    of positions) sequence, in which a tile weighs 2 for an item of more than 128
+//    rows and 1 for a smaller one, and leaves one partial (m, l, O) a row for every
+//    item its share touches.
+//  * join: one warp (or CTA) a query head combines its partials, and the suffix's.
 //
-// scan, per CTA: two streams, each with a softmax warpgroup (a thread a row), an MMA
-// warp, two buffers for its logits S (128 x 64, fp32) and its output O (128 x 128,
-// fp32), which fill the 512 columns of TMEM; and one copy warp for both. With more
-// than 128 rows the streams are the item's two halves over the same tiles; with
-// fewer they are the same rows over alternate tiles, and leave a partial each. An MMA
-// warp issues S of two tiles and then, tile by tile, O += P V and S of the tile after
-// next, so a warpgroup that hands over P (bf16, written over S) finds the next S
-// ready, and a copied tile is used as soon as it has landed: the ring's ten 16 KB
-// stages are in flight rather than waiting. A warpgroup rescales O only when a
-// row's maximum has grown by more than 2^8 since the reference it uses (the weights
-// stay below 2^8 of their row's sum, far inside bf16 and fp32), after the previous
-// tile's product is complete.
+// scan, per CTA: two streams, each with a softmax warpgroup (a thread a row), its
+// logits S in TMEM (128 x 128 fp32 columns in all) and its output O (128 x 128); a copy
+// warp; and the warps that issue the MMAs. With more than 128 rows the streams are
+// the item's two halves over the same tiles; with fewer they are the same rows over
+// alternate tiles, and leave a partial each. P goes to the second product in bf16,
+// written over S. A warpgroup rescales O only when a row's maximum has grown by more
+// than 2^8 since the reference it uses (the weights stay below 2^8 of their row's sum,
+// far inside bf16 and fp32), once the previous tile's product is complete.
+//
+// It has two forms. Launches of at most 128 rows a KV head are bound by the prefix's
+// bytes: the narrow form works in 64-position tiles with two S buffers a stream and
+// an MMA warp each, so that a copied tile is used as soon as it has landed and the
+// ring's ten 16 KB stages are in flight rather than waiting. More rows are bound by
+// the tensor cores and the exponentials: the wide form works in 128-position tiles
+// (an S product of 128 columns reads Q from shared memory half as often: 75 cycles a
+// 128x128x16 step against 57 a 128x64x16), and one MMA warp issues P0 V, S0 of the
+// next tile, P1 V, S1 of the next tile, which keeps the streams half a turn apart: one
+// has the tensor cores while the other has the exponentials.
 //
 // Every wait is bounded in time; a timeout sets a device error bit, and the CTA
 // leaves once its own copies and MMAs have landed.
@@ -52,25 +58,29 @@ constexpr float kScaleLog2 = 0.12751743082459868f; // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kFull = 0xffffffffu;
 
-constexpr int kTile = 64;            // positions a tile
 constexpr int kRows = 128;           // rows a stream
 constexpr int kItemRows = 2 * kRows; // rows an item
 constexpr int kGridCap = 256;        // persistent CTAs never exceed this (sizes the workspace)
-constexpr int kStages = 10;
-constexpr int kHalfBytes = kTile * 128;       // [64 positions x 64 bf16], 128B swizzle
-constexpr int kTileBytes = 2 * kHalfBytes;    // [64 x 128]
 constexpr int kQHalfBytes = kRows * 128, kQBytes = 2 * kQHalfBytes;
-constexpr int kThreads = 384;                 // two softmax warpgroups, one for copies and MMAs
+
+constexpr int kThreads = 384;        // two softmax warpgroups, one for copies and MMAs
 constexpr int kSoftmaxWarps = 8;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;    // and 10: one a stream
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+
+// The scan's two forms, by the positions of a tile.
+template <int TILE> struct Form {
+    static constexpr int kStages = TILE == 64 ? 10 : 5;
+    static constexpr int kHalfBytes = TILE * 128;      // [TILE positions x 64 bf16], 128B swizzle
+    static constexpr int kTileBytes = 2 * kHalfBytes;  // [TILE x 128]
+    static constexpr int kOffQ = 0, kOffRing = 2 * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
+    static constexpr int kSmem = kOffBar + 512 + 1024; // and room to align the base to 1024 B
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
 #ifndef SR_PREFIX_POLY
 #define SR_PREFIX_POLY 0
 #endif
 constexpr int kPolyOf8 = SR_PREFIX_POLY; // pairs of 8 whose 2^x is a polynomial
 constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
-constexpr int kOffQ = 0, kOffRing = 2 * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
-constexpr int kSmem = kOffBar + 512 + 1024; // and room to align the base to 1024 B
-static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 // Workspace: [error word | total weight | active count, first item of each KV head | active
 // sequences of each head | rank of each unit | items | item at each weight | (m, l) | O]
@@ -120,6 +130,7 @@ struct Params {
     __nv_bfloat16 *out;
     float *out_f32, *lse;
     int B, Hq, Hkv, M, prefix_len, row_cap, grid;
+    int tile; // positions a tile
 };
 
 // An item's weight: its tiles take two row tiles' products or one.
@@ -279,7 +290,7 @@ struct Walk {
     int nt;
     __device__ __forceinline__ Walk(const Params &p_) : p(p_)
     {
-        nt = (p.prefix_len + kTile - 1) / kTile;
+        nt = (p.prefix_len + p.tile - 1) / p.tile;
         cost = item_cost(nt);
         const int weight = __ldcg(p.weight);
         const long long share = share_of(weight, nt, gridDim.x);
@@ -311,21 +322,24 @@ struct Streams {
     __device__ __forceinline__ int tile(int s, int t) const { return two ? t : 2 * t + s; }
 };
 
-// Copies come in the order of their first use: the keys of a stream's first two
-// steps, then each step's values and the keys of the step after next. Places of
-// step t's keys and values in that sequence of 2 * steps copies.
-__device__ __forceinline__ int key_at(int t) { return t < 2 ? t : 2 * t - 1; }
-__device__ __forceinline__ int value_at(int t, int steps) { return min(2, steps) + t + min(t, max(steps - 2, 0)); }
+// Copies come in the order of their first use: the keys of the first `look` steps (or
+// tiles), then each one's values and the next keys. Places of the keys and values of
+// step t of n in that sequence of 2 n copies.
+__device__ __forceinline__ int key_at(int look, int t) { return t < look ? t : 2 * t + 1 - look; }
+__device__ __forceinline__ int value_at(int look, int t, int n)
+{
+    return min(look, n) + t + min(t, max(n - look, 0));
+}
 
-// The stages form two rings of kRing. Streams over the same tiles share one
-// sequence, whose copies alternate between the rings; streams over alternate tiles
-// have a ring each. So whoever waits for a ring waits for its copies in order, and a
-// barrier's parity is never two phases off.
-constexpr int kRing = kStages / 2;
-
+// Narrow form: the stages form two rings. Streams over the same tiles share one sequence, whose
+// copies alternate between the rings; streams over alternate tiles have a ring each.
+// So whoever waits for a ring waits for its copies in order, and a barrier's parity
+// is never two phases off.
 struct Place {
     uint32_t stage, parity;
 };
+
+constexpr int kRing = Form<64>::kStages / 2;
 
 __device__ __forceinline__ Place place_of(bool two, int s, int at, uint32_t used0, uint32_t used1)
 {
@@ -334,47 +348,53 @@ __device__ __forceinline__ Place place_of(bool two, int s, int at, uint32_t used
     return {ring * kRing + i % kRing, (i / kRing) & 1};
 }
 
+// Narrow form: the barrier that step t of stream s uses, of the pair that its steps
+// use in turn, as a byte offset, and the parity of its phase. done: steps of earlier
+// segments on each of the pair.
+struct Turn {
+    uint32_t off, parity;
+};
+__device__ __forceinline__ Turn turn_of(int s, int t, uint32_t done0, uint32_t done1)
+{
+    return {(uint32_t)(16 * s + 8 * (t & 1)), (((t & 1) ? done1 : done0) + (t >> 1)) & 1};
+}
+
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t s_full[2][2], p_full[2][2], o_full[2][2]; // stream, step parity
+    uint64_t full[10], empty[10];
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2]; // stream; step parity (narrow) or half of P (wide)
     uint64_t q_full, seg_done, drain[2];
     uint32_t tmem;
     int abort_flag;
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
 
-__global__ void __launch_bounds__(kThreads, 1)
-scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
+// Barriers, TMEM and the dependency on the plan; returns the TMEM base.
+template <int TILE>
+__device__ __forceinline__ uint32_t scan_prologue(Shared *sh, const CUtensorMap *tmK, const CUtensorMap *tmV, int warp,
+                                                  int lane)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared *sh = reinterpret_cast<Shared *>(smem + kOffBar);
-    volatile int *abort_flag = &sh->abort_flag;
-    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
-    const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty), q_full = smem_u32(&sh->q_full);
-    const uint32_t s_full = smem_u32(sh->s_full), p_full = smem_u32(sh->p_full), o_full = smem_u32(sh->o_full);
-    const uint32_t seg_done = smem_u32(&sh->seg_done);
-
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 2); // one arrival a stream, or two of the one that used the tile
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Form<TILE>::kStages; ++s) {
+            mbar_init(smem_u32(&sh->full[s]), 1);
+            // narrow: one arrival a stream, or two of the one that used the tile
+            mbar_init(smem_u32(&sh->empty[s]), TILE == 64 ? 2 : 1);
         }
-        mbar_init(q_full, kSoftmaxWarps);
-        mbar_init(seg_done, kSoftmaxWarps);
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, kSoftmaxWarps / 2);
-            mbar_init(o_full + 8 * i, 1);
+        mbar_init(smem_u32(&sh->q_full), kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->seg_done), kSoftmaxWarps);
+        for (int s = 0; s < 2; ++s) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&sh->s_full[s][i]), 1);
+                mbar_init(smem_u32(&sh->p_full[s][i]), kSoftmaxWarps / 2);
+                mbar_init(smem_u32(&sh->o_full[s][i]), 1);
+            }
+            mbar_init(smem_u32(&sh->drain[s]), 1);
         }
-        mbar_init(smem_u32(&sh->drain[0]), 1);
-        mbar_init(smem_u32(&sh->drain[1]), 1);
         sh->abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kCopyWarp && lane == 0) {
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
+        prefetch_tensormap(tmK);
+        prefetch_tensormap(tmV);
     }
     if (warp == kMmaWarp)
         tmem_alloc(smem_u32(&sh->tmem), 512);
@@ -384,16 +404,217 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     const uint32_t tmem = sh->tmem;
     grid_dependency_wait();
     grid_launch_dependents();
+    return tmem;
+}
+
+// All warps: a timeout is reported, TMEM given back.
+__device__ __forceinline__ void scan_epilogue(const Params &p, bool ok, uint32_t tmem, int warp, int lane)
+{
+    if (!ok && lane == 0)
+        atomicOr(p.err, SR_DEVERR_TIMEOUT);
+    __syncthreads();
+    __syncwarp();
+    if (warp == kMmaWarp)
+        tmem_dealloc(tmem, 512);
+}
+
+// A warp's MMAs in flight finish before it leaves on a timeout.
+__device__ __forceinline__ void drain_mmas(uint32_t bar)
+{
+    volatile int never = 0;
+    if (elect_one())
+        mma_commit(bar);
+    __syncwarp();
+    (void)wait_bar(bar, 0, &never);
+}
+
+// One arrival a warp, behind every lane's work (a lane's own arrival each would be
+// served one after another).
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane)
+{
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar);
+}
+
+// The two 64-column boxes of TILE positions into a stage.
+template <int TILE>
+__device__ __forceinline__ void copy_tile(uint8_t *smem, const CUtensorMap *map, uint32_t stage, uint32_t full_bar, int j, int g)
+{
+    using F = Form<TILE>;
+    const uint32_t dst = smem_u32(smem + F::kOffRing + stage * F::kTileBytes);
+    if (elect_one()) {
+        mbar_arrive_expect_tx(full_bar, F::kTileBytes);
+        tma_load_3d_plain(dst, map, full_bar, 0, j * TILE, g);
+        tma_load_3d_plain(dst + F::kHalfBytes, map, full_bar, 64, j * TILE, g);
+    }
+    __syncwarp();
+}
+
+// S[128 x TILE] = Q K^T, the elected lane.
+template <int TILE> __device__ __forceinline__ void issue_logits(uint32_t d, uint32_t sq, uint32_t sk)
+{
+    const uint64_t a = smem_desc_sw128(sq, 16, 1024), b = smem_desc_sw128(sk, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) // 16 of the 128 dimensions each
+        mma_ss(d, a + (k >> 2) * (kQHalfBytes >> 4) + (k & 3) * 2, b + (k >> 2) * (Form<TILE>::kHalfBytes >> 4) + (k & 3) * 2,
+               bf16_idesc(kRows, TILE, false), k > 0);
+}
+
+// O[128 x 128] (+)= P V over 64 positions, from position 64 * h of the tile on; the
+// elected lane.
+template <int TILE> __device__ __forceinline__ void issue_output(uint32_t d, uint32_t tp, uint32_t sv, int h, bool accumulate)
+{
+    const uint64_t b = smem_desc_sw128(sv, Form<TILE>::kHalfBytes, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) // 16 positions each
+        mma_ts(d, tp + h * 32 + k * 8, b + (4 * h + k) * (2048 >> 4), bf16_idesc(kRows, kHeadDim, true), accumulate || k > 0);
+}
+
+// The row of a segment's item in a softmax thread's lane (past the item: none). Narrow
+// streams of at most 64 rows: the second stream's start at lane 64, so that the
+// streams' rows fall to different schedulers.
+__device__ __forceinline__ int row_of(bool two, int rows, int s, int row)
+{
+    const int shift = !two && rows <= kRows / 2 ? s * (kRows / 2) : 0;
+    return two ? s * kRows + row : (row + kRows - shift) % kRows;
+}
+
+// Stages this thread's query row (zeros for none) in stream s's swizzled tile.
+__device__ __forceinline__ void stage_query(const Params &p, uint8_t *tile, const int4 &it, int qrow, int row)
+{
+    uint4 *dst = reinterpret_cast<uint4 *>(tile);
+    const uint4 *src = nullptr;
+    if (qrow < it.z) {
+        const int r = it.y + qrow, a = r / p.M;
+        const int b = __ldcg(p.list + (size_t)it.x * p.B + a);
+        src = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.Hq + (size_t)it.x * p.M + (r - a * p.M)) * kHeadDim);
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const uint4 x = src ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        dst[(c >> 3) * (kQHalfBytes / 16) + row * 8 + ((c & 7) ^ (row & 7))] = x;
+    }
+    fence_proxy_async_smem();
+}
+
+// Logits behind the prefix count as -inf: columns c >= left of N.
+template <int N> __device__ __forceinline__ void mask_columns(uint32_t (&x)[N / 32][32], int left)
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        if (c >= left)
+            x[c / 32][c % 32] = 0xff800000u;
+}
+
+// Largest of N logits, NaN if one is.
+template <int N> __device__ __forceinline__ float largest(const uint32_t (&x)[N / 32][32])
+{
+    float mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        auto at = [&](int i) { return __uint_as_float(x[(c * (N / 4) + i) / 32][(c * (N / 4) + i) % 32]); };
+        mx[c] = max_nan(at(0), at(1), at(2));
+#pragma unroll
+        for (int i = 3; i + 1 < N / 4; i += 2)
+            mx[c] = max_nan(mx[c], at(i), at(i + 1));
+        mx[c] = max_nan(mx[c], mx[c], at(N / 4 - 1));
+    }
+    return max_nan(max_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+}
+
+// A row's reference m takes its new largest logit: l and O follow it.
+__device__ __forceinline__ void raise_reference(float top, float &m, float &l, uint32_t tO)
+{
+    const float mn = max_nan(m, top, top);
+    const float f = mn == m ? 1.f : exp2_approx((m - mn) * kScaleLog2);
+    m = mn;
+    l *= f;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(o, tO + 16 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st16(tO + 16 * c, o);
+    }
+}
+
+// Weights 2^(s * scale - sub) of 64 logits as bf16 pairs, and their fp32 sum.
+__device__ __forceinline__ float weights64(const uint32_t (&x0)[32], const uint32_t (&x1)[32], float sub, uint32_t (&w)[32])
+{
+    const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), nsub2 = pack2(-sub, -sub);
+    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t(&src)[32] = i < 16 ? x0 : x1;
+        const uint64_t y =
+            fma2(pack2(__uint_as_float(src[(2 * i) & 31]), __uint_as_float(src[(2 * i + 1) & 31])), scale2, nsub2);
+        float a, b;
+        if ((i & 7) < kPolyOf8) {
+            exp2_poly2(y, a, b);
+        } else {
+            unpack2(y, a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+        }
+        sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+        w[i] = pack_bf16x2(a, b);
+    }
+    float s0, s1;
+    unpack2(add2(sum[0], sum[1]), s0, s1);
+    return s0 + s1;
+}
+
+// What the weights' exponents are taken against. A row without a finite logit yet
+// keeps weights of 0; an infinite maximum makes them NaN.
+__device__ __forceinline__ float subtrahend(float m) { return m == -INFINITY ? 0.f : fmaf(m, kScaleLog2, m - m); }
+
+// The segment's O of a row: eight elements a row and block of 16.
+__device__ __forceinline__ void store_partial(const Params &p, size_t part, uint32_t tO, int prow, bool mine)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o, tO + 32 * c);
+        tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                __stcg(reinterpret_cast<float4 *>(p.o + part * kHeadDim +
+                                                  ((size_t)(4 * c + (i >> 1)) * p.row_cap + prow) * 8 + (i & 1) * 4),
+                       make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
+{
+    using F = Form<64>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared *sh = reinterpret_cast<Shared *>(smem + F::kOffBar);
+    volatile int *abort_flag = &sh->abort_flag;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+    const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty), q_full = smem_u32(&sh->q_full);
+    const uint32_t s_full = smem_u32(sh->s_full), p_full = smem_u32(sh->p_full), o_full = smem_u32(sh->o_full);
+    const uint32_t seg_done = smem_u32(&sh->seg_done);
+    const uint32_t tmem = scan_prologue<64>(sh, &tmK, &tmV, warp, lane);
 
     Walk walk(p);
     Segment seg;
     bool ok = true;
 
-    if (warp >= 8) {
+    // The copy and MMA warps run converged and elect the issuing lane at each issue:
+    // the instructions take their descriptors from uniform registers, which code under
+    // a divergent branch has to fill one by one.
+    if (warp >= kSoftmaxWarps) {
         regs_dec<120>();
-        // Both warps run converged and elect the issuing lane at each issue: the
-        // instructions take their descriptors from uniform registers, which code
-        // under a divergent branch has to fill one by one.
         if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             uint32_t used0 = 0, used1 = 0; // copies issued to each ring
@@ -401,25 +622,19 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 const uint32_t i = ring ? used1 : used0, st = ring * kRing + i % kRing;
                 if (!wait_warp(empty0 + 8 * st, ((i / kRing) & 1) ^ 1, abort_flag))
                     return false;
-                const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem + kOffRing + st * kTileBytes);
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(fb, kTileBytes);
-                    tma_load_3d_plain(dst, map, fb, 0, j * kTile, g);
-                    tma_load_3d_plain(dst + kHalfBytes, map, fb, 64, j * kTile, g);
-                }
-                __syncwarp();
+                copy_tile<64>(smem, map, st, full0 + 8 * st, j, g);
                 ++(ring ? used1 : used0);
                 return true;
             };
             while (ok && walk.next(seg)) {
                 const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
                 const int g = seg.it.x, lead = st.two ? 2 : 4;
-                // Shared sequence: copy i goes to ring i % 2 (keys 0, keys 1, then values
-                // j and keys j + 2: rings 0 and 1). Alternate tiles: tile j to ring j % 2.
+                // Shared sequence: copy i goes to ring i % 2. Alternate tiles: tile j to
+                // ring j % 2.
                 for (int j = 0; ok && j < min(lead, st.n); ++j)
                     ok = copy(&tmK, j & 1, g, seg.j0 + j);
                 for (int j = 0; ok && j < st.n; ++j) {
-                    const int at = value_at(j, st.n);
+                    const int at = value_at(2, j, st.n);
                     ok = copy(&tmV, (st.two ? at : j) & 1, g, seg.j0 + j) &&
                          (j + lead >= st.n || copy(&tmK, (st.two ? at + 1 : j) & 1, g, seg.j0 + j + lead));
                 }
@@ -433,58 +648,48 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                         (void)wait_bar(full0 + 8 * (ring * kRing + i % kRing), (i / kRing) & 1, &never);
                 }
         } else if (warp <= kMmaWarp + 1) {
-            // -------------------------------------------------------------- MMAs
-            constexpr uint32_t kIdescS = bf16_idesc(kRows, kTile, false), kIdescO = bf16_idesc(kRows, kHeadDim, true);
+            // ---------------------------------------------- MMAs, a warp a stream
             const int s = warp - kMmaWarp;
-            const uint32_t tO = tmem + 256 + s * 128, sq = smem_u32(smem + kOffQ + s * kQBytes);
-            const uint32_t drain = smem_u32(&sh->drain[s]);
+            const uint32_t tO = tmem + 256 + s * 128, sq = smem_u32(smem + F::kOffQ + s * kQBytes);
             uint32_t used0 = 0, used1 = 0, nseg = 0; // copies of earlier segments in each ring; segments
-            uint32_t done0 = 0, done1 = 0; // steps of earlier segments, by their parity
+            uint32_t done0 = 0, done1 = 0;           // steps of earlier segments, by their parity
             while (ok && walk.next(seg)) {
                 const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
                 const int steps = st.steps(s);
                 if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
                     break;
                 tc_fence_after();
+                auto release = [&](uint32_t stage) {
+                    mma_commit(empty0 + 8 * stage);
+                    if (!st.two)
+                        mma_commit(empty0 + 8 * stage);
+                };
                 // S of step t into its buffer
                 auto logits = [&](int t) -> bool {
-                    const auto [stage, parity] = place_of(st.two, s, key_at(t), used0, used1);
-                    const uint64_t a = smem_desc_sw128(sq, 16, 1024);
-                    const uint64_t b = smem_desc_sw128(smem_u32(smem + kOffRing + stage * kTileBytes), 16, 1024);
-                    const uint32_t d = tmem + s * 128 + (t & 1) * 64, sf = s_full + 16 * s + 8 * (t & 1);
+                    const auto [stage, parity] = place_of(st.two, s, key_at(2, t), used0, used1);
                     if (!wait_warp(full0 + 8 * stage, parity, abort_flag))
                         return false;
                     if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) // 16 of the 128 dimensions each
-                            mma_ss(d, a + (k >> 2) * (kQHalfBytes >> 4) + (k & 3) * 2,
-                                   b + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2, kIdescS, k > 0);
-                        mma_commit(sf);
-                        mma_commit(empty0 + 8 * stage);
-                        if (!st.two)
-                            mma_commit(empty0 + 8 * stage);
+                        issue_logits<64>(tmem + s * 128 + (t & 1) * 64, sq, smem_u32(smem + F::kOffRing + stage * F::kTileBytes));
+                        mma_commit(s_full + turn_of(s, t, done0, done1).off);
+                        release(stage);
                     }
                     __syncwarp();
                     return true;
                 };
                 ok = (steps < 1 || logits(0)) && (steps < 2 || logits(1));
                 for (int t = 0; ok && t < steps; ++t) {
-                    // O += P V of step t
-                    const auto [stage, parity] = place_of(st.two, s, value_at(t, steps), used0, used1);
-                    const uint64_t b = smem_desc_sw128(smem_u32(smem + kOffRing + stage * kTileBytes), kHalfBytes, 1024);
-                    const uint32_t a = tmem + s * 128 + (t & 1) * 64, bars = 16 * s + 8 * (t & 1);
+                    const auto [stage, parity] = place_of(st.two, s, value_at(2, t, steps), used0, used1);
+                    const Turn turn = turn_of(s, t, done0, done1);
                     if (!(ok = wait_warp(full0 + 8 * stage, parity, abort_flag) &&
-                               wait_warp(p_full + bars, (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)))
+                               wait_warp(p_full + turn.off, turn.parity, abort_flag)))
                         break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k) // 16 positions each
-                            mma_ts(tO, a + k * 8, b + k * (2048 >> 4), kIdescO, t > 0 || k > 0);
-                        mma_commit(o_full + bars);
-                        mma_commit(empty0 + 8 * stage);
-                        if (!st.two)
-                            mma_commit(empty0 + 8 * stage);
+                        issue_output<64>(tO, tmem + s * 128 + (t & 1) * 64,
+                                         smem_u32(smem + F::kOffRing + stage * F::kTileBytes), 0, t > 0);
+                        mma_commit(o_full + turn.off);
+                        release(stage);
                     }
                     __syncwarp();
                     if (t + 2 < steps)
@@ -496,184 +701,83 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 done1 += steps / 2;
                 ++nseg;
             }
-            if (!ok) { // MMAs in flight finish before TMEM is given back
-                volatile int never = 0;
-                if (elect_one())
-                    mma_commit(drain);
-                __syncwarp();
-                (void)wait_bar(drain, 0, &never);
-            }
+            if (!ok)
+                drain_mmas(smem_u32(&sh->drain[s]));
         }
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<192>();
-        const int s = warp >> 2, row = tid & (kRows - 1); // stream, row of its tile
+        const int s = warp >> 2, row = tid & (kRows - 1);  // stream, row of its tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // this warp's TMEM lanes
         const uint32_t tO = tmem + 256 + s * 128 + lanes;
         uint32_t done0 = 0, done1 = 0, nseg = 0; // steps of earlier segments, by their parity; segments
-        auto arrive = [&](uint32_t bar) { // one arrival a warp, behind every lane's work
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar);
-        };
         while (walk.next(seg)) {
-            const int4 it = seg.it;
-            const Streams st{it.z > kRows, seg.j1 - seg.j0};
-            // Row of the item in this thread's lane. With at most 64 rows the second
-            // stream's start at lane 64, so that the streams' rows fall to different
-            // schedulers.
-            const int turn = !st.two && it.z <= kRows / 2 ? s * (kRows / 2) : 0;
-            const int qrow = st.two ? s * kRows + row : (row + kRows - turn) % kRows;
-            const bool mine = qrow < it.z;
+            const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+            const int qrow = row_of(st.two, seg.it.z, s, row);
+            const bool mine = qrow < seg.it.z;
             const bool busy = __any_sync(kFull, mine); // a warp without a row only keeps the barriers' count
             // Every earlier MMA that read Q is complete (both groups have met below).
-            {
-                uint4 *dst = reinterpret_cast<uint4 *>(smem + kOffQ + s * kQBytes);
-                const uint4 *src = nullptr;
-                if (mine) {
-                    const int r = it.y + qrow, a = r / p.M;
-                    const int b = __ldcg(p.list + (size_t)it.x * p.B + a);
-                    src = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.Hq + (size_t)it.x * p.M + (r - a * p.M)) *
-                                                                    kHeadDim);
-                }
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint4 x = src ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    dst[(c >> 3) * (kQHalfBytes / 16) + row * 8 + ((c & 7) ^ (row & 7))] = x;
-                }
-                fence_proxy_async_smem();
-            }
-            arrive(q_full);
+            stage_query(p, smem + F::kOffQ + s * kQBytes, seg.it, qrow, row);
+            arrive_warp(q_full, lane);
 
             float m = -INFINITY, l = 0.f; // m in the logits' units
             const int steps = st.steps(s);
             for (int t = 0; t < steps; ++t) {
-                const uint32_t bars = 16 * s + 8 * (t & 1);
+                const Turn turn = turn_of(s, t, done0, done1);
                 const uint32_t tS = tmem + s * 128 + (t & 1) * 64 + lanes;
-                if (!wait_warp(s_full + bars, (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)) {
+                if (!wait_warp(s_full + turn.off, turn.parity, abort_flag)) {
                     ok = false;
                     break;
                 }
-                if (!busy) {
-                    arrive(p_full + bars);
-                    continue;
-                }
-                tc_fence_after();
-                uint32_t x[2][32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    tmem_ld32(x[c], tS + 32 * c);
-                tmem_wait_ld();
-                const int left = p.prefix_len - (seg.j0 + st.tile(s, t)) * kTile;
-                if (left < kTile) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i >= left)
-                                x[c][i] = 0xff800000u; // -inf
-                }
-                float mx[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t *q = &x[c >> 1][(c & 1) * 16];
-                    mx[c] = max_nan(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]));
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2)
-                        mx[c] = max_nan(mx[c], __uint_as_float(q[i]), __uint_as_float(q[i + 1]));
-                    mx[c] = max_nan(mx[c], mx[c], __uint_as_float(q[15]));
-                }
-                const float top = max_nan(max_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-                if (t == 0) {
-                    m = top;
-                } else if (__any_sync(kFull, !((top - m) * kScaleLog2 <= kGrowth))) { // also for a NaN
-                    // The buffer's S means that the product before the last is
-                    // complete; wait for the last one.
-                    const uint32_t prev = 16 * s + 8 * ((t - 1) & 1);
-                    if (!wait_warp(o_full + prev, ((((t - 1) & 1) ? done1 : done0) + ((t - 1) >> 1)) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                if (busy) {
                     tc_fence_after();
-                    const float mn = max_nan(m, top, top);
-                    const float f = mn == m ? 1.f : exp2_approx((m - mn) * kScaleLog2);
-                    m = mn;
-                    l *= f;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o, tO + 32 * c);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(tO + 32 * c, o);
+                    uint32_t x[2][32];
+                    tmem_ld32(x[0], tS);
+                    tmem_ld32(x[1], tS + 32);
+                    tmem_wait_ld();
+                    const int left = p.prefix_len - (seg.j0 + st.tile(s, t)) * 64;
+                    if (left < 64)
+                        mask_columns<64>(x, left);
+                    const float top = largest<64>(x);
+                    if (t == 0) {
+                        m = top;
+                    } else if (__any_sync(kFull, !((top - m) * kScaleLog2 <= kGrowth))) { // also for a NaN
+                        // This S means that the product before the last is complete:
+                        // wait for the last one.
+                        const Turn last = turn_of(s, t - 1, done0, done1);
+                        if (!wait_warp(o_full + last.off, last.parity, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        raise_reference(top, m, l, tO);
                     }
+                    uint32_t w[32];
+                    l += weights64(x[0], x[1], subtrahend(m), w);
+                    tmem_st32(tS, w);
+                    tmem_wait_st();
                 }
-                // A row without a finite logit yet keeps weights of 0; an infinite
-                // maximum makes them NaN.
-                const float sub = m == -INFINITY ? 0.f : fmaf(m, kScaleLog2, m - m);
-                const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), nsub2 = pack2(-sub, -sub);
-                uint64_t sum[2] = {0ull, 0ull};
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t(&src)[32] = x[i >> 4];
-                    const uint64_t y = fma2(pack2(__uint_as_float(src[(2 * i) & 31]),
-                                                  __uint_as_float(src[(2 * i + 1) & 31])), scale2, nsub2);
-                    float a, b;
-                    if ((i & 7) < kPolyOf8) {
-                        exp2_poly2(y, a, b);
-                    } else {
-                        unpack2(y, a, b);
-                        a = exp2_approx(a);
-                        b = exp2_approx(b);
-                    }
-                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-                    w[i] = pack_bf16x2(a, b);
-                }
-                tmem_st32(tS, w);
-                tmem_wait_st();
-                arrive(p_full + bars);
-                float s0, s1;
-                unpack2(add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
+                arrive_warp(p_full + turn.off, lane);
             }
             if (!ok)
                 break;
-            // ---- the segment's partial of this row
-            const size_t slot = (size_t)blockIdx.x + seg.item;
-            const size_t part = (slot * 2 + s) * p.row_cap;
+            const size_t part = (((size_t)blockIdx.x + seg.item) * 2 + s) * p.row_cap;
             const int prow = qrow % kRows;
             if (steps > 0) {
-                const int t = steps - 1;
-                if (!wait_warp(o_full + 16 * s + 8 * (t & 1), (((t & 1) ? done1 : done0) + (t >> 1)) & 1, abort_flag)) {
+                const Turn last = turn_of(s, steps - 1, done0, done1);
+                if (!wait_warp(o_full + last.off, last.parity, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(o, tO + 32 * c);
-                    tmem_wait_ld();
-                    if (mine) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) // eight elements a row and block of 16
-                            __stcg(reinterpret_cast<float4 *>(p.o + part * kHeadDim +
-                                                              ((size_t)(4 * c + (i >> 1)) * p.row_cap + prow) * 8 + (i & 1) * 4),
-                                   make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
-                    }
-                }
+                store_partial(p, part, tO, prow, mine);
             }
             if (mine)
                 __stcg(p.ml + part + prow, make_float2(m * kScaleLog2, l));
-            // Both groups are done with the segment's Q, S and O.
             done0 += (steps + 1) / 2;
             done1 += steps / 2;
-            arrive(seg_done);
+            // Both groups are done with the segment's Q, S and O.
+            arrive_warp(seg_done, lane);
             if (!wait_warp(seg_done, nseg & 1, abort_flag)) {
                 ok = false;
                 break;
@@ -681,12 +785,192 @@ scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             ++nseg;
         }
     }
-    if (!ok && lane == 0)
-        atomicOr(p.err, SR_DEVERR_TIMEOUT);
-    __syncthreads();
-    __syncwarp();
-    if (warp == kMmaWarp)
-        tmem_dealloc(tmem, 512);
+    scan_epilogue(p, ok, tmem, warp, lane);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p)
+{
+    using F = Form<128>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared *sh = reinterpret_cast<Shared *>(smem + F::kOffBar);
+    volatile int *abort_flag = &sh->abort_flag;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+    const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty), q_full = smem_u32(&sh->q_full);
+    const uint32_t s_full = smem_u32(sh->s_full), p_full = smem_u32(sh->p_full), o_full = smem_u32(sh->o_full);
+    const uint32_t seg_done = smem_u32(&sh->seg_done);
+    const uint32_t tmem = scan_prologue<128>(sh, &tmK, &tmV, warp, lane);
+
+    Walk walk(p);
+    Segment seg;
+    bool ok = true;
+
+    if (warp >= kSoftmaxWarps) {
+        regs_dec<88>();
+        if (warp == kCopyWarp) {
+            // ------------------------------------------------------------ copies
+            uint32_t used = 0; // copies issued
+            auto copy = [&](const CUtensorMap *map, int g, int j) -> bool {
+                const uint32_t st = used % F::kStages;
+                if (!wait_warp(empty0 + 8 * st, ((used / F::kStages) & 1) ^ 1, abort_flag))
+                    return false;
+                copy_tile<128>(smem, map, st, full0 + 8 * st, j, g);
+                ++used;
+                return true;
+            };
+            while (ok && walk.next(seg)) {
+                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+                const int g = seg.it.x, lead = st.two ? 1 : 2;
+                for (int j = 0; ok && j < min(lead, st.n); ++j)
+                    ok = copy(&tmK, g, seg.j0 + j);
+                for (int j = 0; ok && j < st.n; ++j)
+                    ok = copy(&tmV, g, seg.j0 + j) && (j + lead >= st.n || copy(&tmK, g, seg.j0 + j + lead));
+            }
+            volatile int never = 0;
+            if (!ok)
+                for (uint32_t i = used > F::kStages ? used - F::kStages : 0; i < used; ++i)
+                    (void)wait_bar(full0 + 8 * (i % F::kStages), (i / F::kStages) & 1, &never);
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------- MMAs of both streams in turn
+            uint32_t used = 0, nseg = 0, np0 = 0, np1 = 0; // copies and segments before; P tiles of each stream
+            while (ok && walk.next(seg)) {
+                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+                const int look = st.two ? 1 : 2, steps0 = st.steps(0), steps1 = st.steps(1);
+                if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
+                    break;
+                tc_fence_after();
+                auto stage_at = [&](int at) { return (used + at) % F::kStages; };
+                auto landed = [&](int at) {
+                    return wait_warp(full0 + 8 * stage_at(at), ((used + at) / F::kStages) & 1, abort_flag);
+                };
+                auto logits = [&](int s, int t) -> bool {
+                    const int at = key_at(look, st.tile(s, t));
+                    if (!landed(at))
+                        return false;
+                    if (elect_one()) {
+                        issue_logits<128>(tmem + s * 128, smem_u32(smem + F::kOffQ + s * kQBytes),
+                                          smem_u32(smem + F::kOffRing + stage_at(at) * F::kTileBytes));
+                        mma_commit(s_full + 16 * s);
+                        if (!st.two || s == 1)
+                            mma_commit(empty0 + 8 * stage_at(at));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto output = [&](int s, int t, int steps, uint32_t &np) -> bool {
+                    const int at = value_at(look, st.tile(s, t), st.n);
+                    if (!landed(at))
+                        return false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) { // P comes in two halves
+                        if (!wait_warp(p_full + 16 * s + 8 * h, np & 1, abort_flag))
+                            return false;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_output<128>(tmem + 256 + s * 128, tmem + s * 128,
+                                              smem_u32(smem + F::kOffRing + stage_at(at) * F::kTileBytes), h, t > 0 || h > 0);
+                            if (h == 1) {
+                                if (!st.two || s == 1)
+                                    mma_commit(empty0 + 8 * stage_at(at));
+                                if (t + 1 == steps)
+                                    mma_commit(o_full + 16 * s);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    ++np;
+                    return true;
+                };
+                ok = logits(0, 0) && (steps1 == 0 || logits(1, 0));
+                for (int t = 0; ok && t < steps0; ++t) {
+                    ok = output(0, t, steps0, np0) && (t + 1 >= steps0 || logits(0, t + 1));
+                    if (ok && t < steps1)
+                        ok = output(1, t, steps1, np1) && (t + 1 >= steps1 || logits(1, t + 1));
+                }
+                used += 2 * (uint32_t)st.n;
+                ++nseg;
+            }
+            if (!ok)
+                drain_mmas(smem_u32(&sh->drain[0]));
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        regs_inc<208>();
+        const int s = warp >> 2, row = tid & (kRows - 1);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t tO = tmem + 256 + s * 128 + lanes, tS = tmem + s * 128 + lanes;
+        uint32_t ns = 0, no = 0, nseg = 0; // S tiles, O results and segments consumed
+        while (walk.next(seg)) {
+            const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
+            const int qrow = row_of(st.two, seg.it.z, s, row);
+            const bool mine = qrow < seg.it.z;
+            const bool busy = __any_sync(kFull, mine);
+            stage_query(p, smem + F::kOffQ + s * kQBytes, seg.it, qrow, row);
+            arrive_warp(q_full, lane);
+
+            float m = -INFINITY, l = 0.f;
+            const int steps = st.steps(s);
+            for (int t = 0; t < steps; ++t) {
+                if (!wait_warp(s_full + 16 * s, ns & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                if (!busy) {
+                    arrive_warp(p_full + 16 * s, lane);
+                    arrive_warp(p_full + 16 * s + 8, lane);
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(x[c], tS + 32 * c);
+                tmem_wait_ld();
+                const int left = p.prefix_len - (seg.j0 + st.tile(s, t)) * 128;
+                if (left < 128)
+                    mask_columns<128>(x, left);
+                const float top = largest<128>(x);
+                // This S means that every earlier product of the stream is complete.
+                if (t == 0)
+                    m = top;
+                else if (__any_sync(kFull, !((top - m) * kScaleLog2 <= kGrowth)))
+                    raise_reference(top, m, l, tO);
+                const float sub = subtrahend(m);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+                    l += weights64(x[2 * h], x[2 * h + 1], sub, w);
+                    tmem_st32(tS + 32 * h, w);
+                    tmem_wait_st();
+                    arrive_warp(p_full + 16 * s + 8 * h, lane);
+                }
+            }
+            if (!ok)
+                break;
+            const size_t part = (((size_t)blockIdx.x + seg.item) * 2 + s) * p.row_cap;
+            const int prow = qrow % kRows;
+            if (steps > 0) {
+                if (!wait_warp(o_full + 16 * s, no & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++no;
+                tc_fence_after();
+                store_partial(p, part, tO, prow, mine);
+            }
+            if (mine)
+                __stcg(p.ml + part + prow, make_float2(m * kScaleLog2, l));
+            arrive_warp(seg_done, lane);
+            if (!wait_warp(seg_done, nseg & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++nseg;
+        }
+    }
+    scan_epilogue(p, ok, tmem, warp, lane);
 }
 
 // ---- join -------------------------------------------------------------------------------
@@ -768,7 +1052,7 @@ template <bool kWhole> __global__ void __launch_bounds__(32 * kJoinWarps) join_k
                           __uint_as_float(v.y & 0xffff0000u));
     } else {
         float m = -INFINITY, l = 0.f;
-        const int nt = (p.prefix_len + kTile - 1) / kTile;
+        const int nt = (p.prefix_len + p.tile - 1) / p.tile;
         if (nt > 0) {
             const int r = rank * p.M + (h - g * p.M);
             const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
@@ -855,7 +1139,9 @@ cudaError_t grid_of(int *grid)
         int sms = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            e = cudaFuncSetAttribute(scan_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Form<64>::kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(scan_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Form<128>::kSmem);
         if (e != cudaSuccess)
             return e;
         known[dev] = sms < kGridCap ? sms : kGridCap;
@@ -923,14 +1209,18 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
     p.M = a.n_q_heads / a.n_kv_heads;
     p.prefix_len = a.prefix_len;
     p.row_cap = w.row_cap;
+    p.tile = a.batch * p.M > kRows ? 128 : 64;
 
     e = launch(plan_kernel, 1, kPlanThreads, 0, stream, p);
     if (e == cudaSuccess && a.prefix_len > 0) {
         CUtensorMap tmK, tmV;
-        if (!make_cache_map(&tmK, a.k_prefix, a.n_kv_heads, a.max_seq_len, kTile, false, a.prefix_len) ||
-            !make_cache_map(&tmV, a.v_prefix, a.n_kv_heads, a.max_seq_len, kTile, false, a.prefix_len))
+        if (!make_cache_map(&tmK, a.k_prefix, a.n_kv_heads, a.max_seq_len, p.tile, false, a.prefix_len) ||
+            !make_cache_map(&tmV, a.v_prefix, a.n_kv_heads, a.max_seq_len, p.tile, false, a.prefix_len))
             return cudaErrorInvalidValue;
-        e = launch(scan_kernel, (unsigned)p.grid, kThreads, kSmem, stream, tmK, tmV, p);
+        if (p.tile == 64)
+            e = launch(scan_narrow_kernel, (unsigned)p.grid, kThreads, Form<64>::kSmem, stream, tmK, tmV, p);
+        else
+            e = launch(scan_wide_kernel, (unsigned)p.grid, kThreads, Form<128>::kSmem, stream, tmK, tmV, p);
     }
     if (e == cudaSuccess) {
         // Few rows have many partials each (the grid is spread over few items): a

@@ -64,6 +64,9 @@ CASES = [
     (64, 1, 8, 257, 300),     # 512 rows
     (2, 2, 8, 40000, 40000),  # long, few rows: many splits
     (129, 3, 1, 384, 384),
+    (70, 8, 8, 3001, 3001),   # 24 items of 24 tiles: a CTA's share ends one item and begins the next
+    (3, 64, 1, 2100, 2100),   # 64 items of few rows, likewise
+    (20, 33, 8, 700, 700),    # 160 rows a KV head: every item has more than one row tile
 ]
 
 
