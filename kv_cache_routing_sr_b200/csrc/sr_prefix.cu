@@ -32,9 +32,9 @@
 // ring's ten 16 KB stages are in flight rather than waiting. More rows are bound by
 // the tensor cores and the exponentials: the wide form works in 128-position tiles
 // (an S product of 128 columns reads Q from shared memory half as often: 75 cycles a
-// 128x128x16 step against 57 a 128x64x16), and one MMA warp issues P0 V, S0 of the
-// next tile, P1 V, S1 of the next tile, which keeps the streams half a turn apart: one
-// has the tensor cores while the other has the exponentials.
+// 128x128x16 step against 57 a 128x64x16), and one MMA warp issues P0 V and S0 of the
+// next tile, then P1 V and S1 of the next tile, which keeps the streams half a turn
+// apart: one has the tensor cores while the other has the exponentials.
 //
 // Every wait is bounded in time; a timeout sets a device error bit, and the CTA
 // leaves once its own copies and MMAs have landed.
@@ -69,7 +69,7 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9;
 
 // The scan's two forms, by the positions of a tile.
 template <int TILE> struct Form {
-    static constexpr int kStages = TILE == 64 ? 10 : 5;
+    static constexpr int kStages = TILE == 64 ? 10 : 4;
     static constexpr int kHalfBytes = TILE * 128;      // [TILE positions x 64 bf16], 128B swizzle
     static constexpr int kTileBytes = 2 * kHalfBytes;  // [TILE x 128]
     static constexpr int kOffQ = 0, kOffRing = 2 * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
@@ -136,9 +136,12 @@ struct Params {
 // An item's weight: its tiles take two row tiles' products or one.
 __device__ __forceinline__ int weight_of(int rows) { return rows > kRows ? 2 : 1; }
 
-// Cost of n tiles of weight 1, even, so that with even shares no tile of weight 2
-// lies across two shares.
-__device__ __forceinline__ long long item_cost(int nt) { return (nt + 1) & ~1; }
+// Cost of an item for each unit of its weight, in tiles of weight 1: an entry that
+// stands for what a CTA spends on beginning an item (its queries, its partial; 8 to
+// 10 us where a wide tile of weight 2 takes 1.9), then its tiles. Even, so that with
+// even shares no tile of weight 2 lies across two shares.
+constexpr int kEntry = 4;
+__device__ __forceinline__ long long item_cost(int nt) { return kEntry + ((nt + 1) & ~1); }
 
 // Cost that one CTA takes of `weight` items of weight 1.
 __device__ __forceinline__ long long share_of(int weight, int nt, int grid)
@@ -304,10 +307,10 @@ struct Walk {
             s.it = __ldcg(p.items + s.item);
             const int w = weight_of(s.it.z);
             const long long begin = s.it.w * cost;
-            s.j0 = (int)((at - begin) / w);
-            s.j1 = (int)min((long long)nt, (end - begin) / w);
+            s.j0 = (int)max((at - begin) / w - kEntry, 0ll);
+            s.j1 = (int)min((long long)nt, (end - begin) / w - kEntry);
             at = min(end, begin + w * cost);
-            if (s.j0 < s.j1) // else only the padding of an odd number of tiles
+            if (s.j0 < s.j1) // else only of the entry, or the padding of an odd number of tiles
                 return true;
         }
         return false;
@@ -361,7 +364,7 @@ __device__ __forceinline__ Turn turn_of(int s, int t, uint32_t done0, uint32_t d
 
 struct Shared {
     uint64_t full[10], empty[10];
-    uint64_t s_full[2][2], p_full[2][2], o_full[2][2]; // stream; step parity (narrow) or half of P (wide)
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2]; // stream; step parity (narrow; wide: the first)
     uint64_t q_full, seg_done, drain[2];
     uint32_t tmem;
     int abort_flag;
@@ -462,14 +465,13 @@ template <int TILE> __device__ __forceinline__ void issue_logits(uint32_t d, uin
                bf16_idesc(kRows, TILE, false), k > 0);
 }
 
-// O[128 x 128] (+)= P V over 64 positions, from position 64 * h of the tile on; the
-// elected lane.
-template <int TILE> __device__ __forceinline__ void issue_output(uint32_t d, uint32_t tp, uint32_t sv, int h, bool accumulate)
+// O[128 x 128] (+)= P V over a tile, the elected lane.
+template <int TILE> __device__ __forceinline__ void issue_output(uint32_t d, uint32_t tp, uint32_t sv, bool accumulate)
 {
     const uint64_t b = smem_desc_sw128(sv, Form<TILE>::kHalfBytes, 1024);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) // 16 positions each
-        mma_ts(d, tp + h * 32 + k * 8, b + (4 * h + k) * (2048 >> 4), bf16_idesc(kRows, kHeadDim, true), accumulate || k > 0);
+    for (int k = 0; k < TILE / 16; ++k) // 16 positions each
+        mma_ts(d, tp + k * 8, b + k * (2048 >> 4), bf16_idesc(kRows, kHeadDim, true), accumulate || k > 0);
 }
 
 // The row of a segment's item in a softmax thread's lane (past the item: none). Narrow
@@ -687,7 +689,7 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     tc_fence_after();
                     if (elect_one()) {
                         issue_output<64>(tO, tmem + s * 128 + (t & 1) * 64,
-                                         smem_u32(smem + F::kOffRing + stage * F::kTileBytes), 0, t > 0);
+                                         smem_u32(smem + F::kOffRing + stage * F::kTileBytes), t > 0);
                         mma_commit(o_full + turn.off);
                         release(stage);
                     }
@@ -833,63 +835,64 @@ scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     (void)wait_bar(full0 + 8 * (i % F::kStages), (i / F::kStages) & 1, &never);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------- MMAs of both streams in turn
-            uint32_t used = 0, nseg = 0, np0 = 0, np1 = 0; // copies and segments before; P tiles of each stream
+            // A wait costs this warp about as much as two MMAs even when it is over, and
+            // its issues are what keeps the tensor cores busy: so a turn waits for all
+            // that it needs (its P, its values and the next keys; streams over the same
+            // tiles wait for these once) and issues both products in one go.
+            const uint32_t ring = smem_u32(smem + F::kOffRing), sq = smem_u32(smem + F::kOffQ);
+            uint32_t used = 0, seg_parity = 0, np0 = 0, np1 = 0; // copies before; parities
             while (ok && walk.next(seg)) {
                 const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
                 const int look = st.two ? 1 : 2, steps0 = st.steps(0), steps1 = st.steps(1);
-                if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
+                if (!(ok = wait_warp(q_full, seg_parity, abort_flag)))
                     break;
                 tc_fence_after();
                 auto stage_at = [&](int at) { return (used + at) % F::kStages; };
                 auto landed = [&](int at) {
                     return wait_warp(full0 + 8 * stage_at(at), ((used + at) / F::kStages) & 1, abort_flag);
                 };
-                auto logits = [&](int s, int t) -> bool {
-                    const int at = key_at(look, st.tile(s, t));
-                    if (!landed(at))
+                // S of stream s, step t, by the elected lane
+                auto logits = [&](int s, int t, bool release) {
+                    const uint32_t stage = stage_at(key_at(look, st.tile(s, t)));
+                    issue_logits<128>(tmem + s * 128, sq + s * kQBytes, ring + stage * F::kTileBytes);
+                    mma_commit(s_full + 16 * s);
+                    if (release)
+                        mma_commit(empty0 + 8 * stage);
+                };
+                auto turn = [&](int s, int t, int steps, uint32_t &np) -> bool {
+                    const int at = value_at(look, st.tile(s, t), st.n);
+                    const bool more = t + 1 < steps, mine = !st.two || s == 1;
+                    if (!st.two || s == 0)
+                        if (!landed(at) || (more && !landed(key_at(look, st.tile(s, t + 1)))))
+                            return false;
+                    if (!wait_warp(p_full + 16 * s, np, abort_flag))
                         return false;
+                    tc_fence_after();
                     if (elect_one()) {
-                        issue_logits<128>(tmem + s * 128, smem_u32(smem + F::kOffQ + s * kQBytes),
-                                          smem_u32(smem + F::kOffRing + stage_at(at) * F::kTileBytes));
-                        mma_commit(s_full + 16 * s);
-                        if (!st.two || s == 1)
-                            mma_commit(empty0 + 8 * stage_at(at));
+                        const uint32_t stage = stage_at(at);
+                        issue_output<128>(tmem + 256 + s * 128, tmem + s * 128, ring + stage * F::kTileBytes, t > 0);
+                        if (mine)
+                            mma_commit(empty0 + 8 * stage);
+                        if (more)
+                            logits(s, t + 1, mine);
+                        else
+                            mma_commit(o_full + 16 * s);
                     }
                     __syncwarp();
+                    np ^= 1;
                     return true;
                 };
-                auto output = [&](int s, int t, int steps, uint32_t &np) -> bool {
-                    const int at = value_at(look, st.tile(s, t), st.n);
-                    if (!landed(at))
-                        return false;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) { // P comes in two halves
-                        if (!wait_warp(p_full + 16 * s + 8 * h, np & 1, abort_flag))
-                            return false;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            issue_output<128>(tmem + 256 + s * 128, tmem + s * 128,
-                                              smem_u32(smem + F::kOffRing + stage_at(at) * F::kTileBytes), h, t > 0 || h > 0);
-                            if (h == 1) {
-                                if (!st.two || s == 1)
-                                    mma_commit(empty0 + 8 * stage_at(at));
-                                if (t + 1 == steps)
-                                    mma_commit(o_full + 16 * s);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    ++np;
-                    return true;
-                };
-                ok = logits(0, 0) && (steps1 == 0 || logits(1, 0));
-                for (int t = 0; ok && t < steps0; ++t) {
-                    ok = output(0, t, steps0, np0) && (t + 1 >= steps0 || logits(0, t + 1));
-                    if (ok && t < steps1)
-                        ok = output(1, t, steps1, np1) && (t + 1 >= steps1 || logits(1, t + 1));
+                ok = landed(key_at(look, 0)) && (st.two || steps1 == 0 || landed(key_at(look, 1)));
+                if (ok && elect_one()) {
+                    logits(0, 0, !st.two);
+                    if (steps1)
+                        logits(1, 0, true);
                 }
+                __syncwarp();
+                for (int t = 0; ok && t < steps0; ++t)
+                    ok = turn(0, t, steps0, np0) && (t >= steps1 || turn(1, t, steps1, np1));
                 used += 2 * (uint32_t)st.n;
-                ++nseg;
+                seg_parity ^= 1;
             }
             if (!ok)
                 drain_mmas(smem_u32(&sh->drain[0]));
@@ -919,7 +922,6 @@ scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 ++ns;
                 if (!busy) {
                     arrive_warp(p_full + 16 * s, lane);
-                    arrive_warp(p_full + 16 * s + 8, lane);
                     continue;
                 }
                 tc_fence_after();
@@ -943,9 +945,9 @@ scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     uint32_t w[32];
                     l += weights64(x[2 * h], x[2 * h + 1], sub, w);
                     tmem_st32(tS + 32 * h, w);
-                    tmem_wait_st();
-                    arrive_warp(p_full + 16 * s + 8 * h, lane);
                 }
+                tmem_wait_st();
+                arrive_warp(p_full + 16 * s, lane);
             }
             if (!ok)
                 break;
@@ -1059,8 +1061,9 @@ template <bool kWhole> __global__ void __launch_bounds__(32 * kJoinWarps) join_k
             const int4 it = __ldcg(p.items + item);
             const bool two = it.z > kRows;
             const long long share = share_of(__ldcg(p.weight), nt, p.grid), begin = it.w * item_cost(nt);
-            const int c0 = (int)(begin / share);
-            const int c1 = (int)((begin + (long long)(nt - 1) * weight_of(it.z)) / share);
+            const int w = weight_of(it.z);
+            const int c0 = (int)((begin + (long long)kEntry * w) / share);
+            const int c1 = (int)((begin + (long long)(kEntry + nt - 1) * w) / share);
             // Partials k: of CTA c0 + k, or of its two streams
             const int n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
             auto part = [&](int k) -> size_t {
