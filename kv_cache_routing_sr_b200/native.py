@@ -1,4 +1,5 @@
-"""ctypes binding of libsinkrouter.so (the C ABI in include/sinkrouter.h).
+"""Binding of libsinkrouter.so (the C ABI in include/sinkrouter.h): ctypes, and for
+the 8-bit cache and the shared prefix the compiled _sr_binding.
 
 Argument marshalling only: every step of the computation runs in the library's
 CUDA kernels. torch provides device memory and the current stream. There is no
@@ -34,10 +35,6 @@ class RowStrides(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
-# What a cache tensor of each dtype is to the library.
-KV_TYPES = {torch.bfloat16: SR_KV_BF16, torch.float8_e4m3fn: SR_KV_E4M3, torch.int8: SR_KV_INT8}
-
-
 class SinkRouterError(RuntimeError):
     def __init__(self, fn: str, status: int, lib):
         msg = lib.sr_status_string(status).decode()
@@ -48,6 +45,10 @@ class SinkRouterError(RuntimeError):
 
 
 _lib = None
+_bound = None  # the compiled binding, once the library is loaded
+# entry points that the compiled binding calls, in its order
+_BOUND = ["sr_kv_append_quant", "sr_kv_dequant", "sr_rope_append_route_kv", "sr_decode_attention_quant",
+          "sr_decode_attention_quant_partial", "sr_prefix_attention", "sr_prefix_attention_partial"]
 
 EXPORTS = ["sr_route", "sr_decode_workspace_bytes", "sr_workspace_init", "sr_decode_attention",
            "sr_status_string", "sr_get_device_error", "sr_clear_device_error", "sr_decode_grid_size",
@@ -65,13 +66,13 @@ def load(path: str | None = None):
     sources), else the in-tree library, which is compiled first if it is
     absent (nvcc, sm_100a). Any other missing path, or a failed compile,
     raises: there is no other implementation to fall back to."""
-    global _lib
+    global _lib, _bound
     if _lib is not None:
         return _lib
     if path is None:
         path = os.environ.get("SINKROUTER_LIBRARY") or LIBRARY
-    if not os.path.exists(path) and os.path.abspath(path) == os.path.abspath(LIBRARY):
-        from . import build as _build
+    if not os.path.exists(_build.BINDING) or (not os.path.exists(path) and
+                                              os.path.abspath(path) == os.path.abspath(LIBRARY)):
         try:
             _build.build()
         except Exception as e:
@@ -136,6 +137,9 @@ def load(path: str | None = None):
     lib.sr_prefix_attention.restype = ctypes.c_int
     lib.sr_prefix_attention_partial.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
     lib.sr_prefix_attention_partial.restype = ctypes.c_int
+    from . import _sr_binding
+    _sr_binding.use(*(ctypes.cast(getattr(lib, n), vp).value for n in _BOUND))
+    _bound = _sr_binding
     _lib = lib
     return lib
 
@@ -179,30 +183,16 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     return t.data_ptr()
 
 
-def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
-    """Pointer of a contiguous CUDA tensor of exactly this dtype, shape and device:
-    the library sees pointers only, and would read another size out of bounds."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr()
-    _dev(t, name, dtype)
-    raise ValueError(f"{name} must have shape {tuple(shape)} on cuda:{device}, got {tuple(t.shape)} on {t.device}")
+def _handle(stream) -> int | None:
+    """A stream for the compiled binding: its handle, None for the current one of
+    the tensors' device (which the binding also makes current)."""
+    return None if stream is None else stream.cuda_stream
 
 
-def _opt(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int | None:
-    return None if t is None else _arg(t, name, dtype, shape, device)
-
-
-def _kv_type(k_cache: torch.Tensor, kv_scales, quant_only: bool = True) -> int:
-    """sr_kv_type of a cache [B, Hkv, Lmax, 128], and whether scales belong to it."""
-    kv = KV_TYPES.get(k_cache.dtype)
-    if kv is None or (quant_only and kv == SR_KV_BF16):
-        raise ValueError(f"k_cache must be float8_e4m3fn or int8{'' if quant_only else ' or bfloat16'}, "
-                         f"got {k_cache.dtype}")
-    if k_cache.dim() != 4 or k_cache.shape[3] != HEAD_DIM:
-        raise ValueError(f"k_cache must be [B, Hkv, Lmax, {HEAD_DIM}], got {tuple(k_cache.shape)}")
-    if (kv == SR_KV_BF16) != (kv_scales is None):
-        raise ValueError("a bfloat16 cache has no kv_scales" if kv == SR_KV_BF16 else "an 8-bit cache needs kv_scales")
-    return kv
+def _loaded():
+    if _bound is None:
+        load()
+    return _bound
 
 
 def dims_of(batch: int, n_q_heads: int, n_kv_heads: int, max_seq_len: int, head_dim: int = HEAD_DIM) -> Dims:
@@ -448,68 +438,27 @@ class QuantCache:
         self.scales = torch.zeros((*shape[:3], 2), dtype=torch.float32, device=device)
 
 
-def _row_strides(t: torch.Tensor, name: str, shape: tuple, device: int) -> RowStrides:
-    """Strides of a bf16 [B, T, Hkv, 128] tensor, which may be a view."""
-    st = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device or st[3] != 1:
-        raise ValueError(f"{name} must be a bfloat16 tensor {shape} on cuda:{device} with a contiguous last dimension, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    # the stride of a dimension of one entry is never used
-    return RowStrides(*(x if n > 1 else 0 for x, n in zip(st, shape[:3])))
-
-
-@_on_tensor_device
 def kv_append_quant(k_new, v_new, start, n_new, k_cache, v_cache, kv_scales, k0=None, v0=None, device_error=None,
                     stream=None):
     """sr_kv_append_quant: quantise tokens t < n_new[b] of k_new / v_new (bf16
     [B, T, Hkv, 128], views allowed) into slots start[b] + t of the 8-bit cache.
     k0 / v0 (both or neither) receive the bf16 rows that land in slot 0. Updates
     k_cache, v_cache, kv_scales, k0 and v0 in place and returns the first three."""
-    kv = _kv_type(k_cache, kv_scales)
-    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
-    dev, i32, cache = k_cache.get_device(), torch.int32, k_cache.dtype
-    if k_new.dim() != 4:
-        raise ValueError("k_new must be [B, T, Hkv, 128]")
-    T = k_new.shape[1]
-    rows, row0 = (B, T, Hkv, d), (B, Hkv, d)
-    ks, vs = _row_strides(k_new, "k_new", rows, dev), _row_strides(v_new, "v_new", rows, dev)
-    if T < 1:
-        return k_cache, v_cache, kv_scales
-    st = load().sr_kv_append_quant(
-        Dims(B, Hkv, Hkv, d, Lmax), kv, T, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-        _arg(start, "start", i32, (B,), dev), _arg(n_new, "n_new", i32, (B,), dev),
-        _arg(k_cache, "k_cache", cache, full, dev), _arg(v_cache, "v_cache", cache, full, dev),
-        _arg(kv_scales, "kv_scales", torch.float32, (B, Hkv, Lmax, 2), dev), _opt(k0, "k0", torch.bfloat16, row0, dev),
-        _opt(v0, "v0", torch.bfloat16, row0, dev), _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
+    st = _loaded().kv_append_quant(k_new, v_new, start, n_new, k_cache, v_cache, kv_scales, k0, v0, device_error,
+                                   _handle(stream))
     _check("sr_kv_append_quant", st)
     return k_cache, v_cache, kv_scales
 
 
-@_on_tensor_device
 def kv_dequant(k_cache, v_cache, kv_scales, start, n, k_out, v_out, device_error=None, stream=None):
     """sr_kv_dequant: positions start[b] .. start[b] + n[b] - 1 of the 8-bit cache
     as bf16 rows 0 .. n[b] - 1 of k_out / v_out [B, Hkv, T, 128]; the other rows
     stay. Returns (k_out, v_out)."""
-    kv = _kv_type(k_cache, kv_scales)
-    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
-    dev, i32, cache = k_cache.get_device(), torch.int32, k_cache.dtype
-    if k_out.dim() != 4:
-        raise ValueError("k_out must be [B, Hkv, T, 128]")
-    T = k_out.shape[2]
-    rows = (B, Hkv, T, d)
-    ko, vo = _arg(k_out, "k_out", torch.bfloat16, rows, dev), _arg(v_out, "v_out", torch.bfloat16, rows, dev)
-    if T < 1:
-        return k_out, v_out
-    st = load().sr_kv_dequant(
-        Dims(B, Hkv, Hkv, d, Lmax), kv, T, _arg(k_cache, "k_cache", cache, full, dev),
-        _arg(v_cache, "v_cache", cache, full, dev), _arg(kv_scales, "kv_scales", torch.float32, (B, Hkv, Lmax, 2), dev),
-        _arg(start, "start", i32, (B,), dev), _arg(n, "n", i32, (B,), dev), ko, vo,
-        _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
+    st = _loaded().kv_dequant(k_cache, v_cache, kv_scales, start, n, k_out, v_out, device_error, _handle(stream))
     _check("sr_kv_dequant", st)
     return k_out, v_out
 
 
-@_on_tensor_device
 def rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache, v_cache, kv_scales, k0, v0, tau,
                          pos_offset: int = 0, seq_lens_out=None, q_out=None, route_mask=None, active_list=None,
                          device_error=None, stream=None):
@@ -517,75 +466,36 @@ def rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cac
     (kv_scales None for bf16) whose slot 0 holds position pos_offset. seq_lens
     advances in place, or into seq_lens_out when that is given. Returns (q_out,
     route_mask, active_list); q_out may be q_in."""
-    kv = _kv_type(k_cache, kv_scales, quant_only=False)
-    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
-    dev, i32, f32, bf16, cache = k_cache.get_device(), torch.int32, torch.float32, torch.bfloat16, k_cache.dtype
-    Hq, U, max_pos = q_in.shape[1], B * Hkv, rope_cos.shape[0]
-    qs, kvs, table = (B, Hq, d), (B, Hkv, d), (max_pos, d // 2)
-    q_ptr = _arg(q_in, "q_in", bf16, qs, dev)
-    if q_out is None:
-        q_out = torch.empty_like(q_in)
-    if route_mask is None:
-        route_mask = torch.empty(U, dtype=torch.uint8, device=q_in.device)
-    if active_list is None:
-        active_list = torch.empty(1 + U, dtype=i32, device=q_in.device)
-    lens = _arg(seq_lens, "seq_lens", i32, (B,), dev)
-    st = load().sr_rope_append_route_kv(
-        Dims(B, Hq, Hkv, d, Lmax), kv, pos_offset, q_ptr, _arg(k_new, "k_new", bf16, kvs, dev),
-        _arg(v_new, "v_new", bf16, kvs, dev), _arg(rope_cos, "rope_cos", f32, table, dev),
-        _arg(rope_sin, "rope_sin", f32, table, dev), max_pos, lens,
-        lens if seq_lens_out is None else _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev),
-        _arg(k_cache, "k_cache", cache, full, dev), _arg(v_cache, "v_cache", cache, full, dev),
-        _opt(kv_scales, "kv_scales", f32, (B, Hkv, Lmax, 2), dev), _arg(k0, "k0", bf16, kvs, dev),
-        _arg(v0, "v0", bf16, kvs, dev), tau, _arg(q_out, "q_out", bf16, qs, dev),
-        _arg(route_mask, "route_mask", torch.uint8, (U,), dev), _arg(active_list, "active_list", i32, (1 + U,), dev),
-        _opt(device_error, "device_error", i32, (1,), dev), _stream(stream))
+    st, q_out, route_mask, active_list = _loaded().rope_append_route_kv(
+        q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache, v_cache, kv_scales, k0, v0, tau, pos_offset,
+        seq_lens_out, q_out, route_mask, active_list, device_error, _handle(stream))
     _check("sr_rope_append_route_kv", st)
     return q_out, route_mask, active_list
 
 
-def _decode_quant(fn, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out, lse, out_dtype,
-                  workspace, stream):
-    """Both forms of the 8-bit scan: they differ in the entry point and the outputs' type."""
-    kv = _kv_type(k_cache, kv_scales)
-    B, Hkv, Lmax, d = full = tuple(k_cache.shape)
-    dev, i32, f32, bf16, cache = k_cache.get_device(), torch.int32, torch.float32, torch.bfloat16, k_cache.dtype
-    Hq = q.shape[1]
-    qs = (B, Hq, d)
-    args = (Dims(B, Hq, Hkv, d, Lmax), kv, _arg(q, "q", bf16, qs, dev), _arg(k_cache, "k_cache", cache, full, dev),
-            _arg(v_cache, "v_cache", cache, full, dev), _arg(kv_scales, "kv_scales", f32, (B, Hkv, Lmax, 2), dev),
-            _arg(v0, "v0", bf16, (B, Hkv, d), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
-            _arg(active_list, "active_list", i32, (1 + B * Hkv,), dev), n_splits,
-            _arg(out, "out" if out_dtype is bf16 else "o_part", out_dtype, qs, dev), _opt(lse, "lse", f32, (B, Hq), dev))
-    if workspace is None:
-        workspace = Workspace(B, Hq, Hkv, Lmax, n_splits, device=q.device)
-    _check(fn, getattr(load(), fn)(*args, workspace.ptr, workspace.nbytes, _stream(stream)))
-
-
-@_on_tensor_device
 def decode_attention_quant(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, out=None, n_splits: int = 0,
                            workspace: Workspace | None = None, stream=None, lse=None):
     """sr_decode_attention_quant: decode_attention over an 8-bit cache. Returns
     out bf16 [B, Hq, 128]; ``lse`` (fp32 [B, Hq]) receives the per-head
     log-sum-exp (NaN for sink heads)."""
-    if out is None:
-        out = torch.empty_like(q)
-    _decode_quant("sr_decode_attention_quant", q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out,
-                  lse, torch.bfloat16, workspace, stream)
+    if workspace is None:
+        workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
+    st, out, _ = _loaded().decode_quant(False, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out,
+                                        lse, workspace.ptr, workspace.nbytes, _handle(stream))
+    _check("sr_decode_attention_quant", st)
     return out
 
 
-@_on_tensor_device
 def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, o_part=None,
                                    lse_part=None, n_splits: int = 0, workspace: Workspace | None = None, stream=None):
     """sr_decode_attention_quant_partial: decode_attention_partial over an 8-bit
     cache. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    if o_part is None:
-        o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    if lse_part is None:
-        lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _decode_quant("sr_decode_attention_quant_partial", q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list,
-                  n_splits, o_part, lse_part, torch.float32, workspace, stream)
+    if workspace is None:
+        workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
+    st, o_part, lse_part = _loaded().decode_quant(True, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list,
+                                                  n_splits, o_part, lse_part, workspace.ptr, workspace.nbytes,
+                                                  _handle(stream))
+    _check("sr_decode_attention_quant_partial", st)
     return o_part, lse_part
 
 
@@ -604,26 +514,6 @@ class PrefixWorkspace(Workspace):
         self._allocate(prefix_workspace_bytes(batch, n_q_heads, n_kv_heads, max_prefix_len), device)
 
 
-def _prefix(fn, q, k_prefix, v_prefix, prefix_len, v0, route_mask, suffix, out, lse, out_dtype, workspace, stream):
-    """Both forms of the prefix attention; suffix: (o_suffix, lse_suffix), or () for the partial form."""
-    if k_prefix.dim() != 3 or k_prefix.shape[2] != HEAD_DIM or q.dim() != 3:
-        raise ValueError("q must be [B, Hq, 128] and k_prefix [Hkv, max_prefix_len, 128]")
-    Hkv, Lmax, d = pre = tuple(k_prefix.shape)
-    B, Hq = q.shape[:2]
-    dev, f32, bf16 = q.get_device(), torch.float32, torch.bfloat16
-    qs, hs = (B, Hq, d), (B, Hq)
-    args = (Dims(B, Hq, Hkv, d, Lmax), prefix_len, _arg(q, "q", bf16, qs, dev),
-            _arg(k_prefix, "k_prefix", bf16, pre, dev), _arg(v_prefix, "v_prefix", bf16, pre, dev),
-            _arg(v0, "v0", bf16, (B, Hkv, d), dev), _arg(route_mask, "route_mask", torch.uint8, (B * Hkv,), dev))
-    if suffix:
-        args += (_opt(suffix[0], "o_suffix", f32, qs, dev), _opt(suffix[1], "lse_suffix", f32, hs, dev))
-    args += (_arg(out, "out" if out_dtype is bf16 else "o_part", out_dtype, qs, dev), _opt(lse, "lse", f32, hs, dev))
-    if workspace is None:
-        workspace = PrefixWorkspace(B, Hq, Hkv, Lmax, device=q.device)
-    _check(fn, getattr(load(), fn)(*args, workspace.ptr, workspace.nbytes, _stream(stream)))
-
-
-@_on_tensor_device
 def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out=None, lse=None, o_suffix=None,
                      lse_suffix=None, workspace: PrefixWorkspace | None = None, stream=None):
     """sr_prefix_attention: one token of every sequence over the prefix that the
@@ -631,24 +521,23 @@ def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out
     prefix_len positions of it), joined with each sequence's suffix when o_suffix
     and lse_suffix (decode_attention_partial's) are given. Returns out bf16 [B, Hq,
     128]; ``lse`` (fp32 [B, Hq]) receives the log-sum-exp (NaN for sink heads)."""
-    if out is None:
-        out = torch.empty_like(q)
-    _prefix("sr_prefix_attention", q, k_prefix, v_prefix, prefix_len, v0, route_mask, (o_suffix, lse_suffix), out, lse,
-            torch.bfloat16, workspace, stream)
+    if workspace is None:
+        workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
+    st, out, _ = _loaded().prefix(False, q, k_prefix, v_prefix, prefix_len, v0, route_mask, o_suffix, lse_suffix, out,
+                                  lse, workspace.ptr, workspace.nbytes, _handle(stream))
+    _check("sr_prefix_attention", st)
     return out
 
 
-@_on_tensor_device
 def prefix_attention_partial(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, o_part=None, lse_part=None,
                              workspace: PrefixWorkspace | None = None, stream=None):
     """sr_prefix_attention_partial: the prefix's part alone, as combine_partials
     takes it. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    if o_part is None:
-        o_part = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    if lse_part is None:
-        lse_part = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _prefix("sr_prefix_attention_partial", q, k_prefix, v_prefix, prefix_len, v0, route_mask, (), o_part, lse_part,
-            torch.float32, workspace, stream)
+    if workspace is None:
+        workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
+    st, o_part, lse_part = _loaded().prefix(True, q, k_prefix, v_prefix, prefix_len, v0, route_mask, None, None, o_part,
+                                            lse_part, workspace.ptr, workspace.nbytes, _handle(stream))
+    _check("sr_prefix_attention_partial", st)
     return o_part, lse_part
 
 

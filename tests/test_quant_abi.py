@@ -108,38 +108,29 @@ def test_prefix_attention(lib, partial):
     assert lib.sr_prefix_workspace_bytes(None) == 0
 
 
-def test_binding_refuses_mismatched_tensors():
-    """The library sees pointers: the binding holds every tensor against the cache's
-    shape and device (CPU tensors here: nothing reaches the library)."""
-    e, i32, bf16 = torch.float8_e4m3fn, torch.int32, torch.bfloat16
-    k = torch.zeros(2, 4, 9, 128, dtype=torch.uint8).view(e)
-    sc = torch.zeros(2, 4, 9, 2)
-    with pytest.raises(ValueError, match="8-bit"):
-        native._kv_type(k, None)
-    with pytest.raises(ValueError, match="k_cache"):
-        native._kv_type(k.view(torch.uint8), sc)
-    with pytest.raises(ValueError, match="k_cache"):
-        native._kv_type(k[0], sc)
+def test_binding_refuses_cpu_tensors_and_wrong_kinds(lib):
+    """What the binding refuses before it would look at a device: CPU tensors, things
+    that are no tensors, caches of another type or rank, scales that do not belong."""
+    i32, bf16 = torch.int32, torch.bfloat16
+    k = torch.zeros(2, 4, 9, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    sc, n = torch.zeros(2, 4, 9, 2), torch.zeros(2, dtype=i32)
     b = torch.zeros(2, 4, 9, 128, dtype=bf16)
-    with pytest.raises(ValueError, match="bfloat16"):
-        native._kv_type(b, sc, quant_only=False)
-    with pytest.raises(ValueError, match="k_cache"):
-        native._kv_type(b, None)
-    assert native._kv_type(k, sc) == native.SR_KV_E4M3 and native._kv_type(b, None, False) == native.SR_KV_BF16
-    assert native._kv_type(k.view(torch.int8), sc) == native.SR_KV_INT8
+    with pytest.raises(ValueError, match="CUDA"):
+        native.kv_dequant(k, k, sc, n, n, b, b)
+    with pytest.raises(ValueError, match="tensor"):
+        native.kv_dequant(None, k, sc, n, n, b, b)
+    with pytest.raises(ValueError, match="CUDA"):
+        native.kv_append_quant(b, b, n, n, k, k, sc)
+    with pytest.raises(ValueError, match="CUDA"):
+        native.prefix_attention(torch.zeros(2, 8, 128, dtype=bf16), b[0], b[0], 3, torch.zeros(2, 4, 128, dtype=bf16),
+                                torch.zeros(8, dtype=torch.uint8), workspace=_FakeWorkspace)
+    with pytest.raises(ValueError, match="CUDA"):
+        native.decode_attention_quant(torch.zeros(2, 8, 128, dtype=bf16), k, k, sc, b[:, :, 0].contiguous(), n, n,
+                                      workspace=_FakeWorkspace)
     with pytest.raises(ValueError, match="8-bit"):
         native.QuantCache(1, 1, 1, torch.float16, device="cpu")
-    x = torch.zeros(2, 3, 4, 128, dtype=bf16)
-    for bad in (x[:, :, :2], x.float(), x.transpose(2, 3)):
-        with pytest.raises(ValueError, match="k_new"):
-            native._row_strides(bad, "k_new", (2, 3, 4, 128), -1)
-    assert native._row_strides(x[:, :, 1:3], "k_new", (2, 3, 2, 128), -1).token == 512
-    for t, dtype, shape, what in ((x, bf16, (2, 3, 4, 128), "CUDA"), (x, torch.float32, (2, 3, 4, 128), "CUDA")):
-        with pytest.raises(ValueError, match=what):
-            native._arg(t, "x", dtype, shape, 0)
-    with pytest.raises(ValueError):  # CPU tensors never reach the library
-        native.kv_dequant(k, k, sc, torch.zeros(2, dtype=i32), torch.zeros(2, dtype=i32), b, b)
-    with pytest.raises(ValueError):
-        native.prefix_attention(torch.zeros(2, 8, 128, dtype=bf16), b[0], b[0], 3, torch.zeros(2, 4, 128, dtype=bf16),
-                                torch.zeros(8, dtype=torch.uint8))
     assert shared_prefix.SharedPrefixDecoder
+
+
+class _FakeWorkspace:
+    ptr, nbytes = FAKE, 1 << 30

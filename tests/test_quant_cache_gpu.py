@@ -551,6 +551,10 @@ def test_far_positions_of_a_cache_over_4_gib(dtype):
         assert ((lse[0, h].double() - torch.log(tot[:, 0])).abs() <= R.lse_bound(torch.log(tot[:, 0]), delta) + 2.0 ** -10).all()
 
 
+class _BadStream:
+    cuda_stream = "default"
+
+
 def test_binding_refusals_on_the_gpu():
     """Every tensor's shape, type, layout and device is held against the cache's."""
     c = native.QuantCache(2, 4, 9)
@@ -574,6 +578,23 @@ def test_binding_refusals_on_the_gpu():
             native.kv_append_quant(k_new, x, sl, sl, c.k, c.v, c.scales)
     with pytest.raises(native.SinkRouterError):
         native.kv_append_quant(x, x, sl, sl, c.k, c.v, c.scales, k0=v0)  # k0 without v0
+    with pytest.raises(ValueError, match="kv_scales"):
+        native.kv_append_quant(x, x, sl, sl, c.k, c.v, None)
+    cs = torch.zeros(20, 64, device=DEV)
+    kn = torch.zeros(2, 4, R.D, device=DEV, dtype=torch.bfloat16)
+    bf = torch.zeros(2, 4, 9, R.D, device=DEV, dtype=torch.bfloat16)
+    for cache, sc, tables, tau, off in ((bf, c.scales, cs, 0.6, 0), (c.k, None, cs, 0.6, 0), (c.k, c.scales, cs[:, :32], 0.6, 0),
+                                        (c.k, c.scales, cs, "x", 0), (c.k, c.scales, cs, math.nan, 0),
+                                        (c.k, c.scales, cs, 0.6, -1), (c.k, c.scales, cs, 0.6, 2 ** 40),
+                                        (c.k, c.scales, cs, 0.6, 0.5), (bf.float(), None, cs, 0.6, 0)):
+        with pytest.raises((ValueError, native.SinkRouterError)):
+            native.rope_append_route_kv(q, kn, kn, tables, tables, sl, cache, cache, sc, v0, v0, tau, pos_offset=off)
+    for bad in (dict(q_out=q[:1]), dict(route_mask=act), dict(active_list=act[:3]), dict(seq_lens_out=sl.long()),
+                dict(device_error=sl)):
+        with pytest.raises(ValueError):
+            native.rope_append_route_kv(q, kn, kn, cs, cs, sl, c.k, c.v, c.scales, v0, v0, 0.6, **bad)
+    with pytest.raises(ValueError):
+        native.decode_attention_quant(*good.values(), stream=_BadStream)
     assert native.kv_append_quant(x[:, :0], x[:, :0], sl, sl, c.k, c.v, c.scales)[0] is c.k  # no token: nothing to do
     torch.cuda.synchronize()
     assert not c.scales.any()
