@@ -90,7 +90,7 @@ typedef enum sr_status {
  *   active_list out int32 [1 + B*Hkv]: [0] = number of active units n, then
  *               their flat indices in ascending order; entries past 1+n are
  *               left untouched
- * One launch, two for more than 192 query rows; no workspace. Errors: SR_ERR_INVALID_ARG,
+ * One launch, two for many query rows (192, or 256 in groups of eight); no workspace. Errors: SR_ERR_INVALID_ARG,
  * SR_ERR_UNSUPPORTED, SR_ERR_CUDA.
  */
 sr_status sr_route(const sr_dims *dims, const void *q, const void *k0, float tau,
@@ -132,7 +132,7 @@ sr_status sr_route(const sr_dims *dims, const void *q, const void *k0, float tau
  *               max_pos)) -- its cache, k0/v0 and length are left untouched,
  *               its q_out rows are zero and its groups are routed from those
  *               rows (so the mask still equals sr_route(q_out, k0, tau))
- * One launch of a cluster of CTAs, or two launches for many units; no workspace.
+ * One launch, two for many units; no workspace.
  * It waits for the preceding kernel in the stream before reading anything and lets
  * the next one (sr_decode_attention, which reads all of its inputs after its own
  * wait) launch early. Errors: SR_ERR_INVALID_ARG, SR_ERR_UNSUPPORTED, SR_ERR_CUDA.

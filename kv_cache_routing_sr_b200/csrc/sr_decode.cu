@@ -80,17 +80,6 @@
 #define SR_DECODE_STAGES 2
 #endif
 
-// 8-bit caches: row blocks of 16 per consumer warp and tile, stages, consumer warps.
-#ifndef SR_QUANT_RB
-#define SR_QUANT_RB 2
-#endif
-#ifndef SR_QUANT_STAGES
-#define SR_QUANT_STAGES 2
-#endif
-#ifndef SR_QUANT_CW
-#define SR_QUANT_CW 8
-#endif
-
 SR_TL_DEFINE(tl_decode)
 #ifdef SR_TIMELINE
 // latest %globaltimer at which a decode CTA left (atomicMax); the next kernel
@@ -1533,13 +1522,14 @@ DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
 using DecodeCfg = Cfg<SR_DECODE_RB, SR_DECODE_STAGES, 4, SR_KV_BF16>;
-// 8-bit caches: eight consumer warps of two row blocks each, 256 rows in two 64 KB
-// stages. Measured back to back (128K with 4 of 8 groups active; four 64K..128K
-// sequences, M = 8): 29.0 and 101.6 us; 128 rows in four 32 KB stages take 31.9 and
-// 122.9 with eight warps, 31.2 and 129.3 with four; 256 rows on four warps 28.3 and
-// 104.5; 64 rows in eight stages 42.6 and 168.6. What a tile costs beside its bytes
-// (barriers, maxima, the scales' copy) is paid half as often.
-template <int KV> using QuantCfg = Cfg<SR_QUANT_RB, SR_QUANT_STAGES, SR_QUANT_CW, KV>;
+// 8-bit caches: 256 rows in two 64 KB stages, on eight consumer warps of two row
+// blocks each when a group has eight heads, else on four warps of four. Measured back
+// to back (4K and 128K with 4 of 8 groups active, M = 4; four 64K..128K sequences, M =
+// 8): eight warps 8.1, 29.0 and 101.6 us, four warps 7.8, 28.3 and 104.5. 128 rows in
+// four 32 KB stages take 31.9 and 122.9 (128K, M = 8) with eight warps, 31.2 and 129.3
+// with four; 64 rows in eight stages 42.6 and 168.6: what a tile costs beside its
+// bytes (barriers, maxima, the scales' copy) is paid half as often.
+template <int KV, bool EIGHT> using QuantCfg = Cfg<EIGHT ? 2 : 4, 2, EIGHT ? 8 : 4, KV>;
 
 // One kernel of the family: its launch shape.
 struct Variant {
@@ -1552,12 +1542,12 @@ template <class C, bool FUSED> Variant variant()
     return {decode_kernel<C, FUSED>, C::THREADS, C::ALLOC, C::BN};
 }
 
-Variant pick(int kv, bool fused)
+Variant pick(int kv, int group, bool fused)
 {
     if (kv == SR_KV_E4M3)
-        return variant<QuantCfg<SR_KV_E4M3>, false>();
+        return group == 8 ? variant<QuantCfg<SR_KV_E4M3, true>, false>() : variant<QuantCfg<SR_KV_E4M3, false>, false>();
     if (kv == SR_KV_INT8)
-        return variant<QuantCfg<SR_KV_INT8>, false>();
+        return group == 8 ? variant<QuantCfg<SR_KV_INT8, true>, false>() : variant<QuantCfg<SR_KV_INT8, false>, false>();
     return fused ? variant<DecodeCfg, true>() : variant<DecodeCfg, false>();
 }
 
@@ -1571,8 +1561,8 @@ cudaError_t configure(int dev, DeviceInfo &info)
         return e;
     // Every variant takes more than half of an SM's shared memory, so the
     // grid (one CTA per SM) is the same for all of them.
-    const Variant all[] = {pick(SR_KV_BF16, false), pick(SR_KV_BF16, true), pick(SR_KV_E4M3, false),
-                           pick(SR_KV_INT8, false)};
+    const Variant all[] = {pick(SR_KV_BF16, 1, false), pick(SR_KV_BF16, 1, true), pick(SR_KV_E4M3, 1, false),
+                           pick(SR_KV_E4M3, 8, false), pick(SR_KV_INT8, 1, false), pick(SR_KV_INT8, 8, false)};
     for (const Variant &v : all) {
         e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e != cudaSuccess)
@@ -1622,7 +1612,7 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream)
         return e;
     const int U = a.batch * a.n_kv_heads;
     CUtensorMap tmK, tmV;
-    const Variant v = pick(a.kv, a.fused);
+    const Variant v = pick(a.kv, a.n_q_heads / a.n_kv_heads, a.fused);
     const bool quant = a.kv != SR_KV_BF16;
     if (!make_cache_map(&tmK, a.k_cache, U, a.max_seq_len, v.rows, quant, a.max_seq_len) ||
         !make_cache_map(&tmV, a.v_cache, U, a.max_seq_len, v.rows, quant, a.max_seq_len))

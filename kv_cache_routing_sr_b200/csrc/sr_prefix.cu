@@ -510,20 +510,29 @@ template <int N> __device__ __forceinline__ void mask_columns(uint32_t (&x)[N / 
             x[c / 32][c % 32] = 0xff800000u;
 }
 
-// Largest of N logits, NaN if one is.
+// Largest of N logits, NaN if one is: N / 16 chains, so that one warp alone on its
+// scheduler does not wait for each comparison.
 template <int N> __device__ __forceinline__ float largest(const uint32_t (&x)[N / 32][32])
 {
-    float mx[4];
+    constexpr int kChains = N / 16;
+    float mx[kChains];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        auto at = [&](int i) { return __uint_as_float(x[(c * (N / 4) + i) / 32][(c * (N / 4) + i) % 32]); };
-        mx[c] = max_nan(at(0), at(1), at(2));
+    for (int c = 0; c < kChains; ++c)
+        mx[c] = max_nan(__uint_as_float(x[c / 2][c % 2 * 16]), __uint_as_float(x[c / 2][c % 2 * 16 + 1]),
+                        __uint_as_float(x[c / 2][c % 2 * 16 + 2]));
 #pragma unroll
-        for (int i = 3; i + 1 < N / 4; i += 2)
-            mx[c] = max_nan(mx[c], at(i), at(i + 1));
-        mx[c] = max_nan(mx[c], mx[c], at(N / 4 - 1));
-    }
-    return max_nan(max_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+    for (int i = 3; i < 15; i += 2)
+#pragma unroll
+        for (int c = 0; c < kChains; ++c)
+            mx[c] = max_nan(mx[c], __uint_as_float(x[c / 2][c % 2 * 16 + i]), __uint_as_float(x[c / 2][c % 2 * 16 + i + 1]));
+#pragma unroll
+    for (int c = 0; c < kChains; c += 2)
+        mx[c] = max_nan(mx[c], __uint_as_float(x[c / 2][15]), __uint_as_float(x[c / 2][31]));
+    float top = mx[0];
+#pragma unroll
+    for (int c = 1; c + 1 < kChains; c += 2)
+        top = max_nan(top, mx[c], mx[c + 1]);
+    return max_nan(top, mx[kChains - 1], mx[kChains - 1]);
 }
 
 // A row's reference m takes its new largest logit: l and O follow it.

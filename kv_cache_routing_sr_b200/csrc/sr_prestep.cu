@@ -25,11 +25,11 @@
 // correctly rounded bf16 rotation first and is quantised from that, by the
 // eight lanes that hold it, so the position-0 key is the bf16 row in either case.
 //
-// Layout: a cluster of eight CTAs of 512 threads with a share of the units each,
-// whose sink flags go to CTA 0's shared memory for the compaction; launches of
-// more than kClusterItems items a CTA use as many CTAs as give every item a
-// thread, and the routing kernel's compaction launch, which then also advances the
-// lengths. Per CTA, in one pass where each thread takes its own item:
+// Layout: one CTA of 512 threads for the smallest launches; else a cluster of eight
+// with a share of the units each, whose sink flags go to CTA 0's shared memory for
+// the compaction; launches of more than kClusterItems items a CTA use as many CTAs
+// as give every item a thread, and the routing kernel's compaction launch, which
+// then also advances the lengths. Per CTA, in one pass where each thread takes its own item:
 // eight threads per new key rotate it (each takes 8 elements and their 8
 // partners), write the cache slot, and stage the group's position-0 key (the
 // captured one at slot 0, else the stored k0); eight threads per query row
@@ -54,14 +54,17 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterCtas = 8;
-// Items (eight per query row and per new key) of one of eight CTAs, 512 threads:
-// beyond this, one chunk of 512 items a CTA and a second launch. Measured back to
-// back, cluster of eight against two launches: 3.7 us against 6.5 at 32 units (M =
-// 4), 6.0 / 6.6 at 128, 8.3 / 6.6 at 256, 25.9 / 6.8 at 1024; M = 8: 6.1 / 7.7 at 64
-// units, 8.1 / 7.8 at 128; M = 1: 5.0 / 6.5 at 256, 7.3 / 6.6 at 512. Fewer CTAs than
-// eight are no faster where they would give every item a thread (32 units, M = 1: 4.6
-// us on one, 3.3 on eight): the fp64 rotations spread over more SMs.
-constexpr int kClusterItems = 768;
+// How a launch is spread, by its items (eight per query row and per new key; a CTA
+// has 512 threads). Measured back to back:
+//   one CTA against a cluster of eight: 3.8 us against 4.0 at 320 items (8 units, M = 4);
+//   4.6 / 3.3 at 512 (32 units, M = 1), 5.2 / 4.1 at 576 (8 units, M = 8) -- the fp64
+//   rotations spread over more SMs;
+//   cluster against two launches: 3.7 / 6.5 at 1280 items (32 units, M = 4), 6.0 / 6.6 at
+//   5120, 8.3 / 6.6 at 10240, 25.9 / 6.8 at 40960; M = 8: 6.1 / 7.7 at 4608, 8.1 / 7.8 at 9216;
+//   M = 1: 5.0 / 6.5 at 4096, 7.3 / 6.6 at 8192.
+enum Spread { kOne, kCluster, kWide };
+constexpr int kOneItems = 384;
+constexpr int kClusterItems = 768; // a CTA
 
 struct PrestepParams {
     const __nv_bfloat16 *q_in, *k_new, *v_new;
@@ -164,10 +167,10 @@ __device__ __forceinline__ void load_table8(const float *tab, int pos, int j, fl
     v[1] = __ldg(t + 1);
 }
 
-template <int M, int KV, bool WIDE>
+template <int M, int KV, int SPREAD>
 __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepParams p, int cu)
 {
-    extern __shared__ __align__(128) uint8_t dsm[]; // [cu*(M+1)*256 staged rows][cluster: B*Hkv sink flags]
+    extern __shared__ __align__(128) uint8_t dsm[]; // [cu*(M+1)*256 staged rows][B*Hkv sink flags, unless wide]
     __shared__ int32_t warp_cnt[kWarps];
     __shared__ int32_t warp_off[kWarps + 1];
 
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     uint4 *rows = reinterpret_cast<uint4 *>(dsm);
     uint8_t *sink_flag = dsm + (size_t)cu * (M + 1) * 256;
     uint8_t *all_flags = sink_flag; // CTA 0's, which compacts the active list
-    if constexpr (!WIDE) {
+    if constexpr (SPREAD == kCluster) {
         all_flags = cooperative_groups::this_cluster().map_shared_rank(sink_flag, 0);
         cooperative_groups::this_cluster().barrier_arrive();
     }
@@ -268,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
         }
     }
     __syncthreads();
-    if constexpr (!WIDE)
+    if constexpr (SPREAD == kCluster)
         cooperative_groups::this_cluster().barrier_wait(); // CTA 0 runs: its shared memory may be written
     route_units_warp<M, false>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
-        if constexpr (!WIDE)
+        if constexpr (SPREAD != kWide)
             all_flags[u0 + lu] = sink ? 1 : 0;
         p.mask[u0 + lu] = sink ? 1 : 0;
     });
@@ -279,24 +282,26 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
 
     if (p.error && __syncthreads_or(bad_slot) && threadIdx.x == 0)
         atomicOr(p.error, SR_DEVERR_APPEND_SLOT);
-    if constexpr (WIDE)
-        return;
-    cooperative_groups::this_cluster().sync();
-    if (blockIdx.x != 0)
-        return;
-    // Every other read of seq_lens, and every flag, is behind the barriers above.
-    for (int b = threadIdx.x; b < p.B; b += kThreads)
-        p.seq_lens_out[b] = p.seq_lens[b] + (slot_of(p, b) >= 0 ? 1 : 0);
-    compact_active<kThreads>(sink_flag, U, p.active, warp_cnt, warp_off);
+    if constexpr (SPREAD != kWide) {
+        if constexpr (SPREAD == kCluster) {
+            cooperative_groups::this_cluster().sync();
+            if (blockIdx.x != 0)
+                return;
+        }
+        // Every other read of seq_lens, and every flag, is behind the barriers above.
+        for (int b = threadIdx.x; b < p.B; b += kThreads)
+            p.seq_lens_out[b] = p.seq_lens[b] + (slot_of(p, b) >= 0 ? 1 : 0);
+        compact_active<kThreads>(sink_flag, U, p.active, warp_cnt, warp_off);
+    }
 }
 
-template <int M, int KV, bool WIDE>
+template <int M, int KV, int SPREAD>
 cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
 {
     const int U = a.batch * a.n_kv_heads;
-    // Units a CTA. Wide: one thread an item (8 a row, M + 1 rows a unit).
-    const int cu = WIDE ? kThreads / (8 * (M + 1)) : (U + kClusterCtas - 1) / kClusterCtas;
-    const size_t smem = (size_t)cu * (M + 1) * 256 + (WIDE ? 0 : (size_t)U);
+    // Units a CTA. Wide: one thread an item.
+    const int cu = SPREAD == kWide ? kThreads / (8 * (M + 1)) : SPREAD == kOne ? U : (U + kClusterCtas - 1) / kClusterCtas;
+    const size_t smem = (size_t)cu * (M + 1) * 256 + (SPREAD == kWide ? 0 : (size_t)U);
     PrestepParams p;
     p.q_in = static_cast<const __nv_bfloat16 *>(a.q_in);
     p.k_new = static_cast<const __nv_bfloat16 *>(a.k_new);
@@ -322,7 +327,7 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     p.pos_offset = a.pos_offset;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(WIDE ? (unsigned)((U + cu - 1) / cu) : (unsigned)kClusterCtas);
+    cfg.gridDim = dim3(SPREAD == kWide ? (unsigned)((U + cu - 1) / cu) : SPREAD == kOne ? 1u : (unsigned)kClusterCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -334,9 +339,9 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = WIDE ? 1 : 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M, KV, WIDE>, p, cu);
-    if (e != cudaSuccess || !WIDE)
+    cfg.numAttrs = SPREAD == kCluster ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_append_route_kernel<M, KV, SPREAD>, p, cu);
+    if (e != cudaSuccess || SPREAD != kWide)
         return e;
     CompactArgs c{};
     c.mask = a.mask;
@@ -353,9 +358,11 @@ cudaError_t launch_m(const PrestepArgs &a, cudaStream_t stream)
 
 template <int M, int KV> cudaError_t launch_kv(const PrestepArgs &a, cudaStream_t stream)
 {
-    const int cluster_units = (a.batch * a.n_kv_heads + kClusterCtas - 1) / kClusterCtas;
-    return cluster_units * 8 * (M + 1) > kClusterItems ? launch_m<M, KV, true>(a, stream)
-                                                       : launch_m<M, KV, false>(a, stream);
+    const int units = a.batch * a.n_kv_heads;
+    if (units * 8 * (M + 1) <= kOneItems)
+        return launch_m<M, KV, kOne>(a, stream);
+    return (units + kClusterCtas - 1) / kClusterCtas * 8 * (M + 1) <= kClusterItems ? launch_m<M, KV, kCluster>(a, stream)
+                                                                                    : launch_m<M, KV, kWide>(a, stream);
 }
 
 template <int M> cudaError_t launch_group(const PrestepArgs &a, cudaStream_t stream)

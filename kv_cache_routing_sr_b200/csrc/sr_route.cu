@@ -13,7 +13,7 @@
 // the key row straight from global memory, and shuffle reductions give each
 // pair's cosine and the group's minimum (sr_route_math.cuh). A warp with more
 // groups to route issues the loads of its next group before reducing the
-// current one. Launches of more than kOneCtaRows query rows give every warp one
+// current one. Launches of more than kOneCtaRows<M> query rows give every warp one
 // chunk of units on as many CTAs as that takes, and compact in a second launch.
 // The compaction writes active units in ascending order with warp
 // ballots and a block prefix, so no CTA of the decode kernel is ever bound to a
@@ -153,15 +153,16 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(CompactArgs a)
 }
 
 // Query rows up to which one CTA routes and compacts. Measured back to back, one
-// CTA against two launches: 1.3 us against 3.5 at 32 rows, 3.5 / 3.5 at 192 (M = 4),
-// 3.4 / 3.7 at 192 (M = 1), 4.4 / 3.8 at 384 (M = 8), 58.8 / 4.1 at 8192.
-constexpr int kOneCtaRows = 192;
+// CTA against two launches: 1.3 us against 3.5 at 32 rows, 3.5 / 3.5 at 192 (M = 4), 3.4 /
+// 3.7 at 192 (M = 1), 4.0 / 3.7 at 256 (M = 1); M = 8: 3.3 / 3.9 at 256, 4.4 / 3.8 at 384,
+// 58.8 / 4.1 at 8192.
+template <int M> constexpr int kOneCtaRows = M == 8 ? 256 : 192;
 
 template <int M>
 cudaError_t launch_route_m(const RouteArgs &a, cudaStream_t stream)
 {
     const int U = a.batch * a.n_kv_heads;
-    const bool wide = U * M > kOneCtaRows;
+    const bool wide = U * M > kOneCtaRows<M>;
     constexpr int kUnits = kRouteWarps * RouteLanes<M>::UNITS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(wide ? (unsigned)((U + kUnits - 1) / kUnits) : 1u);
