@@ -63,7 +63,8 @@ constexpr int kItemRows = 2 * kRows; // rows an item
 constexpr int kGridCap = 256;        // persistent CTAs never exceed this (sizes the workspace)
 constexpr int kQHalfBytes = kRows * 128, kQBytes = 2 * kQHalfBytes;
 
-constexpr int kThreads = 384;        // two softmax warpgroups, one for copies and MMAs
+constexpr int kThreads = 384;        // two softmax warpgroups, one for copies and MMAs:
+                                     // 168 registers a thread, of which the last gives some up
 constexpr int kSoftmaxWarps = 8;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
 
@@ -76,10 +77,6 @@ template <int TILE> struct Form {
     static constexpr int kSmem = kOffBar + 512 + 1024; // and room to align the base to 1024 B
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
-#ifndef SR_PREFIX_POLY
-#define SR_PREFIX_POLY 0
-#endif
-constexpr int kPolyOf8 = SR_PREFIX_POLY; // pairs of 8 whose 2^x is a polynomial
 constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
 
 // Workspace: [error word | total weight | active count, first item of each KV head | active
@@ -258,28 +255,6 @@ __device__ __forceinline__ float max_nan(float a, float b, float c)
     return d;
 }
 
-// 2^y of a pair without the special-function unit: y = n + f with n the nearest
-// integer (added and taken off as 1.5 2^23 + n), 2^f on [-1/2, 1/2] by the degree-4
-// polynomial of least largest relative error (2.7e-6, mean 4e-8; Remez exchange), n
-// added to its exponent. y below -126 counts as -126; y must be below 127.
-__device__ __forceinline__ void exp2_poly2(uint64_t y2, float &a, float &b)
-{
-    unpack2(y2, a, b);
-    y2 = pack2(a < -126.f ? -126.f : a, b < -126.f ? -126.f : b);
-    const uint64_t t = add2(y2, pack2(12582912.f, 12582912.f));
-    const uint64_t f = sub2(y2, add2(t, pack2(-12582912.f, -12582912.f)));
-    uint64_t r = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
-                      pack2(0.05591785907745361f, 0.05591785907745361f));
-    r = fma2(r, f, pack2(0.240247443318367f, 0.240247443318367f));
-    r = fma2(r, f, pack2(0.6931217908859253f, 0.6931217908859253f));
-    r = fma2(r, f, pack2(0.9999992847442627f, 0.9999992847442627f));
-    float ta, tb, ra, rb;
-    unpack2(t, ta, tb);
-    unpack2(r, ra, rb);
-    a = __uint_as_float(__float_as_uint(ra) + (__float_as_uint(ta) << 23));
-    b = __uint_as_float(__float_as_uint(rb) + (__float_as_uint(tb) << 23));
-}
-
 // A CTA's part of one item: tiles [j0, j1).
 struct Segment {
     int item, j0, j1;
@@ -327,29 +302,17 @@ struct Streams {
 
 // Copies come in the order of their first use: the keys of the first `look` steps (or
 // tiles), then each one's values and the next keys. Places of the keys and values of
-// step t of n in that sequence of 2 n copies.
+// number t of n in that sequence of 2 n copies.
 __device__ __forceinline__ int key_at(int look, int t) { return t < look ? t : 2 * t + 1 - look; }
 __device__ __forceinline__ int value_at(int look, int t, int n)
 {
     return min(look, n) + t + min(t, max(n - look, 0));
 }
 
-// Narrow form: the stages form two rings. Streams over the same tiles share one sequence, whose
-// copies alternate between the rings; streams over alternate tiles have a ring each.
-// So whoever waits for a ring waits for its copies in order, and a barrier's parity
-// is never two phases off.
-struct Place {
-    uint32_t stage, parity;
-};
-
+// Narrow form: each stream has a ring of half the stages to itself, so that its MMA
+// warp waits for every copy of the ring, in order, and a barrier's parity is never two
+// phases off.
 constexpr int kRing = Form<64>::kStages / 2;
-
-__device__ __forceinline__ Place place_of(bool two, int s, int at, uint32_t used0, uint32_t used1)
-{
-    const int ring = two ? at & 1 : s;
-    const uint32_t i = (ring ? used1 : used0) + (two ? at >> 1 : at);
-    return {ring * kRing + i % kRing, (i / kRing) & 1};
-}
 
 // Narrow form: the barrier that step t of stream s uses, of the pair that its steps
 // use in turn, as a byte offset, and the parity of its phase. done: steps of earlier
@@ -379,8 +342,7 @@ __device__ __forceinline__ uint32_t scan_prologue(Shared *sh, const CUtensorMap 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Form<TILE>::kStages; ++s) {
             mbar_init(smem_u32(&sh->full[s]), 1);
-            // narrow: one arrival a stream, or two of the one that used the tile
-            mbar_init(smem_u32(&sh->empty[s]), TILE == 64 ? 2 : 1);
+            mbar_init(smem_u32(&sh->empty[s]), 1);
         }
         mbar_init(smem_u32(&sh->q_full), kSoftmaxWarps);
         mbar_init(smem_u32(&sh->seg_done), kSoftmaxWarps);
@@ -474,8 +436,8 @@ template <int TILE> __device__ __forceinline__ void issue_output(uint32_t d, uin
         mma_ts(d, tp + k * 8, b + k * (2048 >> 4), bf16_idesc(kRows, kHeadDim, true), accumulate || k > 0);
 }
 
-// The row of a segment's item in a softmax thread's lane (past the item: none). Narrow
-// streams of at most 64 rows: the second stream's start at lane 64, so that the
+// The row of a segment's item in a softmax thread's lane (past the item: none). Of two
+// streams over the same rows, at most 64, the second's start at lane 64, so that the
 // streams' rows fall to different schedulers.
 __device__ __forceinline__ int row_of(bool two, int rows, int s, int row)
 {
@@ -565,13 +527,9 @@ __device__ __forceinline__ float weights64(const uint32_t (&x0)[32], const uint3
         const uint64_t y =
             fma2(pack2(__uint_as_float(src[(2 * i) & 31]), __uint_as_float(src[(2 * i + 1) & 31])), scale2, nsub2);
         float a, b;
-        if ((i & 7) < kPolyOf8) {
-            exp2_poly2(y, a, b);
-        } else {
-            unpack2(y, a, b);
-            a = exp2_approx(a);
-            b = exp2_approx(b);
-        }
+        unpack2(y, a, b);
+        a = exp2_approx(a);
+        b = exp2_approx(b);
         sum[i & 1] = add2(sum[i & 1], pack2(a, b));
         w[i] = pack_bf16x2(a, b);
     }
@@ -618,7 +576,7 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const uint32_t tmem = scan_prologue<64>(sh, &tmK, &tmV, warp, lane);
 
     Walk walk(p);
-    Segment seg;
+    Segment seg{};
     bool ok = true;
 
     // The copy and MMA warps run converged and elect the issuing lane at each issue:
@@ -629,26 +587,21 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies
             uint32_t used0 = 0, used1 = 0; // copies issued to each ring
-            auto copy = [&](const CUtensorMap *map, int ring, int g, int j) -> bool {
+            auto copy = [&](const CUtensorMap *map, int j) -> bool { // tile j of the segment
+                const int ring = j & 1;
                 const uint32_t i = ring ? used1 : used0, st = ring * kRing + i % kRing;
                 if (!wait_warp(empty0 + 8 * st, ((i / kRing) & 1) ^ 1, abort_flag))
                     return false;
-                copy_tile<64>(smem, map, st, full0 + 8 * st, j, g);
+                copy_tile<64>(smem, map, st, full0 + 8 * st, seg.j0 + j, seg.it.x);
                 ++(ring ? used1 : used0);
                 return true;
             };
             while (ok && walk.next(seg)) {
-                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
-                const int g = seg.it.x, lead = st.two ? 2 : 4;
-                // Shared sequence: copy i goes to ring i % 2. Alternate tiles: tile j to
-                // ring j % 2.
-                for (int j = 0; ok && j < min(lead, st.n); ++j)
-                    ok = copy(&tmK, j & 1, g, seg.j0 + j);
-                for (int j = 0; ok && j < st.n; ++j) {
-                    const int at = value_at(2, j, st.n);
-                    ok = copy(&tmV, (st.two ? at : j) & 1, g, seg.j0 + j) &&
-                         (j + lead >= st.n || copy(&tmK, (st.two ? at + 1 : j) & 1, g, seg.j0 + j + lead));
-                }
+                const int n = seg.j1 - seg.j0; // each stream looks two steps ahead: four tiles
+                for (int j = 0; ok && j < min(4, n); ++j)
+                    ok = copy(&tmK, j);
+                for (int j = 0; ok && j < n; ++j)
+                    ok = copy(&tmV, j) && (j + 4 >= n || copy(&tmK, j + 4));
             }
             // Copies in flight land before the CTA can leave.
             volatile int never = 0;
@@ -662,52 +615,46 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             // ---------------------------------------------- MMAs, a warp a stream
             const int s = warp - kMmaWarp;
             const uint32_t tO = tmem + 256 + s * 128, sq = smem_u32(smem + F::kOffQ + s * kQBytes);
-            uint32_t used0 = 0, used1 = 0, nseg = 0; // copies of earlier segments in each ring; segments
-            uint32_t done0 = 0, done1 = 0;           // steps of earlier segments, by their parity
+            const uint32_t ring = smem_u32(smem + F::kOffRing + s * kRing * F::kTileBytes);
+            const uint32_t full = full0 + 8 * s * kRing, empty = empty0 + 8 * s * kRing;
+            uint32_t used = 0, nseg = 0;   // copies of earlier segments in the ring; segments
+            uint32_t done0 = 0, done1 = 0; // steps of earlier segments, by their parity
             while (ok && walk.next(seg)) {
-                const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
-                const int steps = st.steps(s);
+                const int steps = Streams{false, seg.j1 - seg.j0}.steps(s);
                 if (!(ok = wait_warp(q_full, nseg & 1, abort_flag)))
                     break;
                 tc_fence_after();
-                auto release = [&](uint32_t stage) {
-                    mma_commit(empty0 + 8 * stage);
-                    if (!st.two)
-                        mma_commit(empty0 + 8 * stage);
-                };
                 // S of step t into its buffer
                 auto logits = [&](int t) -> bool {
-                    const auto [stage, parity] = place_of(st.two, s, key_at(2, t), used0, used1);
-                    if (!wait_warp(full0 + 8 * stage, parity, abort_flag))
+                    const uint32_t i = used + key_at(2, t), stage = i % kRing;
+                    if (!wait_warp(full + 8 * stage, (i / kRing) & 1, abort_flag))
                         return false;
                     if (elect_one()) {
-                        issue_logits<64>(tmem + s * 128 + (t & 1) * 64, sq, smem_u32(smem + F::kOffRing + stage * F::kTileBytes));
+                        issue_logits<64>(tmem + s * 128 + (t & 1) * 64, sq, ring + stage * F::kTileBytes);
                         mma_commit(s_full + turn_of(s, t, done0, done1).off);
-                        release(stage);
+                        mma_commit(empty + 8 * stage);
                     }
                     __syncwarp();
                     return true;
                 };
                 ok = (steps < 1 || logits(0)) && (steps < 2 || logits(1));
                 for (int t = 0; ok && t < steps; ++t) {
-                    const auto [stage, parity] = place_of(st.two, s, value_at(2, t, steps), used0, used1);
+                    const uint32_t i = used + value_at(2, t, steps), stage = i % kRing;
                     const Turn turn = turn_of(s, t, done0, done1);
-                    if (!(ok = wait_warp(full0 + 8 * stage, parity, abort_flag) &&
+                    if (!(ok = wait_warp(full + 8 * stage, (i / kRing) & 1, abort_flag) &&
                                wait_warp(p_full + turn.off, turn.parity, abort_flag)))
                         break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_output<64>(tO, tmem + s * 128 + (t & 1) * 64,
-                                         smem_u32(smem + F::kOffRing + stage * F::kTileBytes), t > 0);
+                        issue_output<64>(tO, tmem + s * 128 + (t & 1) * 64, ring + stage * F::kTileBytes, t > 0);
                         mma_commit(o_full + turn.off);
-                        release(stage);
+                        mma_commit(empty + 8 * stage);
                     }
                     __syncwarp();
                     if (t + 2 < steps)
                         ok = logits(t + 2);
                 }
-                used0 += (uint32_t)(st.two ? st.n : 2 * st.steps(0));
-                used1 += (uint32_t)(st.two ? st.n : 2 * st.steps(1));
+                used += 2 * (uint32_t)steps;
                 done0 += (steps + 1) / 2;
                 done1 += steps / 2;
                 ++nseg;
@@ -723,8 +670,8 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         const uint32_t tO = tmem + 256 + s * 128 + lanes;
         uint32_t done0 = 0, done1 = 0, nseg = 0; // steps of earlier segments, by their parity; segments
         while (walk.next(seg)) {
-            const Streams st{seg.it.z > kRows, seg.j1 - seg.j0};
-            const int qrow = row_of(st.two, seg.it.z, s, row);
+            const Streams st{false, seg.j1 - seg.j0};
+            const int qrow = row_of(false, seg.it.z, s, row);
             const bool mine = qrow < seg.it.z;
             const bool busy = __any_sync(kFull, mine); // a warp without a row only keeps the barriers' count
             // Every earlier MMA that read Q is complete (both groups have met below).
@@ -814,7 +761,7 @@ scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const uint32_t tmem = scan_prologue<128>(sh, &tmK, &tmV, warp, lane);
 
     Walk walk(p);
-    Segment seg;
+    Segment seg{};
     bool ok = true;
 
     if (warp >= kSoftmaxWarps) {

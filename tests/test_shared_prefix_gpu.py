@@ -67,6 +67,8 @@ CASES = [
     (70, 8, 8, 3001, 3001),   # 24 items of 24 tiles: a CTA's share ends one item and begins the next
     (3, 64, 1, 2100, 2100),   # 64 items of few rows, likewise
     (20, 33, 8, 700, 700),    # 160 rows a KV head: every item has more than one row tile
+    (1, 700, 1, 70, 71),      # more KV heads than the plan takes at a time
+    (1500, 1, 2, 65, 65),     # one KV head, twelve items
 ]
 
 
