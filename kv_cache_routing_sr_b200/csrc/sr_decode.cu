@@ -603,7 +603,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             }
             atomicOr(&bitmap[u >> 5], 1u << (u & 31));
             ltab[i] = L;
-            local += L;
         }
     } else {
         // Routing inside the kernel: every input may come from the preceding
@@ -632,7 +631,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 atomicOr(&bitmap[u >> 5], 1u << (u & 31));
                 ltab[i] = L;
                 utab[i] = (int16_t)u;
-                local += L;
                 if (blockIdx.x == 0 && p.active_out)
                     p.active_out[1 + i] = u;
             }
@@ -641,8 +639,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         if (blockIdx.x == 0 && tid == 0 && p.active_out)
             p.active_out[0] = n;
     }
+    // More than kFastUnits units: each thread sums the lengths of a run of consecutive
+    // ranks, so that one block scan gives the total and where each run starts.
+    const int run = (n + kThreads - 1) / kThreads, run0 = tid * run;
+    long long run_start = 0;
     if (!fast) {
-        (void)block_scan<kThreads / 32>(local, misc, &P);
+        __syncthreads(); // the length table is complete
+        for (int i = run0; i < n && i < run0 + run; ++i)
+            local += ltab[i];
+        run_start = block_scan<kThreads / 32>(local, misc, &P) - local;
         if (errbits && blockIdx.x == 0)
             atomicOr(p.err, errbits);
     }
@@ -714,20 +719,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             __syncwarp();
         }
     } else {
-        if (p.n_splits == 0 && P > 0 && r0 < P) { // find the active entry whose positions contain r0
-            long long carry = 0;
-            for (int base = 0; base < n; base += kThreads) {
-                const int i = base + tid;
-                const int L = (i < n) ? ltab[i] : 0;
-                long long tot;
-                const long long incl = block_scan<kThreads / 32>(L, misc, &tot);
-                const long long S = carry + incl - L;
-                if (i < n && L > 0 && S <= r0 && r0 < S + L) {
-                    misc->i0 = i;
-                    misc->s0 = S;
-                }
-                carry += tot;
-            }
+        // the active entry whose positions contain r0
+        if (p.n_splits == 0 && run_start <= r0 && r0 < run_start + local) {
+            int i = run0;
+            long long S = run_start;
+            while (S + ltab[i] <= r0)
+                S += ltab[i++];
+            misc->i0 = i;
+            misc->s0 = S;
         }
         // Generic stores into the stage buffers (tables) must be ordered
         // before the TMA writes that will reuse those bytes.
