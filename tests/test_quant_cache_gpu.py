@@ -648,3 +648,70 @@ def test_prefill_then_decode_steps(dtype):
                 under = vd.shape[0] * 2.0 ** -39 * float(vd.abs().max())
                 assert ((out[b, h].double() - oo).abs() <= R.bound(oo, a, delta, R.HALF_F16, R.HALF_BF16, under)).all()
     assert dec.workspace.device_error() == 0
+
+
+@both
+@pytest.mark.parametrize("B,Hkv,M", [(1, 8, 4), (40, 8, 2)], ids=["few", "many"])
+def test_captured_append_steps_advance(B, Hkv, M, dtype):
+    """append_step in a CUDA graph: every replay takes the next slot of what the
+    lengths then are, like eager steps on a second cache; a full cache is reported and
+    left alone."""
+    Lmax, Hq = 24, Hkv * M
+    cs, sn = inputs.rope_tables(Lmax, device=DEV)
+    proj = [inputs.make_projections(B, Hq, Hkv, seed=70 + i, device=DEV) for i in range(5)]
+    side = []
+    for _ in range(2):
+        c = native.QuantCache(B, Hkv, Lmax, dtype)
+        k0, v0 = (torch.zeros(B, Hkv, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+        seq = torch.tensor([(5 * b) % 20 for b in range(B)], dtype=torch.int32, device=DEV)
+        fill = torch.randn(B, Lmax, Hkv, R.D, generator=gen(3), device=DEV).to(torch.bfloat16)
+        native.kv_append_quant(fill, fill, torch.zeros_like(seq), seq, c.k, c.v, c.scales, k0, v0)
+        side.append((c, k0, v0, seq, native.QuantDecoder(B, Hq, Hkv, Lmax), torch.zeros(1, dtype=torch.int32, device=DEV)))
+    q, kn, vn = (torch.empty_like(x) for x in proj[0])
+    step = lambda s, x: s[4].append_step(*x, cs, sn, s[0], s[1], s[2], s[3], TAU, device_error=s[5])  # noqa: E731
+    for x in (q, kn, vn):
+        x.zero_()
+    graph = torch.cuda.CUDAGraph()
+    warm = [t.clone() for t in (side[0][0].k.view(torch.uint8), side[0][0].v.view(torch.uint8), side[0][0].scales,
+                                side[0][1], side[0][2], side[0][3])]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step(side[0], (q, kn, vn))
+    torch.cuda.current_stream().wait_stream(stream)
+    with torch.cuda.graph(graph):
+        step(side[0], (q, kn, vn))
+    for t, w in zip((side[0][0].k.view(torch.uint8), side[0][0].v.view(torch.uint8), side[0][0].scales, side[0][1],
+                     side[0][2], side[0][3]), warm):
+        t.copy_(w)
+    side[0][5].zero_()
+    for x in proj:
+        for dst, src in zip((q, kn, vn), x):
+            dst.copy_(src)
+        graph.replay()
+        want = step(side[1], x)
+        torch.cuda.synchronize()
+        assert torch.equal(side[0][4].out, want)
+        for a, b in zip(side[0][1:4], side[1][1:4]):
+            assert torch.equal(a, b)
+        assert torch.equal(side[0][0].k.view(torch.uint8), side[1][0].k.view(torch.uint8))
+        assert torch.equal(side[0][0].scales, side[1][0].scales)
+    assert int(side[0][5]) == int(side[1][5]) == (native.SR_DEVERR_APPEND_SLOT if B > 4 and max((5 * b) % 20 for b in range(B)) + 5 > Lmax else 0)
+    assert int(side[0][3].max()) <= Lmax
+
+
+def test_scan_of_units_that_are_one_split_each():
+    """Many short units (a split each, written without a partial) against the same
+    units cut into three splits: the same attention inside both bounds, and bf16 out
+    equal to the rounded fp32 partial."""
+    B, Hkv, M, Lmax = 60, 4, 2, 300
+    lens = [1 + (37 * b) % Lmax for b in range(B)]
+    for dtype in R.DTYPES:
+        c = filled_cache(B, Hkv, Lmax, lens, dtype, 31)
+        q = torch.randn(B, Hkv * M, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+        v0 = torch.randn(B, Hkv, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+        mask = torch.rand(B, Hkv, generator=gen(3), device=DEV) < 0.2
+        for ns in (0, 1, 3):
+            out, lse, o = scan(q, c, v0, lens, mask, ns)
+            check_scan(q, c, v0, lens, mask.tolist(), out, lse, o)
+            assert torch.equal(out, o.to(torch.bfloat16))

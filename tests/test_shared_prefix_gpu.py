@@ -132,6 +132,23 @@ def test_prefix_extreme_logits(case):
     check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.view(B, Hkv).tolist(), out, lse)
 
 
+@pytest.mark.parametrize("B,M", [(2, 4), (40, 8)], ids=["narrow", "wide"])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_prefix_propagates_nan(where, B, M):
+    """A NaN inside the prefix reaches every active row of its KV head, and no other."""
+    Hkv, Lp = 3, 500
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    (k if where == "k" else v)[1, 333, 5] = math.nan
+    mask = torch.zeros(B, Hkv, dtype=torch.uint8, device=DEV)
+    mask[0, 1] = 1
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse).view(B, Hkv, M, R.D)
+    assert torch.isfinite(out[:, [0, 2]]).all() and torch.equal(out[0, 1], v0[0, 1].expand(M, -1))
+    bad = torch.isnan(out[1:, 1])
+    assert bad.all() if where == "k" else (bad[..., 5].all() and not bad[..., :5].any() and not bad[..., 6:].any())
+
+
 def suffix_of(kind, B, Hkv, n, seed):
     k, v = randn((B, n, Hkv, R.D), seed), randn((B, n, Hkv, R.D), seed + 1)
     if kind == "bf16":
