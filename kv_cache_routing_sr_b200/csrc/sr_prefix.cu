@@ -1182,9 +1182,9 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
             e = launch(scan_wide_kernel, (unsigned)p.grid, kThreads, Form<128>::kSmem, stream, tmK, tmV, p);
     }
     if (e == cudaSuccess) {
-        // Few rows have many partials each (the grid is spread over few items): a
-        // CTA a row. 128K prefix, 8 sequences, 74 partials a row: 32 us with a warp a
-        // row, @@ with a CTA.
+        // Few rows have many partials each (the grid is spread over few items): a CTA
+        // a row. The whole call, a warp a row against a CTA: 107.8 us / 93.1 for 256 rows
+        // over 128K, 68.8 / 58.9 for 1024 over 32K, 57.0 / 67.7 for 2048.
         const long long rows = (long long)a.batch * a.n_q_heads;
         if (rows <= kWholeRows)
             e = launch(join_kernel<true>, (unsigned)rows, 32 * kJoinWarps, 0, stream, p);
