@@ -26,15 +26,15 @@
 // than 2^8 since the reference it uses (the weights stay below 2^8 of their row's sum,
 // far inside bf16 and fp32), once the previous tile's product is complete.
 //
-// It has two forms. Launches of at most 128 rows a KV head are bound by the prefix's
-// bytes: the narrow form works in 64-position tiles with two S buffers a stream and
-// an MMA warp each, so that a copied tile is used as soon as it has landed and the
-// ring's ten 16 KB stages are in flight rather than waiting. More rows are bound by
-// the tensor cores and the exponentials: the wide form works in 128-position tiles
-// (an S product of 128 columns reads Q from shared memory half as often: 75 cycles a
-// 128x128x16 step against 57 a 128x64x16), and one MMA warp issues P0 V and S0 of the
-// next tile, then P1 V and S1 of the next tile, which keeps the streams half a turn
-// apart: one has the tensor cores while the other has the exponentials.
+// It has two forms. The wide form works in 128-position tiles (an S product of 128
+// columns reads Q from shared memory half as often: 75 cycles a 128x128x16 step
+// against 57 a 128x64x16), and one MMA warp issues P0 V and S0 of the next tile, then
+// P1 V and S1 of the next tile, which keeps the streams half a turn apart: one has the
+// tensor cores while the other has the exponentials. Many rows are bound by those two,
+// few rows by the prefix's bytes. A short prefix with at most 128 rows a KV head gives
+// a CTA only a few tiles, whose latency counts: the narrow form works in 64-position
+// tiles, with two S buffers a stream and an MMA warp each, so that a copied tile is
+// used as soon as it has landed and the shares are cut half as coarse.
 //
 // Every wait is bounded in time; a timeout sets a device error bit, and the CTA
 // leaves once its own copies and MMAs have landed.
@@ -1110,6 +1110,7 @@ cudaError_t grid_of(int *grid)
 }
 
 constexpr long long kWholeRows = 1024;
+constexpr int kShortPrefix = 4096;
 
 template <typename... Args>
 cudaError_t launch(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
@@ -1168,7 +1169,10 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
     p.M = a.n_q_heads / a.n_kv_heads;
     p.prefix_len = a.prefix_len;
     p.row_cap = w.row_cap;
-    p.tile = a.batch * p.M > kRows ? 128 : 64;
+    // At most 128 rows a KV head, narrow form against wide, the whole call in us: 14.0 /
+    // 16.1 for 32 KV heads over 577 positions, 23.6 / 25.8 for 32 over 2048, 15.1 / 15.0 for
+    // 8 over 4096, 22.9 / 21.3 for 8 over 8192, 58.9 / 52.4 for 8 over 32768 (128 rows).
+    p.tile = a.batch * p.M <= kRows && a.prefix_len < kShortPrefix ? 64 : 128;
 
     e = launch(plan_kernel, 1, kPlanThreads, 0, stream, p);
     if (e == cudaSuccess && a.prefix_len > 0) {

@@ -63,6 +63,11 @@ CASES = [
     (40, 2, 8, 2500, 2500),   # 320 rows
     (64, 1, 8, 257, 300),     # 512 rows
     (2, 2, 8, 40000, 40000),  # long, few rows: many splits
+    (5, 3, 8, 4095, 4096),    # the last length of a short prefix, and the first of a long one
+    (5, 3, 8, 4096, 4096),
+    (16, 5, 8, 8191, 8192),   # 128 rows a KV head
+    (2, 40, 2, 4500, 4500),   # 40 items of few rows over a long prefix
+    (1, 1, 1, 9000, 9001),
     (129, 3, 1, 384, 384),
     (70, 8, 8, 3001, 3001),   # 24 items of 24 tiles: a CTA's share ends one item and begins the next
     (3, 64, 1, 2100, 2100),   # 64 items of few rows, likewise
@@ -132,11 +137,11 @@ def test_prefix_extreme_logits(case):
     check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.view(B, Hkv).tolist(), out, lse)
 
 
-@pytest.mark.parametrize("B,M", [(2, 4), (40, 8)], ids=["narrow", "wide"])
+@pytest.mark.parametrize("B,M,Lp", [(2, 4, 500), (40, 8, 500), (2, 4, 6000)], ids=["narrow", "wide", "wide_few_rows"])
 @pytest.mark.parametrize("where", ["k", "v"])
-def test_prefix_propagates_nan(where, B, M):
+def test_prefix_propagates_nan(where, B, M, Lp):
     """A NaN inside the prefix reaches every active row of its KV head, and no other."""
-    Hkv, Lp = 3, 500
+    Hkv = 3
     q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
     k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
     (k if where == "k" else v)[1, 333, 5] = math.nan
