@@ -15,7 +15,7 @@
 //    of positions) sequence, in which a tile weighs 2 for an item of more than 128
 //    rows and 1 for a smaller one, and leaves one partial (m, l, O) a row for every
 //    item its share touches.
-//  * join: one warp (or CTA) a query head combines its partials, and the suffix's.
+//  * join: the partials of every query head are combined, and the suffix's.
 //
 // scan, per CTA: two streams, each with a softmax warpgroup (a thread a row), its
 // logits S in TMEM (128 x 128 fp32 columns in all) and its output O (128 x 128); a copy
@@ -934,151 +934,213 @@ scan_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 // ---- join -------------------------------------------------------------------------------
 
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBatch = 8; // partials in flight a thread
+constexpr int kJoinBatch = 4; // partials in flight a thread, four loads each
+constexpr int kJoinRows = 4;  // query heads a warp: eight lanes each
 
-// (m, l, acc) += parts k0, k0 + step, ... below n of `part`, lane c holding columns
-// 4c .. 4c + 3: lane i fetches the batch's i-th (m, l), and the weights reach the
-// other lanes by shuffles. A part with l = 0 has no O.
-template <typename Part>
-__device__ __forceinline__ void add_parts(const Params &p, Part &&part, int pr, int k0, int step, int n, int lane, float &m,
-                                          float &l, float4 &acc)
+// A row's partials (m, l, acc) += k0, k0 + step, ... below n, `stride` rows of (m, l)
+// apart from `ml` on, their columns from `o` on. Eight lanes (the low bits, `sub`) share
+// a row: element i of acc is columns 32 i + 4 sub .. + 3. Lane i of them fetches the
+// batch's i-th (m, l), and the weights reach the others by shuffles. A part with l = 0
+// has no O. n may differ between the rows of a warp.
+__device__ __forceinline__ void add_parts(const float2 *ml, const float *o, size_t stride, int row_cap, int k0, int step,
+                                          int n, int lane, float &m, float &l, float4 (&acc)[4])
 {
-    for (; k0 < n; k0 += step * 32) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (k0 + lane * step < n)
-            ml = __ldcg(p.ml + part(k0 + lane * step) + pr);
-        float mb = ml.y == 0.f ? -INFINITY : ml.x;
+    const int sub = lane & 7;
+    o += (size_t)(sub >> 1) * row_cap * 8 + (sub & 1) * 4;
+    for (; __any_sync(kFull, k0 < n); k0 += step * 8) {
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (k0 + sub * step < n)
+            x = __ldcg(ml + (k0 + sub * step) * stride);
+        float mb = x.y == 0.f ? -INFINITY : x.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o));
+        for (int b = 4; b > 0; b >>= 1)
+            mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, b));
         const float mn = fmaxf(m, mb);
         const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - mn);
-        float ls = ml.y * w;
+        const float w = x.y == 0.f ? 0.f : exp2f(x.x - mn);
+        float ls = x.y * w;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            ls += __shfl_xor_sync(kFull, ls, o);
+        for (int b = 4; b > 0; b >>= 1)
+            ls += __shfl_xor_sync(kFull, ls, b);
         l = l * keep + ls;
-        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-        const int nb = min(32, (n - k0 + step - 1) / step);
-        for (int i0 = 0; i0 < nb; i0 += kJoinBatch) {
-            float4 o[kJoinBatch];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            acc[c].x *= keep, acc[c].y *= keep, acc[c].z *= keep, acc[c].w *= keep;
+        const unsigned used = __ballot_sync(kFull, w != 0.f); // NaN too
+#pragma unroll 1
+        for (int i0 = 0; i0 < 8 && (used >> i0 & 0x01010101u * ((1u << kJoinBatch) - 1u)); i0 += kJoinBatch) {
+            float4 y[kJoinBatch][4];
             float wi[kJoinBatch];
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) {
-                wi[i] = __shfl_sync(kFull, w, (i0 + i) & 31);
-                if (i0 + i >= nb)
-                    wi[i] = 0.f;
-                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wi[i] != 0.f)
-                    o[i] = __ldcg(reinterpret_cast<const float4 *>(
-                        p.o + part(k0 + (i0 + i) * step) * kHeadDim + ((size_t)(lane >> 1) * p.row_cap + pr) * 8 +
-                        (lane & 1) * 4));
+                wi[i] = __shfl_sync(kFull, w, (lane & 24) + i0 + i);
+                const float4 *from = reinterpret_cast<const float4 *>(o + (k0 + (i0 + i) * step) * stride * kHeadDim);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    y[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (wi[i] != 0.f)
+                        y[i][c] = __ldcg(from + (size_t)c * 8 * row_cap);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) {
-                acc.x = fmaf(o[i].x, wi[i], acc.x);
-                acc.y = fmaf(o[i].y, wi[i], acc.y);
-                acc.z = fmaf(o[i].z, wi[i], acc.z);
-                acc.w = fmaf(o[i].w, wi[i], acc.w);
-            }
+            for (int i = 0; i < kJoinBatch; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    acc[c].x = fmaf(y[i][c].x, wi[i], acc[c].x);
+                    acc[c].y = fmaf(y[i][c].y, wi[i], acc[c].y);
+                    acc[c].z = fmaf(y[i][c].z, wi[i], acc[c].z);
+                    acc[c].w = fmaf(y[i][c].w, wi[i], acc[c].w);
+                }
         }
         m = mn;
     }
 }
 
-// One warp a query head, or (kWhole) a CTA of eight, each with every eighth
-// partial; lane c owns elements 4c .. 4c + 3.
-template <bool kWhole> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
+// How the query heads are spread. Four heads a warp where there are enough of them:
+// the partials keep eight columns of consecutive rows side by side, so that the heads
+// of a group make whole lines of them.
+enum class Join {
+    kWarpFour, // a warp four heads, all partials
+    kCtaFour,  // a CTA four heads, its warps every eighth partial
+    kCtaOne    // a CTA one head, eight lanes every 32nd partial
+};
+
+template <Join J> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p)
 {
-    __shared__ float4 sh_acc[kJoinWarps][32];
-    __shared__ float2 sh_ml[kJoinWarps];
+    constexpr bool one = J == Join::kCtaOne, split = J != Join::kWarpFour;
+    constexpr int kParts = J == Join::kCtaFour ? 4 : 1; // float4 of a thread's that meet in shared memory
+    __shared__ float4 sh_acc[kJoinWarps][kParts][32];
+    __shared__ float2 sh_ml[kJoinWarps][kJoinRows];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = kWhole ? (long long)blockIdx.x : (long long)blockIdx.x * kJoinWarps + warp; // b * Hq + h
-    if (row >= (long long)p.B * p.Hq)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane >> 3;
+    const long long rows = (long long)p.B * p.Hq;
+    const long long row0 = one ? blockIdx.x : kJoinRows * (split ? blockIdx.x : (long long)blockIdx.x * kJoinWarps + warp);
+    const long long row = one ? row0 : row0 + group; // b * Hq + h
+    if (row0 >= rows)
         return;
     const int b = (int)(row / p.Hq), h = (int)(row - (long long)b * p.Hq), g = h / p.M;
     const size_t u = (size_t)b * p.Hkv + g;
-    const int rank = __ldcg(p.rank + u);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float lse = __int_as_float(0x7fc00000); // sink heads
-    if (rank < 0) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v0 + u * kHeadDim) + lane);
-        acc = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                          __uint_as_float(v.y & 0xffff0000u));
-    } else {
-        float m = -INFINITY, l = 0.f;
-        const int nt = (p.prefix_len + p.tile - 1) / p.tile;
-        if (nt > 0) {
-            const int r = rank * p.M + (h - g * p.M);
-            const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
-            const int4 it = __ldcg(p.items + item);
-            const bool two = it.z > kRows;
-            const long long share = share_of(__ldcg(p.weight), nt, p.grid), begin = it.w * item_cost(nt);
-            const int w = weight_of(it.z);
-            const int c0 = (int)((begin + (long long)kEntry * w) / share);
-            const int c1 = (int)((begin + (long long)(kEntry + nt - 1) * w) / share);
-            // Partials k: of CTA c0 + k, or of its two streams
-            const int n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
-            auto part = [&](int k) -> size_t {
-                const size_t slot = (size_t)(c0 + (two ? k : k >> 1)) + item;
-                return (slot * 2 + (two ? ir / kRows : k & 1)) * p.row_cap;
-            };
-            add_parts(p, part, ir % kRows, kWhole ? warp : 0, kWhole ? kJoinWarps : 1, n, lane, m, l, acc);
-        }
-        if constexpr (kWhole) {
-            sh_acc[warp][lane] = acc;
-            if (lane == 0)
-                sh_ml[warp] = make_float2(m, l);
-            __syncthreads();
-            m = -INFINITY;
-            l = 0.f;
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w)
-                m = fmaxf(m, sh_ml[w].x);
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                const float2 ml = sh_ml[w];
-                const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
-                const float4 o = sh_acc[w][lane];
-                l = fmaf(ml.y, f, l);
-                acc.x = fmaf(o.x, f, acc.x);
-                acc.y = fmaf(o.y, f, acc.y);
-                acc.z = fmaf(o.z, f, acc.z);
-                acc.w = fmaf(o.w, f, acc.w);
-            }
-        }
-        // acc and l are in units of 2^m; join the suffix's normalised part
-        lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        float wp = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
-        float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.o_suffix) {
-            const float ls = __ldg(p.lse_suffix + row), top = fmaxf(lse, ls);
-            if (ls != -INFINITY) {
-                os = __ldg(reinterpret_cast<const float4 *>(p.o_suffix + (size_t)row * kHeadDim) + lane);
-                const float ep = expf(lse - top), es = expf(ls - top), tot = ep + es;
-                wp *= ep / tot;
-                ws = es / tot;
-                lse = top + logf(tot);
-            }
-        }
-        acc.x = acc.x * wp + os.x * ws;
-        acc.y = acc.y * wp + os.y * ws;
-        acc.z = acc.z * wp + os.z * ws;
-        acc.w = acc.w * wp + os.w * ws;
+    const int rank = row < rows ? __ldcg(p.rank + u) : -1;
+    const int nt = (p.prefix_len + p.tile - 1) / p.tile;
+    float m = -INFINITY, l = 0.f;
+    float4 acc[4] = {};
+    int n = 0, pr = 0;
+    size_t first = 0, stride = 0; // of its partials
+    if (rank >= 0 && nt > 0) {
+        const int r = rank * p.M + (h - g * p.M);
+        const int item = __ldcg(p.first + g) + r / kItemRows, ir = r % kItemRows;
+        const int4 it = __ldcg(p.items + item);
+        const bool two = it.z > kRows;
+        const long long share = share_of(__ldcg(p.weight), nt, p.grid), begin = it.w * item_cost(nt);
+        const int w = weight_of(it.z);
+        const int c0 = (int)((begin + (long long)kEntry * w) / share);
+        const int c1 = (int)((begin + (long long)(kEntry + nt - 1) * w) / share);
+        // CTAs c0 .. c1: one partial each, of the stream that has the row, or both streams'
+        n = two ? c1 - c0 + 1 : 2 * (c1 - c0 + 1);
+        first = ((size_t)(c0 + item) * 2 + (two ? ir / kRows : 0)) * p.row_cap;
+        stride = (size_t)(two ? 2 : 1) * p.row_cap;
+        pr = ir % kRows;
     }
-    if (kWhole && warp != 0)
+    add_parts(p.ml + first + pr, p.o + first * kHeadDim + pr * 8, stride, p.row_cap,
+              one ? kJoinRows * warp + group : split ? warp : 0, one ? kJoinRows * kJoinWarps : split ? kJoinWarps : 1, n,
+              lane, m, l, acc);
+    if constexpr (one) { // the warp's four
+        float top = m;
+#pragma unroll
+        for (int d = 8; d < 32; d <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+        const float f = l == 0.f ? 0.f : exp2f(m - top);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            acc[c].x *= f, acc[c].y *= f, acc[c].z *= f, acc[c].w *= f;
+#pragma unroll
+        for (int d = 8; d < 32; d <<= 1) {
+            l += __shfl_xor_sync(kFull, l, d);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[c].x += __shfl_xor_sync(kFull, acc[c].x, d);
+                acc[c].y += __shfl_xor_sync(kFull, acc[c].y, d);
+                acc[c].z += __shfl_xor_sync(kFull, acc[c].z, d);
+                acc[c].w += __shfl_xor_sync(kFull, acc[c].w, d);
+            }
+        }
+    }
+    if constexpr (split) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if constexpr (one) {
+                if (group == c)
+                    sh_acc[warp][0][lane] = acc[c];
+            } else {
+                sh_acc[warp][c % kParts][lane] = acc[c];
+            }
+        }
+        if ((lane & 7) == 0)
+            sh_ml[warp][group] = make_float2(m, l);
+        __syncthreads();
+        if (warp >= kParts) // the others finish, with a float4 of the row a thread
+            return;
+        m = -INFINITY;
+        l = 0.f;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w)
+            m = fmaxf(m, sh_ml[w][group].x);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float2 ml = sh_ml[w][group];
+            const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+            const float4 o = sh_acc[w][warp][lane];
+            l = fmaf(ml.y, f, l);
+            acc[0].x = fmaf(o.x, f, acc[0].x);
+            acc[0].y = fmaf(o.y, f, acc[0].y);
+            acc[0].z = fmaf(o.z, f, acc[0].z);
+            acc[0].w = fmaf(o.w, f, acc[0].w);
+        }
+    }
+    if (row >= rows)
         return;
-    if (p.lse && lane == 0)
-        p.lse[row] = lse;
-    if (p.out_f32)
-        reinterpret_cast<float4 *>(p.out_f32 + (size_t)row * kHeadDim)[lane] = acc;
-    else
-        reinterpret_cast<uint2 *>(p.out + (size_t)row * kHeadDim)[lane] =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    // acc and l are in units of 2^m; join the suffix's normalised part
+    float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    float wp = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
+    bool suffix = false;
+    if (p.o_suffix && rank >= 0) {
+        const float ls = __ldg(p.lse_suffix + row), top = fmaxf(lse, ls);
+        if ((suffix = ls != -INFINITY)) {
+            const float ep = expf(lse - top), es = expf(ls - top), tot = ep + es;
+            wp *= ep / tot;
+            ws = es / tot;
+            lse = top + logf(tot);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < (split ? 1 : 4); ++c) {
+        const int at = one ? lane : 8 * (split ? warp : c) + (lane & 7); // of the row's 32 float4
+        float4 x = acc[c];
+        if (rank < 0) { // a sink head
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v0 + u * kHeadDim) + at);
+            x = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                            __uint_as_float(v.y & 0xffff0000u));
+        } else {
+            float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (suffix)
+                os = __ldg(reinterpret_cast<const float4 *>(p.o_suffix + (size_t)row * kHeadDim) + at);
+            x.x = x.x * wp + os.x * ws;
+            x.y = x.y * wp + os.y * ws;
+            x.z = x.z * wp + os.z * ws;
+            x.w = x.w * wp + os.w * ws;
+        }
+        if (p.out_f32)
+            reinterpret_cast<float4 *>(p.out_f32 + (size_t)row * kHeadDim)[at] = x;
+        else
+            reinterpret_cast<uint2 *>(p.out + (size_t)row * kHeadDim)[at] =
+                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+    if (p.lse && (one ? lane == 0 : (lane & 7) == 0) && (!split || warp == 0))
+        p.lse[row] = rank < 0 ? __int_as_float(0x7fc00000) : lse;
 }
 
 // ---- host side ------------------------------------------------------------------------
@@ -1109,7 +1171,7 @@ cudaError_t grid_of(int *grid)
     return cudaSuccess;
 }
 
-constexpr long long kWholeRows = 1024;
+constexpr long long kJoinOne = 384, kJoinFour = 4096;
 constexpr int kShortPrefix = 4096;
 
 template <typename... Args>
@@ -1186,14 +1248,19 @@ cudaError_t launch_prefix(const PrefixArgs &a, cudaStream_t stream)
             e = launch(scan_wide_kernel, (unsigned)p.grid, kThreads, Form<128>::kSmem, stream, tmK, tmV, p);
     }
     if (e == cudaSuccess) {
-        // Few rows have many partials each (the grid is spread over few items): a CTA
-        // a row. The whole call, a warp a row against a CTA: 107.8 us / 93.1 for 256 rows
-        // over 128K, 68.8 / 58.9 for 1024 over 32K, 57.0 / 67.7 for 2048.
-        const long long rows = (long long)a.batch * a.n_q_heads;
-        if (rows <= kWholeRows)
-            e = launch(join_kernel<true>, (unsigned)rows, 32 * kJoinWarps, 0, stream, p);
+        // The fewer the rows, the more partials each has (the grid is spread over fewer
+        // items), and the more of the GPU a row needs. The whole call in us with a CTA a
+        // row, a CTA four, a warp four: 90.8 / 93.4 / 122 for 256 rows over 128K; 40.5 /
+        // 40.0 / 64.5 for 512, 53.5 / 48.3 / 73.5 for 1024, 108 / 86 / 85 for 4096
+        // and 192 / 145 / 135 for 8192 over 32K.
+        const long long rows = (long long)a.batch * a.n_q_heads, quads = (rows + kJoinRows - 1) / kJoinRows;
+        if (rows <= kJoinOne)
+            e = launch(join_kernel<Join::kCtaOne>, (unsigned)rows, 32 * kJoinWarps, 0, stream, p);
+        else if (rows <= kJoinFour)
+            e = launch(join_kernel<Join::kCtaFour>, (unsigned)quads, 32 * kJoinWarps, 0, stream, p);
         else
-            e = launch(join_kernel<false>, (unsigned)((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream, p);
+            e = launch(join_kernel<Join::kWarpFour>, (unsigned)((quads + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0,
+                       stream, p);
     }
     return e;
 }
