@@ -55,6 +55,8 @@ typedef enum sr_status {
 
 /* Largest B*Hkv the kernels accept. */
 #define SR_MAX_UNITS 16384
+/* n_splits of sr_decode_attention_partial: automatic, and short units stay whole */
+#define SR_SPLITS_BY_UNIT (-1)
 /* Largest forced split count per unit. */
 #define SR_MAX_SPLITS 4096
 
@@ -281,6 +283,10 @@ sr_status sr_route_decode_attention(const sr_dims *dims, const void *q, const vo
  *            (q . k_j / sqrt(d)) over those positions; NaN for sink heads
  * Every rank must route identically (same q, k0, tau) and pass the same active
  * list; seq_lens holds the lengths of this call's shard (>= 1 each).
+ * n_splits may also be SR_SPLITS_BY_UNIT: automatic, but where the active units
+ * have fewer than 256 positions on average, a share is that average times the
+ * units a CTA has to take, so that many short units spread over all SMs (the
+ * bits of the result then differ from n_splits = 0, as between any two splits).
  * Errors: as sr_decode_attention.
  */
 sr_status sr_decode_attention_partial(const sr_dims *dims, const void *q, const void *k_cache,
@@ -464,7 +470,8 @@ sr_status sr_rope_append_route_kv(const sr_dims *dims, int32_t kv_type, int32_t 
  *               positions >= L_b are never used and may be anything
  *   lse         optional out fp32 [B, Hq] (NULL = not wanted), as for
  *               sr_decode_attention_lse
- * Other arguments, results, workspace and errors: as sr_decode_attention.
+ * Other arguments, results, workspace and errors: as sr_decode_attention;
+ * n_splits = 0 cuts shares as SR_SPLITS_BY_UNIT does.
  */
 sr_status sr_decode_attention_quant(const sr_dims *dims, int32_t kv_type, const void *q, const void *k_cache,
                                     const void *v_cache, const float *kv_scales, const void *v0,

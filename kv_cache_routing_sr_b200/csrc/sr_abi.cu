@@ -319,7 +319,7 @@ sr_status sr_decode_attention_partial(const sr_dims *dims, const void *q, const 
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(v0, 16) ||
         !aligned(o_part, 16) || !aligned(seq_lens, 4) || !aligned(active_list, 4) || !aligned(lse_part, 4))
         return SR_ERR_INVALID_ARG;
-    if (n_splits < 0 || n_splits > SR_MAX_SPLITS)
+    if (n_splits < SR_SPLITS_BY_UNIT || n_splits > SR_MAX_SPLITS)
         return SR_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256))
         return SR_ERR_WORKSPACE;

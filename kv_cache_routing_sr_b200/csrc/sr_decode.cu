@@ -15,7 +15,8 @@
 //  * Automatic splits: the active positions of all units are concatenated and
 //    cut into one contiguous chunk per CTA (rounded to whole tiles, >= 256
 //    positions), so every SM streams the same number of bytes whatever the mix
-//    of unit lengths. A chunk may cover the end of one unit and the start of
+//    of unit lengths; 8-bit caches, and bf16 ones on request, shares of the mean
+//    length times the units a CTA where that mean is below 256. A chunk may cover the end of one unit and the start of
 //    the next; each (CTA, unit) overlap is one split.
 //  * The producer lane walks its splits tile by tile and issues 3-D TMA loads
 //    (two 128-byte-wide boxes for K, two for V, 128B swizzle) into a ring of
@@ -169,6 +170,7 @@ struct Params {
     float *part_o;
     float2 *part_ml;
     int B, Hq, Hkv, M, Lmax, n_splits;
+    bool by_unit; // automatic splits of short units follow the units
     // fused routing (sr_route_decode_attention) only
     const __nv_bfloat16 *k0;
     float tau;
@@ -658,9 +660,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     // the plan; its first emit only writes the header and arrives.
     bool early = false;
     if (p.n_splits == 0 && P > 0) {
-        chunk = div_nonneg(P + G - 1, G);
-        chunk = (chunk + C::BN - 1) / C::BN * C::BN;
-        chunk = chunk < kMinChunk ? kMinChunk : chunk;
+        // A split costs about 3 us besides its bytes: where the units are short, the
+        // shares hold as few of them as the grid allows, rather than 256 positions.
+        const long long mean = p.by_unit ? div_nonneg(P + n - 1, n) : kMinChunk;
+        if (mean < kMinChunk) {
+            chunk = mean * ((n + G - 1) / G);
+        } else {
+            chunk = div_nonneg(P + G - 1, G);
+            chunk = (chunk + C::BN - 1) / C::BN * C::BN;
+            chunk = chunk < kMinChunk ? kMinChunk : chunk;
+        }
         r0 = (long long)blockIdx.x * chunk;
         r1 = r0 + chunk < P ? r0 + chunk : P;
     }
@@ -1632,7 +1641,8 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream)
     p.Hkv = a.n_kv_heads;
     p.M = a.n_q_heads / a.n_kv_heads;
     p.Lmax = a.max_seq_len;
-    p.n_splits = a.n_splits;
+    p.n_splits = a.n_splits > 0 ? a.n_splits : 0;
+    p.by_unit = a.n_splits == SR_SPLITS_BY_UNIT || a.kv != SR_KV_BF16;
     p.k0 = static_cast<const __nv_bfloat16 *>(a.k0);
     p.tau = a.tau;
     p.mask_out = a.mask_out;

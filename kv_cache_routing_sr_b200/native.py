@@ -23,6 +23,7 @@ SR_DEVERR_APPEND_SLOT, SR_DEVERR_ROW_COUNT = 8, 16
 SR_KV_BF16, SR_KV_E4M3, SR_KV_INT8 = range(3)
 SR_MAX_UNITS = 16384
 SR_MAX_SPLITS = 4096
+SPLITS_BY_UNIT = -1
 HEAD_DIM = 128
 
 
@@ -307,7 +308,8 @@ def decode_attention_partial(q, k_cache, v_cache, k0, v0, seq_lens, active_list,
                              n_splits: int = 0, workspace: Workspace | None = None, stream=None):
     """sr_decode_attention_partial: the scan over this cache's positions with
     fp32 normalised outputs o_part [B, Hq, 128] and natural-log lse_part [B, Hq]
-    (NaN for sink heads), ready for combine_partials. Returns (o_part, lse_part)."""
+    (NaN for sink heads), ready for combine_partials. ``n_splits`` may be
+    SPLITS_BY_UNIT. Returns (o_part, lse_part)."""
     B, Hq, d = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
     if o_part is None:
@@ -315,7 +317,7 @@ def decode_attention_partial(q, k_cache, v_cache, k0, v0, seq_lens, active_list,
     if lse_part is None:
         lse_part = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = Workspace(B, Hq, Hkv, Lmax, n_splits, device=q.device)
+        workspace = Workspace(B, Hq, Hkv, Lmax, max(n_splits, 0), device=q.device)
     dims = dims_of(B, Hq, Hkv, Lmax, d)
     k0p = _dev(k0, "k0", torch.bfloat16) if k0 is not None else None
     st = load().sr_decode_attention_partial(

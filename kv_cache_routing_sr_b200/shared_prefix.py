@@ -49,7 +49,7 @@ class SharedPrefixDecoder:
         s = self.suffix
         if kv_scales is None:
             native.decode_attention_partial(q, k_cache, v_cache, None, v0, seq_lens, s.active_list, self.o_suffix,
-                                            self.lse_suffix, n_splits, s.workspace, stream)
+                                            self.lse_suffix, n_splits or native.SPLITS_BY_UNIT, s.workspace, stream)
         else:
             native.decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens, s.active_list,
                                                   self.o_suffix, self.lse_suffix, n_splits, s.workspace, stream)

@@ -90,6 +90,15 @@ def test_decode_attention_quant(lib, partial):
             (dict(ws=None), WS), (dict(ws=FAKE + 128), WS), (dict(wsb=need - 1), WS)])
 
 
+def test_splits_by_unit_belong_to_the_partial_form(lib):
+    order = ["q", "kc", "vc", "k0", "v0", "sl", "act", "ns"]
+    part = caller(lib, "sr_decode_attention_partial", [*order, "o", "lse", "ws", "wsb"], dict(ws=None, wsb=1 << 30))
+    whole = caller(lib, "sr_decode_attention", [*order, "o", "ws", "wsb"], dict(ws=None, wsb=1 << 30))
+    # the workspace is looked at after the splits
+    refuses(part, [(dict(ns=native.SPLITS_BY_UNIT), WS), (dict(ns=0), WS), (dict(ns=-2), INV)])
+    refuses(whole, [(dict(ns=native.SPLITS_BY_UNIT), INV), (dict(ns=0), WS)])
+
+
 @pytest.mark.parametrize("partial", [False, True])
 def test_prefix_attention(lib, partial):
     order = ["Lp", "q", "k", "v", "v0", "mask"] + ([] if partial else ["os", "ls"]) + ["o", "lse", "ws", "wsb"]

@@ -388,6 +388,14 @@ SCANS = [
     (1, 8, 4, 20011, [20011], 0),
     (1, 2, 8, 4099, [4099], 37),
     (40, 2, 2, 67, [1 + (13 * i) % 67 for i in range(40)], 0),  # more than 32 units
+    # short units, whose shares follow the units: fewer than the grid's CTAs, more, many
+    (4, 8, 4, 9, [9, 1, 3, 9], 0),
+    (1, 32, 1, 255, [255], 0),
+    (7, 32, 1, 2, [2, 1, 2, 2, 1, 1, 2], 0),
+    (54, 32, 1, 2, [1 + i % 2 for i in range(54)], 0),
+    (60, 5, 8, 3, [1 + i % 3 for i in range(60)], 0),
+    (64, 8, 2, 2000, [2000] + [1 + i % 7 for i in range(63)], 0),  # one long sequence among short ones
+    (3, 8, 8, 300, [300, 220, 247], 0),  # an average of just less than a whole share
 ]
 
 

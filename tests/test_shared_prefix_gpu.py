@@ -202,6 +202,30 @@ def test_shared_prefix_step(B, Hkv, M, Lp, kind):
     check(q, parts, v0, mask, joined, None)
 
 
+@pytest.mark.parametrize("B,Hkv,M,cap,top", [(4, 8, 4, 9, 9), (7, 32, 1, 2, 2), (54, 32, 1, 40, 3), (60, 4, 8, 300, 300),
+                                            (1, 1, 1, 1, 1)])
+def test_short_bf16_suffixes_by_unit(B, Hkv, M, cap, top):
+    """SPLITS_BY_UNIT against 64 bits, and against the shares of whole tiles."""
+    lens = [1 + (7 * b + top - 1) % top for b in range(B)]
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((B, Hkv, cap, R.D), 3), randn((B, Hkv, cap, R.D), 4)
+    mask = [[(3 * b + g) % 5 == 4 for g in range(Hkv)] for b in range(B)]
+    units = [b * Hkv + g for b in range(B) for g in range(Hkv) if not mask[b][g]]
+    active = torch.tensor([len(units), *units] + [-1] * (B * Hkv - len(units)), dtype=torch.int32, device=DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = native.Workspace(B, Hkv * M, Hkv, cap)
+    for b in range(B):
+        k[b, :, lens[b]:], v[b, :, lens[b]:] = math.nan, math.nan
+    parts = lambda b, g, rows: [R.attention(rows, k[b, g], v[b, g], lens[b])]  # noqa: E731
+    for ns in (native.SPLITS_BY_UNIT, 0):
+        o, z = native.decode_attention_partial(q, k, v, None, v0, sl, active, n_splits=ns, workspace=ws)
+        assert ws.device_error() == 0
+        check(q, parts, v0, mask, o, z, R.HALF_F32)
+    o2, z2 = native.decode_attention_partial(q, k, v, None, v0, sl, active, n_splits=native.SPLITS_BY_UNIT)
+    o1, z1 = native.decode_attention_partial(q, k, v, None, v0, sl, active, n_splits=native.SPLITS_BY_UNIT, workspace=ws)
+    assert torch.equal(o1, o2) and torch.equal(torch.nan_to_num(z1, nan=-7.0), torch.nan_to_num(z2, nan=-7.0))
+
+
 def test_join_with_an_empty_part():
     """A suffix (or prefix) without a position weighs nothing; both empty give 0."""
     B, Hkv, M, Lp = 2, 2, 4, 50
