@@ -20,7 +20,9 @@
 // are streaming ones.
 //
 // Measured, inputs larger than L2: 131 us for the 128K x 8 rows of a prompt (814 MB,
-// 6.2 TB/s); with 58 registers and four blocks per SM in place of 40 and six 144 us.
+// 6.2 TB/s); with 58 registers and four blocks per SM in place of 40 and six 144 us. To
+// int8, whose quotients take five operations a value, 154 us (162 with four blocks); with
+// an operation a value in place of two, and every lane with both rows' divisions, 173.
 // Reading 32K x 8 rows back takes 34.1 us (203 MB, 6.0 TB/s); with cached loads 38.0, and
 // with 16 consecutive values a lane, whose stores cover half sectors, 39.7.
 #include <cuda_bf16.h>
@@ -81,6 +83,8 @@ template <int KV> __global__ void __launch_bounds__(kThreads, 6) write_kernel(Kv
             if (a.error)
                 atomicOr(a.error, SR_DEVERR_APPEND_SLOT);
         }
+        if (!__any_sync(0xffffffffu, live))
+            continue;
         uint4 x[2][2] = {};
         if (live) {
             const uint4 *k = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k_new) +
@@ -92,23 +96,44 @@ template <int KV> __global__ void __launch_bounds__(kThreads, 6) write_kernel(Kv
             x[1][0] = __ldcs(v + j);
             x[1][1] = __ldcs(v + j + 8);
         }
-        RowQuant rq[2];
-        uint2 codes[2][2];
+        uint32_t w[2][8], top = 0u; // top: of the key in the low half, of the value in the high one
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint32_t w[8] = {x[s][0].x, x[s][0].y, x[s][0].z, x[s][0].w,
-                                   x[s][1].x, x[s][1].y, x[s][1].z, x[s][1].w};
             uint32_t m = 0u;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                m = abs_max_bf16x2(m, w[e]);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-            rq[s] = row_quant<KV>(max(m & 0xffffu, m >> 16));
-            codes[s][0] = make_uint2(quant4<KV>(w[0], w[1], rq[s]), quant4<KV>(w[2], w[3], rq[s]));
-            codes[s][1] = make_uint2(quant4<KV>(w[4], w[5], rq[s]), quant4<KV>(w[6], w[7], rq[s]));
+            for (int e = 0; e < 8; ++e) {
+                const uint4 &y = x[s][e >> 2];
+                w[s][e] = e % 4 == 0 ? y.x : e % 4 == 1 ? y.y : e % 4 == 2 ? y.z : y.w;
+                m = abs_max_bf16x2(m, w[s][e]);
+            }
+            top |= max(m & 0xffffu, m >> 16) << (16 * s);
         }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        RowQuant rq[2];
+        if constexpr (KV == SR_KV_E4M3) {
+            rq[0] = row_quant<KV>(top & 0xffffu);
+            rq[1] = row_quant<KV>(top >> 16);
+        } else { // three divisions: even lanes do the key's, odd ones the value's
+            const RowQuant mine = row_quant<KV>(j & 1 ? top >> 16 : top & 0xffffu);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int from = (lane & 24) + s;
+                rq[s].scale = __shfl_sync(0xffffffffu, mine.scale, from);
+                rq[s].mul = __shfl_sync(0xffffffffu, mine.mul, from);
+                rq[s].up = __shfl_sync(0xffffffffu, mine.up, from);
+                rq[s].f = __shfl_sync(0xffffffffu, mine.f, from);
+                rq[s].rcp = __shfl_sync(0xffffffffu, mine.rcp, from);
+            }
+        }
+        uint2 codes[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                codes[s][h] = make_uint2(quant4<KV>(w[s][4 * h], w[s][4 * h + 1], rq[s]),
+                                         quant4<KV>(w[s][4 * h + 2], w[s][4 * h + 3], rq[s]));
         if (!live)
             continue;
         const size_t u = (size_t)it.b * a.n_kv_heads + it.g;

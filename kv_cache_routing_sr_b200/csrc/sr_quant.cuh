@@ -29,6 +29,13 @@ __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t acc, uint32_t w)
     return __vmaxu2(acc, w & 0x7fff7fffu);
 }
 
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
 // What a row's codes are computed from.
 struct RowQuant {
     float scale; // stored scale (NaN for a row with a non-finite value)
@@ -88,15 +95,22 @@ template <int KV> __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32
         // exact, and a quotient that fp32 can hold -- every tie between two codes is one --
         // comes out exactly; any other quotient is at least 2^-16 of itself
         // away from a tie, since x and top have 8 bits each. Adding 1.5 2^23
-        // rounds to an integer, ties to even, whose low byte is the code.
+        // rounds to an integer, ties to even, whose low byte is the code. Two
+        // values an instruction.
+        const uint64_t mul = pack_f32x2(r.mul, r.mul), up = pack_f32x2(r.up, r.up), nf = pack_f32x2(-r.f, -r.f),
+                       rcp = pack_f32x2(r.rcp, r.rcp), magic = pack_f32x2(12582912.f, 12582912.f);
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float y0 = x[i] * r.mul;
-            const float res = fmaf(-y0, r.f, x[i] * r.up);
-            const float y = fmaf(res, r.rcp, y0);
-            c[i] = __float_as_uint(__fadd_rn(y, 12582912.f));
-        }
+        for (int i = 0; i < 4; i += 2)
+            asm("{\n\t.reg .b64 y, u, z;\n\t"
+                "mul.rn.f32x2 y, %2, %3;\n\t"
+                "mul.rn.f32x2 u, %2, %4;\n\t"
+                "fma.rn.f32x2 u, y, %5, u;\n\t"
+                "fma.rn.f32x2 y, u, %6, y;\n\t"
+                "add.rn.f32x2 z, y, %7;\n\t"
+                "mov.b64 {%0, %1}, z;\n\t}"
+                : "=r"(c[i]), "=r"(c[i + 1])
+                : "l"(pack_f32x2(x[i], x[i + 1])), "l"(mul), "l"(up), "l"(nf), "l"(rcp), "l"(magic));
         return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
 }
