@@ -21,8 +21,8 @@
 //
 // Measured, inputs larger than L2: 131 us for the 128K x 8 rows of a prompt (814 MB,
 // 6.2 TB/s); with 58 registers and four blocks per SM in place of 40 and six 144 us. To
-// int8, whose quotients take five operations a value, 154 us (162 with four blocks); with
-// an operation a value in place of two, and every lane with both rows' divisions, 173.
+// int8, whose quotients take five operations a value, 150 us (162 with four blocks); with
+// an operation a value in place of one for two, and scales by three divisions, 173.
 // Reading 32K x 8 rows back takes 34.1 us (203 MB, 6.0 TB/s); with cached loads 38.0, and
 // with 16 consecutive values a lane, whose stores cover half sectors, 39.7.
 #include <cuda_bf16.h>
@@ -111,22 +111,7 @@ template <int KV> __global__ void __launch_bounds__(kThreads, 6) write_kernel(Kv
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1)
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        RowQuant rq[2];
-        if constexpr (KV == SR_KV_E4M3) {
-            rq[0] = row_quant<KV>(top & 0xffffu);
-            rq[1] = row_quant<KV>(top >> 16);
-        } else { // three divisions: even lanes do the key's, odd ones the value's
-            const RowQuant mine = row_quant<KV>(j & 1 ? top >> 16 : top & 0xffffu);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int from = (lane & 24) + s;
-                rq[s].scale = __shfl_sync(0xffffffffu, mine.scale, from);
-                rq[s].mul = __shfl_sync(0xffffffffu, mine.mul, from);
-                rq[s].up = __shfl_sync(0xffffffffu, mine.up, from);
-                rq[s].f = __shfl_sync(0xffffffffu, mine.f, from);
-                rq[s].rcp = __shfl_sync(0xffffffffu, mine.rcp, from);
-            }
-        }
+        const RowQuant rq[2] = {row_quant<KV>(top & 0xffffu), row_quant<KV>(top >> 16)};
         uint2 codes[2][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s)

@@ -64,11 +64,14 @@ template <int KV> __device__ __forceinline__ RowQuant row_quant(uint32_t top_bit
         r.up = r.f = r.rcp = 0.f;
     } else {
         const float down2 = __uint_as_float((255u - (t >> 23)) << 23); // 2 2^-E, normal for every E
-        r.scale = __fdiv_rn(__uint_as_float(t), 127.f);
+        // top / 127, corrected like a code below; nearest for all 128 significands of
+        // a bf16 top (checked in exact arithmetic, as all codes of all pairs of them)
+        const float top = __uint_as_float(t), s0 = top * (1.f / 127.f);
+        r.scale = fmaf(fmaf(-s0, 127.f, top), 1.f / 127.f, s0);
         r.f = __uint_as_float((t & 0x7fffffu) | 0x3f800000u);
-        r.mul = __fdiv_rn(63.5f, r.f) * down2;
-        r.up = 63.5f * down2;
         r.rcp = __frcp_rn(r.f);
+        r.mul = 63.5f * r.rcp * down2;
+        r.up = 63.5f * down2;
     }
     return r;
 }
