@@ -16,8 +16,9 @@
 //    cut into one contiguous chunk per CTA (rounded to whole tiles, >= 256
 //    positions), so every SM streams the same number of bytes whatever the mix
 //    of unit lengths; 8-bit caches, and bf16 ones on request, shares of the mean
-//    length times the units a CTA where that mean is below 256. A chunk may cover the end of one unit and the start of
-//    the next; each (CTA, unit) overlap is one split.
+//    length times the units a CTA where that mean is below 256. A chunk may cover
+//    the end of one unit and the start of the next; each (CTA, unit) overlap is one
+//    split.
 //  * The producer lane walks its splits tile by tile and issues 3-D TMA loads
 //    (two 128-byte-wide boxes for K, two for V, 128B swizzle) into a ring of
 //    shared-memory stages, each guarded by a full/empty mbarrier pair. A small
@@ -661,7 +662,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     bool early = false;
     if (p.n_splits == 0 && P > 0) {
         // A split costs about 3 us besides its bytes: where the units are short, the
-        // shares hold as few of them as the grid allows, rather than 256 positions.
+        // shares hold as few of them as the grid allows, rather than 256 positions. 240
+        // units of 1 or 2 positions: 303 us with shares of 256, 12 so; 1024 of 125 to 250
+        // (bf16, eight heads): 42.8 and 40.6.
         const long long mean = p.by_unit ? div_nonneg(P + n - 1, n) : kMinChunk;
         if (mean < kMinChunk) {
             chunk = mean * ((n + G - 1) / G);
