@@ -995,7 +995,11 @@ __device__ __forceinline__ void add_parts(const float2 *ml, const float *o, size
             acc[c].x *= keep, acc[c].y *= keep, acc[c].z *= keep, acc[c].w *= keep;
         const unsigned used = __ballot_sync(kFull, w != 0.f); // NaN too
 #pragma unroll 1
-        for (int i0 = 0; i0 < 8 && (used >> i0 & 0x01010101u * ((1u << kJoinBatch) - 1u)); i0 += kJoinBatch) {
+        for (int i0 = 0; i0 < 8; i0 += kJoinBatch) {
+            // A batch that weighs nothing in any of the rows is skipped; the next one
+            // may hold all the weight (its maxima far above this one's).
+            if (!(used >> i0 & 0x01010101u * ((1u << kJoinBatch) - 1u)))
+                continue;
             float4 y[kJoinBatch][4];
             float wi[kJoinBatch];
 #pragma unroll

@@ -314,3 +314,26 @@ def test_generation_behind_a_shared_prefix(kind):
               v0, dec.route_mask.view(B, Hkv).tolist(), out, None)
         if kind == "bf16":
             assert torch.equal(kc[:, :, step].cpu().view(torch.int16), ref[2][:, :, step].view(torch.int16))
+
+
+@pytest.mark.parametrize("B,Hkv,M,Lp", [(1, 1, 8, 40000), (16, 4, 8, 9000), (70, 8, 8, 3000), (3, 32, 1, 577)],
+                         ids=["cta_a_row", "cta_four_rows", "warp_four_rows", "narrow"])
+def test_join_of_parts_that_weigh_nothing_beside_a_later_one(B, Hkv, M, Lp):
+    """Every eighth of the prefix in turn lies some 140 nats above the rest for every
+    head, so that exactly the partials of the other eighths weigh 0 in fp32. A row has
+    160, 74 and 7 or 8 partials in the three forms of the join, which takes them in
+    groups of 256, 64 and 8, half a group at a time."""
+    d = torch.randn(R.D, generator=gen(9), device=DEV)
+    d = d / d.norm()
+    q = (randn((B, Hkv * M, R.D), 1).float() + 40 * d).to(torch.bfloat16)
+    v0, base, v = randn((B, Hkv, R.D), 2), randn((Hkv, Lp, R.D), 3).float(), randn((Hkv, Lp, R.D), 4)
+    mask = torch.zeros(B, Hkv, dtype=torch.uint8, device=DEV)
+    mask[0, 0] = B * Hkv > 1
+    ws = native.PrefixWorkspace(B, Hkv * M, Hkv, Lp)
+    for part in range(8):
+        k = base.clone()
+        k[:, part * Lp // 8:(part + 1) * Lp // 8] += 40 * d
+        k = k.to(torch.bfloat16)
+        lse = torch.zeros(q.shape[:2], device=DEV)
+        out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse, workspace=ws)
+        check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.tolist(), out, lse)  # noqa: B023
