@@ -333,14 +333,12 @@ __device__ __forceinline__ void route_all_units(const Params &p, int U, uint8_t 
     }
 }
 
-// Issues the copies of one tile into a stage, all counted on its full barrier,
-// which must already expect tile_bytes() of them. Returns the scale pair of tile
-// row 0 in the stage's scale buffer.
+// Where the scale pairs of one tile (8-bit caches) come from and go to.
 template <class C> struct TileScales {
-    int32_t sc0 = 0;      // scale pair of row 0 in the buffer
+    int32_t sc0 = 0;      // scale pair of row 0 in the stage's scale buffer
     uint32_t bytes = 0;   // bulk copy
     const float2 *src = nullptr;
-    bool tail = false;    // the pair behind the copy is moved by the issuing lane
+    bool tail = false;    // the pair behind the copy is moved by the producer lane itself
 };
 
 // The scale pairs of rows [pos0, pos0 + BN) of unit u that exist, rounded out to
@@ -365,6 +363,21 @@ template <class C> __device__ __forceinline__ TileScales<C> tile_scales(const Pa
     return r;
 }
 
+// The pair that the bulk copy leaves out, moved by the producer lane. It must precede
+// the lane's arrival on the stage's full barrier, which is what orders a plain store
+// before the consumers' loads: the copies complete the phase by themselves once the
+// lane has arrived. Plain and L2 accesses: the append step may have just written it.
+template <class C> __device__ __forceinline__ void store_tail(uint8_t *smem, int stage, const TileScales<C> &sc)
+{
+    if (C::QUANT && sc.tail) {
+        uint8_t *dst = smem + C::OFF_SCALES + stage * C::SCALES;
+        *reinterpret_cast<float2 *>(dst + sc.bytes) = __ldcg(sc.src + sc.bytes / 8);
+        fence_proxy_async_smem(); // a later tile's bulk copy may cover the place
+    }
+}
+
+// Issues the copies of one tile into a stage, all counted on its full barrier, which
+// must already expect STAGE + sc.bytes of them.
 template <class C>
 __device__ __forceinline__ void issue_tile(const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *smem, int stage,
                                            uint32_t fb, int pos0, int unit, const TileScales<C> &sc, uint64_t pol)
@@ -373,11 +386,8 @@ __device__ __forceinline__ void issue_tile(const CUtensorMap *tmK, const CUtenso
     if constexpr (C::QUANT) {
         tma_load_3d(sb, tmK, fb, 0, pos0, unit, pol);
         tma_load_3d(sb + C::OFF_V, tmV, fb, 0, pos0, unit, pol);
-        uint8_t *dst = smem + C::OFF_SCALES + stage * C::SCALES;
         if (sc.bytes)
-            bulk_load(smem_u32(dst), sc.src, sc.bytes, fb);
-        if (sc.tail)
-            *reinterpret_cast<float2 *>(dst + sc.bytes) = __ldg(sc.src + sc.bytes / 8);
+            bulk_load(smem_u32(smem + C::OFF_SCALES + stage * C::SCALES), sc.src, sc.bytes, fb);
     } else {
         tma_load_3d(sb, tmK, fb, 0, pos0, unit, pol);
         tma_load_3d(sb + C::HALF, tmK, fb, 64, pos0, unit, pol);
@@ -705,6 +715,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 const TileScales<C> sc = tile_scales<C>(p, fu, pos0);
                 mbar_expect_tx(full0, (uint32_t)C::STAGE + (uint32_t)(M * kHeadDim * 2) + sc.bytes);
                 issue_tile<C>(&tmK, &tmV, smem, 0, full0, pos0, fu, sc, pol0);
+                store_tail<C>(smem, 0, sc); // its arrival follows with the header
                 const uint8_t *qsrc = reinterpret_cast<const uint8_t *>(p.q + (size_t)fq * kHeadDim);
                 for (int hq = 0; hq < M; ++hq)
                     bulk_load(smem_u32(smem + C::OFF_Q + hq * kQRowBytes), qsrc + hq * kHeadDim * 2, kHeadDim * 2,
@@ -803,6 +814,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             }
             const uint32_t bytes = (h.nvalid > 0 ? (uint32_t)C::STAGE + sc.bytes : 0u) + qbytes;
             if (bytes) {
+                store_tail<C>(smem, stage, sc);
                 mbar_arrive_expect_tx(fb, bytes);
                 if (h.nvalid > 0) {
 #ifdef SR_TIMELINE

@@ -723,3 +723,33 @@ def test_scan_of_units_that_are_one_split_each():
             out, lse, o = scan(q, c, v0, lens, mask, ns)
             check_scan(q, c, v0, lens, mask.tolist(), out, lse, o)
             assert torch.equal(out, o.to(torch.bfloat16))
+
+
+@both
+@pytest.mark.parametrize("B,Hkv,M,Lmax,ns", [
+    (33, 1, 4, 67, 0),     # more than 32 units
+    (1, 1, 4, 40193, 0),   # the last share ends with a tile of one row
+    (1, 1, 8, 1001, 3),    # forced splits of two tiles
+    (1, 5, 4, 4099, 1),    # one split of 17 tiles
+    (3, 11, 1, 513, 5),    # 33 units, forced splits
+    (1, 3, 2, 257, 1),     # the last pair alone in the last tile
+])
+def test_scan_reads_the_last_pair_of_an_odd_count(B, Hkv, M, Lmax, ns, dtype):
+    """An odd number of scale pairs leaves the last one without a neighbour for the
+    16-byte copy. All sequences full, the last unit active, the last position of every
+    unit aligned with its queries and its value scale eight times the others'; several
+    times over, with other values in between."""
+    assert B * Hkv * Lmax % 2 == 1
+    lens = [Lmax] * B
+    v0 = torch.randn(B, Hkv, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    mask = torch.zeros(B, Hkv, dtype=torch.bool, device=DEV)
+    mask[0, 0] = True
+    for seed in (11, 12, 13):
+        c = filled_cache(B, Hkv, Lmax, lens, dtype, seed)
+        q = torch.randn(B, Hkv, M, R.D, generator=gen(seed + 7), device=DEV)
+        last = c.k[:, :, -1].float() * c.scales[:, :, -1, :1]
+        q = (0.3 * q + 2.0 * last[:, :, None] / last[:, :, None].norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+        c.scales[:, :, -1, 0] *= 4.0
+        c.scales[:, :, -1, 1] *= 8.0
+        out, lse, o = scan(q.reshape(B, Hkv * M, R.D), c, v0, lens, mask, ns)
+        check_scan(q.reshape(B, Hkv * M, R.D), c, v0, lens, mask.tolist(), out, lse, o)
