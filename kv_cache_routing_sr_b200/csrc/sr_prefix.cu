@@ -354,7 +354,7 @@ __device__ __forceinline__ uint32_t scan_prologue(Shared *sh, const CUtensorMap 
             mbar_init(smem_u32(&sh->empty[s]), 1);
         }
         mbar_init(smem_u32(&sh->q_full), kSoftmaxWarps);
-        mbar_init(smem_u32(&sh->seg_done), kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->seg_done), kSoftmaxWarps + (TILE == 64 ? 2 : 0)); // narrow: and its MMA warps
         for (int s = 0; s < 2; ++s) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&sh->s_full[s][i]), 1);
@@ -681,10 +681,18 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     if (t + 2 < steps)
                         ok = logits(t + 2);
                 }
+                if (!ok)
+                    break;
                 used += 2 * (uint32_t)steps;
                 done0 += (steps + 1) / 2;
                 done1 += steps / 2;
                 ++nseg;
+                // A segment of one tile gives the second stream's warp no step, and nobody
+                // else waits for it: without its arrival q_full could complete twice
+                // before the warp has seen it once.
+                if (lane == 0)
+                    mbar_arrive(seg_done);
+                __syncwarp();
             }
             if (!ok)
                 drain_mmas(smem_u32(&sh->drain[s]));
@@ -761,7 +769,8 @@ scan_narrow_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 __stcg(p.ml + part + prow, make_float2(m * kScaleLog2, l));
             done0 += (steps + 1) / 2;
             done1 += steps / 2;
-            // Both groups are done with the segment's Q, S and O.
+            // Both groups are done with the segment's Q, S and O, and both MMA warps have
+            // issued all of it.
             arrive_warp(seg_done, lane);
             if (!wait_warp(seg_done, nseg & 1, abort_flag)) {
                 ok = false;

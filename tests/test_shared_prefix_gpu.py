@@ -337,3 +337,19 @@ def test_join_of_parts_that_weigh_nothing_beside_a_later_one(B, Hkv, M, Lp):
         lse = torch.zeros(q.shape[:2], device=DEV)
         out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse, workspace=ws)
         check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.tolist(), out, lse)  # noqa: B023
+
+
+@pytest.mark.parametrize("B,Hkv,M,Lp", [(2, 700, 1, 40), (16, 800, 8, 64), (1, 2000, 1, 1), (3, 300, 2, 129)],
+                         ids=["B2", "B16", "one_position", "three_tiles"])
+def test_items_of_one_tile(B, Hkv, M, Lp):
+    """Many items a CTA of one 64-position tile each: the second stream has no step in
+    them. Back to back calls keep their bits."""
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    mask = (torch.rand(B, Hkv, generator=gen(5), device=DEV) < 0.2).to(torch.uint8)
+    ws = native.PrefixWorkspace(B, Hkv * M, Hkv, Lp)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    outs = [native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse, workspace=ws) for _ in range(50)]
+    assert ws.device_error() == 0
+    check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.tolist(), outs[0], lse)
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
