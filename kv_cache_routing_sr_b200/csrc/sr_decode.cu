@@ -1342,7 +1342,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 break;
             // Partial of the split, one float4 column per thread: the warps'
             // states weighted by 2^(m_w - max_w m_w) (0 for a warp that saw no
-            // row of this split).
+            // row of this split: l_w = 0. A NaN logit leaves the maximum as it is
+            // and makes l NaN: a warp, or a split, of nothing but NaN rows has m =
+            // -inf and l = NaN, and its NaN reaches the result).
             // A split that is its whole unit needs no partial: its state is the
             // merge's result, bit for bit (the only weight is 2^0).
             float *po = p.part_o + (size_t)h.slot * M * kHeadDim;
@@ -1360,7 +1362,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 float Lh = 0.f;
 #pragma unroll
                 for (int ww = 0; ww < kCWarps; ++ww) {
-                    const float f = (ml[ww].x == -INFINITY) ? 0.f : exp2f(ml[ww].x - Mh);
+                    const float f = (ml[ww].y == 0.f) ? 0.f : exp2f(ml[ww].x - Mh);
                     const float4 x =
                         *reinterpret_cast<const float4 *>(comb + ww * (kMaxGroup * kCombStride) + head * kCombStride + d4);
                     acc.x = fmaf(x.x, f, acc.x);
@@ -1444,26 +1446,25 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
                         for (int off = 16; off > 0; off >>= 1)
                             mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, off));
+                        // Weights of 0 for what has no maximum yet; NaN sums stay NaN.
                         const float mn = fmaxf(m, mb);
-                        if (mn != -INFINITY) {
-                            const float a = exp2f(m - mn);
-                            const float cw = (xl.x == -INFINITY) ? 0.f : exp2f(xl.x - mn);
-                            float ls = xl.y * cw;
+                        const float a = (m == -INFINITY) ? 0.f : exp2f(m - mn);
+                        const float cw = (xl.x == -INFINITY) ? 0.f : exp2f(xl.x - mn);
+                        float ls = xl.y * cw;
 #pragma unroll
-                            for (int off = 16; off > 0; off >>= 1)
-                                ls += __shfl_xor_sync(kFull, ls, off);
-                            l = l * a + ls;
-                            acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+                        for (int off = 16; off > 0; off >>= 1)
+                            ls += __shfl_xor_sync(kFull, ls, off);
+                        l = l * a + ls;
+                        acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
 #pragma unroll
-                            for (int k = 0; k < kMergeBatch; ++k) {
-                                const float c = __shfl_sync(kFull, cw, k);
-                                acc.x += y[k].x * c;
-                                acc.y += y[k].y * c;
-                                acc.z += y[k].z * c;
-                                acc.w += y[k].w * c;
-                            }
-                            m = mn;
+                        for (int k = 0; k < kMergeBatch; ++k) {
+                            const float c = __shfl_sync(kFull, cw, k);
+                            acc.x += y[k].x * c;
+                            acc.y += y[k].y * c;
+                            acc.z += y[k].z * c;
+                            acc.w += y[k].w * c;
                         }
+                        m = mn;
                     }
                     if (sgrp == 1) {
                         if (p.lse && d4 == 0)
@@ -1487,7 +1488,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         for (int q = 0; q < sgrp; ++q) {
                             const int e = q * cpg + ctid;
                             const float2 ml = *reinterpret_cast<const float2 *>(comb + 4 * kMergeThreads + 2 * e);
-                            if (ml.x == -INFINITY)
+                            if (ml.y == 0.f) // no partial of its own
                                 continue;
                             const float c = exp2f(ml.x - m);
                             const float4 y = *reinterpret_cast<const float4 *>(comb + 4 * e);

@@ -753,3 +753,36 @@ def test_scan_reads_the_last_pair_of_an_odd_count(B, Hkv, M, Lmax, ns, dtype):
         c.scales[:, :, -1, 1] *= 8.0
         out, lse, o = scan(q.reshape(B, Hkv * M, R.D), c, v0, lens, mask, ns)
         check_scan(q.reshape(B, Hkv * M, R.D), c, v0, lens, mask.tolist(), out, lse, o)
+
+
+@pytest.mark.parametrize("kind", ["bf16", *R.IDS])
+@pytest.mark.parametrize("M", [1, 4, 8])
+@pytest.mark.parametrize("L,bad,ns", [
+    (33, range(32, 33), 0), (65, range(64, 65), 0), (129, range(128, 129), 0),  # a warp's only row
+    (300, range(0, 128), 0),             # all rows of a warp, or of several
+    (4, range(3, 4), 4), (4, range(0, 1), 4),         # a split's only row
+    (64, range(0, 25), 64), (64, range(30, 64), 64),  # a whole batch of the merge
+    (5000, range(4992, 5000), 0),        # the end of the last share
+    (1, range(0, 1), 0), (70, range(0, 70), 7),       # nothing but NaN
+], ids=lambda x: f"{x.start}to{x.stop}" if isinstance(x, range) else str(x))
+def test_nan_keys_reach_the_result_whatever_shares_their_rows(L, bad, ns, M, kind):
+    """NaN logits leave the running maximum as it is, so a warp or a split that holds
+    nothing else has a maximum of -inf: its NaN must not be taken for a part without
+    rows. The other unit of the launch stays finite."""
+    q = torch.randn(1, 2 * M, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.randn(1, 2, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    sl = torch.tensor([L], dtype=torch.int32, device=DEV)
+    active = torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV)
+    lse = torch.zeros(1, 2 * M, device=DEV)
+    if kind == "bf16":
+        k, v = (torch.randn(1, 2, L, R.D, generator=gen(i), device=DEV).to(torch.bfloat16) for i in (3, 4))
+        k[0, 1, bad.start:bad.stop, 17] = math.nan
+        out = native.decode_attention(q, k, v, None, v0, sl, active, n_splits=ns, lse=lse)
+        o, z = native.decode_attention_partial(q, k, v, None, v0, sl, active, n_splits=ns)
+    else:
+        c = filled_cache(1, 2, L, [L], R.DTYPES[R.IDS.index(kind)], 3)
+        c.scales[0, 1, bad.start:bad.stop, 0] = math.nan
+        out = native.decode_attention_quant(q, c.k, c.v, c.scales, v0, sl, active, n_splits=ns, lse=lse)
+        o, z = native.decode_attention_quant_partial(q, c.k, c.v, c.scales, v0, sl, active, n_splits=ns)
+    for t in (out, o, lse, z):
+        assert torch.isfinite(t[0, :M]).all() and torch.isnan(t[0, M:]).all()
