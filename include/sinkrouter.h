@@ -376,9 +376,10 @@ typedef enum sr_kv_type {
  *   int8: scale = top / 127 rounded to fp32,
  *         code_i = 127 x_i / top rounded to an integer (nearest, ties to even)
  * A row with an infinity or a NaN gets codes 0 and scale NaN, so that it reads
- * back as NaN. Readers take any finite scale, not only the writer's. The
- * position-0 key and value k0 / v0 stay bf16: routing and the sink bypass work
- * on the unquantised rows.
+ * back as NaN. Readers take finite scales of other writers too, as long as what
+ * they make is in fp32's range: code * scale, and a key row's scale times the
+ * query's largest magnitude. The position-0 key and value k0 / v0 stay bf16:
+ * routing and the sink bypass work on the unquantised rows.
  */
 
 /* Strides, in elements, of a bf16 tensor [B, T, Hkv, d] whose last dimension is
@@ -463,7 +464,10 @@ sr_status sr_rope_append_route_kv(const sr_dims *dims, int32_t kv_type, int32_t 
  * served from v0 as there. fp32 logits, softmax statistics and sums; the query
  * and the softmax weights (times the value rows' scales) enter the products in
  * fp16, scaled by powers of two (query: exact to 2^-24 of the row's largest
- * magnitude; weights: relative 2^-11).
+ * magnitude; weights: relative 2^-11, as long as weight * scale is at least 2^-28 of
+ * the largest value scale that a warp has met in its part of the unit; below 2^-39 of
+ * it a row may count as 0, whatever its weight. Rows of one unit whose value scales lie
+ * more than 2^28 apart therefore do not belong into one 8-bit cache).
  *
  *   kv_type     SR_KV_E4M3 or SR_KV_INT8
  *   k_cache, v_cache, kv_scales   as above, 16-byte aligned; codes and scales of

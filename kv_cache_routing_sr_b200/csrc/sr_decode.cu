@@ -53,8 +53,11 @@
 //    16-column chunk and row r + 8 column 2 r + 1.
 //  * The key rows' scales multiply the fp32 logits; the value rows' scales
 //    multiply the softmax weights before these are rounded to fp16 (relative
-//    2^-11), relative to the largest value scale that the warp has met in the
-//    split, times 2^14: the full range of fp16 is below a row that matters. The
+//    2^-11), relative to the power of two at or below the largest value scale that
+//    the warp has met in the split, times 2^14. A weight times its scale that lies
+//    2^-28 below that power loses bits, 2^-39 below it is 0, however much of the
+//    softmax the row holds: value scales of one unit within a factor of 2^28 of one
+//    another, as activations have them, are never near that. The
 //    query enters in fp16 times a power of two that puts its largest element in
 //    [2^13, 2^14).
 #include <climits>
@@ -1017,8 +1020,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     mrun[0] = mrun[1] = -INFINITY;
     lrun[0] = lrun[1] = 0.f;
     // 8-bit caches: logit factor of heads 2t and 2t + 1 (the query's power of two
-    // taken back, and log2(e) / sqrt(d)); the largest value scale met in the
-    // split, in whose units times 2^-14 O accumulates
+    // taken back, and log2(e) / sqrt(d)); the power of two at or below the largest
+    // value scale met in the split, in whose units times 2^-14 O accumulates
     float cq0 = 0.f, cq1 = 0.f, vref = kMinValueScale;
 
     int stage = 0;
@@ -1221,13 +1224,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     vm = fmaxf(vm, __shfl_xor_sync(kFull, vm, off));
-                const float inv = __fdividef(1.f, vm);
-                grow = vref * inv;
-                vref = vm;
+                // the reference is vm's power of two, so that every scale of fp32 has an
+                // exact factor and nothing is divided: weights are below 2^15
+                const int e = (int)(__float_as_uint(vm) >> 23) - 127;
+                const float mul = exp2_int(14 - e), ref = exp2_int(e);
+                grow = vref * mul * 6.103515625e-05f; // 2^-14
+                vref = ref;
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) {
-                    wv[rb][0] = rsc[rb][0].y * inv * 16384.f;
-                    wv[rb][1] = rsc[rb][1].y * inv * 16384.f;
+                    wv[rb][0] = rsc[rb][0].y * mul;
+                    wv[rb][1] = rsc[rb][1].y * mul;
                 }
             }
             float ps0 = 0.f, ps1 = 0.f;

@@ -786,3 +786,26 @@ def test_nan_keys_reach_the_result_whatever_shares_their_rows(L, bad, ns, M, kin
         o, z = native.decode_attention_quant_partial(q, c.k, c.v, c.scales, v0, sl, active, n_splits=ns)
     for t in (out, o, lse, z):
         assert torch.isfinite(t[0, :M]).all() and torch.isnan(t[0, M:]).all()
+
+
+@both
+@pytest.mark.parametrize("exp", [-120.0, 60.0, 125.9, 126.2, 127.0, 127.9])
+def test_scan_takes_value_scales_to_the_end_of_fp32(exp, dtype):
+    """Codes of -1, 0 and 1 under scales up to nearly 2^128: one position with the
+    largest scale holds nearly all the weight (so that no sum passes fp32's end), the
+    others' scales are 2^9 below it."""
+    n = 200
+    c = filled_cache(1, 2, n, [n], dtype, 3)
+    q = torch.randn(1, 8, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.zeros(1, 2, R.D, device=DEV, dtype=torch.bfloat16)
+    c.v.copy_(torch.randint(-1, 2, c.v.shape, generator=gen(3), device=DEV).float().to(dtype))
+    c.scales[..., 1] = 2.0 ** (exp - 9)
+    key = c.k[0, :, 77].float() * c.scales[0, :, 77, :1]
+    q = (q.view(2, 4, R.D).float() * 0.1 + 4 * key[:, None] / key[:, None].norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    c.scales[0, :, 77, 0] *= 40.0
+    c.scales[0, :, 77, 1] = 2.0 ** exp
+    mask = torch.zeros(1, 2, dtype=torch.bool, device=DEV)
+    out, lse, o = scan(q.reshape(1, 8, R.D), c, v0, [n], mask)
+    check_scan(q.reshape(1, 8, R.D), c, v0, [n], mask.tolist(), out, lse, o)
+    big = float(out.double().abs().max())
+    assert 2.0 ** (exp - 0.1) < big <= 2.0 ** (exp + 0.01)
