@@ -194,7 +194,7 @@ cudaError_t launch_rows(void (*kernel)(Args, long long, int), const Args &a, int
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    const int nblk = (rows + kRowsPerWarp - 1) / kRowsPerWarp;
+    const int nblk = rows / kRowsPerWarp + (rows % kRowsPerWarp != 0); // rows may be INT_MAX
     const long long items = (long long)a.batch * a.n_kv_heads * nblk;
     const long long want = (items + kWarps - 1) / kWarps, cap = (long long)blocks_per_sm * sms;
     cudaLaunchConfig_t cfg = {};

@@ -809,3 +809,19 @@ def test_scan_takes_value_scales_to_the_end_of_fp32(exp, dtype):
     check_scan(q.reshape(1, 8, R.D), c, v0, [n], mask.tolist(), out, lse, o)
     big = float(out.double().abs().max())
     assert 2.0 ** (exp - 0.1) < big <= 2.0 ** (exp + 0.01)
+
+
+@both
+def test_append_quant_takes_the_largest_token_count(dtype):
+    """T = 2^31 - 1 (a view of one token repeated): the blocks of four tokens round it
+    up past 2^31."""
+    c = sentinel_cache(1, 2, 8, dtype)
+    x = rows((1, 1, 2, R.D), 3)
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    many = x.expand(1, 2 ** 31 - 1, 2, R.D)
+    native.kv_append_quant(many, many, z + 1, z + 3, c.k, c.v, c.scales, device_error=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    assert_rows(c.k[0, :, 1:4], c.scales[0, :, 1:4, 0], x[0, 0, :, None].expand(2, 3, R.D), dtype, "rows")
+    assert (c.scales[0, :, [0, 4, 5, 6, 7]] == -7.0).all()
