@@ -4,20 +4,23 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
 #include <cstring>
 #include <cuda_runtime.h>
-#include <string>
 
 #include "sinkrouter.h"
 #include "sr_internal.h"
 
 namespace {
 
-thread_local std::string g_last_cuda_error;
+thread_local char g_last_cuda_error[256]; // no allocation: nothing to throw at a C entry
 
+// Keeps the message and clears the runtime's own record of the error, which the next
+// call's check of its launch would report as that launch's.
 sr_status cuda_fail(cudaError_t e)
 {
-    g_last_cuda_error = std::string(cudaGetErrorName(e)) + ": " + cudaGetErrorString(e);
+    std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
+    (void)cudaGetLastError();
     return SR_ERR_CUDA;
 }
 
@@ -81,7 +84,7 @@ const char *sr_status_string(sr_status s)
     return "unknown sr_status";
 }
 
-const char *sr_last_cuda_error(void) { return g_last_cuda_error.c_str(); }
+const char *sr_last_cuda_error(void) { return g_last_cuda_error; }
 
 sr_status sr_route(const sr_dims *dims, const void *q, const void *k0, float tau, uint8_t *route_mask,
                    int32_t *active_list, void *stream)

@@ -1629,8 +1629,10 @@ cudaError_t device_info(DeviceInfo **out)
 int decode_grid_size()
 {
     DeviceInfo *info = nullptr;
-    if (device_info(&info) != cudaSuccess)
+    if (device_info(&info) != cudaSuccess) {
+        (void)cudaGetLastError(); // not the next call's
         return 0;
+    }
     return info->grid;
 }
 

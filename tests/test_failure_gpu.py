@@ -4,6 +4,10 @@ SR_DEVERR_TIMEOUT after about its bound, and the context stays usable (a decode
 step afterwards still matches the oracle)."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -28,3 +32,36 @@ def test_context_usable_after_a_timeout():
     ref = H.oracle_full(x, x.tau)
     H.assert_route_equal(mask_g, act_g, ref.mask, ref.active_list)
     H.check_against_oracle(x, out_g, mask_g, what="after a bounded-wait timeout")
+
+
+AFTER_AN_ERROR = """
+import torch
+from kv_cache_routing_sr_b200 import native
+q = torch.randn(1, 32, 128, device="cuda").to(torch.bfloat16)
+k0 = torch.randn(1, 8, 128, device="cuda").to(torch.bfloat16)
+ws = native.Workspace(1, 32, 8, 64)
+want, _ = native.route(q, k0, 0.6)
+torch.cuda.synchronize()
+seen = None
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        try:
+            ws.device_error()  # synchronises, which a capturing stream refuses
+        except native.SinkRouterError as e:
+            seen = e.status
+except RuntimeError:
+    pass  # the capture is void
+assert seen == native.SR_ERR_CUDA
+got, _ = native.route(q, k0, 0.6)
+assert torch.equal(got, want)
+assert b"capturing" in native.load().sr_last_cuda_error()
+print("usable")
+"""
+
+
+def test_a_failed_call_is_not_reported_by_the_next_one():
+    """A CUDA error that a call has returned is cleared: the next call succeeds. In a
+    process of its own, since the voided capture is torch's affair too."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", AFTER_AN_ERROR], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "usable" in r.stdout, r.stderr[-2000:]
