@@ -42,6 +42,21 @@ def _run(cmd) -> str:
     return r.stdout + r.stderr
 
 
+def _binding_mark() -> bytes:
+    """What a binding compiled against the installed torch contains."""
+    import torch
+    return f"sr_binding for torch {torch.__version__};".encode()
+
+
+def binding_current(path: str = BINDING) -> bool:
+    """Whether the Python binding is there and was compiled against the installed torch
+    (its C++ interface is fixed within one version only)."""
+    if not os.path.exists(path):
+        return False
+    with open(path, "rb") as f:
+        return _binding_mark() in f.read()
+
+
 def build_binding(output: str = BINDING) -> str:
     """Compile the Python binding against the installed torch and return its path."""
     import torch
@@ -49,9 +64,10 @@ def build_binding(output: str = BINDING) -> str:
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
     lib = os.path.join(root, "lib")
-    tmp = output + ".tmp"
+    tmp = f"{output}.{os.getpid()}.tmp"
     _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc],
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f'-DSR_BINDING_MARK="{_binding_mark().decode()}"', *[f"-I{i}" for i in inc],
           os.path.join(CSRC, "sr_binding.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
           "-ltorch_python", f"-Wl,-rpath,{lib}"])
     os.replace(tmp, output)
@@ -66,7 +82,7 @@ def build(output: str = LIBRARY, defines=(), verbose_ptxas: bool = False, quiet:
     if verbose_ptxas:
         flags += ["-Xptxas", "-v"]
 
-    tmp = output + ".tmp"
+    tmp = f"{output}.{os.getpid()}.tmp"
     with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(len(SOURCES) + 1) as pool:
         binding = pool.submit(build_binding) if os.path.abspath(output) == os.path.abspath(LIBRARY) else None
         objs = [os.path.join(objects, s + ".o") for s in SOURCES]  # one compiler a source, side by side
@@ -81,7 +97,7 @@ def build(output: str = LIBRARY, defines=(), verbose_ptxas: bool = False, quiet:
 
 
 def needs_build(output: str = LIBRARY) -> bool:
-    if not os.path.exists(output) or not os.path.exists(BINDING):
+    if not os.path.exists(output) or not binding_current():
         return True
     newest = max(os.path.getmtime(os.path.join(CSRC, f)) for f in os.listdir(CSRC))
     newest = max(newest, os.path.getmtime(os.path.join(INCLUDE, "sinkrouter.h")))

@@ -408,7 +408,9 @@ PyMethodDef g_methods[] = {
     {"prefix", fast(&guarded<prefix, 14>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_sr_binding", nullptr, -1, g_methods};
+// The docstring names the torch that this was compiled against: the build looks for it
+// in the file before Python loads it into another.
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_sr_binding", SR_BINDING_MARK, -1, g_methods};
 
 } // namespace
 

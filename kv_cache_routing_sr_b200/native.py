@@ -46,7 +46,7 @@ class SinkRouterError(RuntimeError):
 
 
 _lib = None
-_bound = None  # the compiled binding, once the library is loaded
+_bound = None  # the compiled binding, once an entry point has needed it
 # entry points that the compiled binding calls, in its order
 _BOUND = ["sr_kv_append_quant", "sr_kv_dequant", "sr_rope_append_route_kv", "sr_decode_attention_quant",
           "sr_decode_attention_quant_partial", "sr_prefix_attention", "sr_prefix_attention_partial"]
@@ -66,14 +66,14 @@ def load(path: str | None = None):
     SINKROUTER_LIBRARY environment variable (another build of the same
     sources), else the in-tree library, which is compiled first if it is
     absent (nvcc, sm_100a). Any other missing path, or a failed compile,
-    raises: there is no other implementation to fall back to."""
-    global _lib, _bound
+    raises: there is no other implementation to fall back to. The compiled
+    binding is not needed for it; the entry points that use that load it."""
+    global _lib
     if _lib is not None:
         return _lib
     if path is None:
         path = os.environ.get("SINKROUTER_LIBRARY") or LIBRARY
-    if not os.path.exists(_build.BINDING) or (not os.path.exists(path) and
-                                              os.path.abspath(path) == os.path.abspath(LIBRARY)):
+    if not os.path.exists(path) and os.path.abspath(path) == os.path.abspath(LIBRARY):
         try:
             _build.build()
         except Exception as e:
@@ -138,11 +138,25 @@ def load(path: str | None = None):
     lib.sr_prefix_attention.restype = ctypes.c_int
     lib.sr_prefix_attention_partial.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
     lib.sr_prefix_attention_partial.restype = ctypes.c_int
-    from . import _sr_binding
-    _sr_binding.use(*(ctypes.cast(getattr(lib, n), vp).value for n in _BOUND))
-    _bound = _sr_binding
     _lib = lib
     return lib
+
+
+def _bind():
+    """Load (once) the compiled binding on top of the library. It is compiled first
+    (g++) where it is absent or belongs to another torch."""
+    global _bound
+    lib = load()
+    if not _build.binding_current(_build.BINDING):
+        try:
+            _build.build_binding(_build.BINDING)
+        except Exception as e:
+            raise RuntimeError("_sr_binding.so is missing, or was compiled against another torch, and compiling it "
+                               f"failed: {e}") from e
+    from . import _sr_binding
+    _sr_binding.use(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND))
+    _bound = _sr_binding
+    return _bound
 
 
 def _on_tensor_device(fn):
@@ -191,9 +205,7 @@ def _handle(stream) -> int | None:
 
 
 def _loaded():
-    if _bound is None:
-        load()
-    return _bound
+    return _bound if _bound is not None else _bind()
 
 
 def dims_of(batch: int, n_q_heads: int, n_kv_heads: int, max_seq_len: int, head_dim: int = HEAD_DIM) -> Dims:

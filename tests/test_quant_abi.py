@@ -143,3 +143,46 @@ def test_binding_refuses_cpu_tensors_and_wrong_kinds(lib):
 
 class _FakeWorkspace:
     ptr, nbytes = FAKE, 1 << 30
+
+
+@pytest.fixture
+def unloaded(monkeypatch):
+    """native as in a process that has loaded nothing yet; what would be compiled."""
+    made = []
+    monkeypatch.setattr(native, "_lib", None)
+    monkeypatch.setattr(native, "_bound", None)
+    monkeypatch.setattr(build, "build", lambda *a, **k: made.append("library"))
+    monkeypatch.setattr(build, "build_binding", lambda *a, **k: made.append("binding"))
+    return made
+
+
+def test_the_library_loads_without_the_binding(lib, unloaded, monkeypatch, tmp_path):
+    """The entry points that ctypes serves need no binding, no compiler and no headers."""
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_sr_binding.so"))
+    monkeypatch.setenv("SINKROUTER_LIBRARY", build.LIBRARY)
+    assert native.load().sr_status_string(0) == b"SR_OK" and unloaded == []
+    assert native.workspace_bytes(1, 32, 8, 4096) > 0 and unloaded == []
+
+
+def test_only_the_binding_is_compiled_where_only_it_is_missing(lib, unloaded, monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_sr_binding.so"))
+    native._loaded()
+    assert unloaded == ["binding"]
+    native._loaded()
+    assert unloaded == ["binding"]
+
+
+def test_a_failed_compile_of_the_binding_says_so(lib, unloaded, monkeypatch, tmp_path):
+    def fails(*a):
+        raise RuntimeError("no g++")
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_sr_binding.so"))
+    monkeypatch.setattr(build, "build_binding", fails)
+    with pytest.raises(RuntimeError, match="_sr_binding.so.*no g"):
+        native.kv_dequant(*[None] * 7)
+    assert native.load() is not None  # the rest still works
+
+
+def test_a_binding_of_another_torch_is_noticed(lib, unloaded, monkeypatch):
+    assert build.binding_current() and not build.needs_build()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    assert not build.binding_current() and build.needs_build()
