@@ -613,13 +613,37 @@ class Decoder:
         return self.out
 
 
+def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device):
+    """The argument checks of a decoder's step, before it launches anything: its own
+    buffers have the decoder's shape, whatever the tensors' is."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on {device}, got {t.dtype} of "
+                         f"{tuple(t.shape)} on {t.device}")
+    if dtype != torch.int32 and t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _expect_splits(shape, n_splits: int, lowest: int, workspace: Workspace):
+    if n_splits < lowest or n_splits > SR_MAX_SPLITS:
+        raise ValueError(f"n_splits must be in [{lowest}, {SR_MAX_SPLITS}], got {n_splits}")
+    if n_splits > 0 and workspace_bytes(*shape, n_splits) > workspace.nbytes:
+        raise SinkRouterError("n_splits above the decoder's max_splits", SR_ERR_WORKSPACE, load())
+
+
 class QuantDecoder(Decoder):
     """A Decoder over an 8-bit cache: step() = sr_route then
     sr_decode_attention_quant, append_step() = sr_rope_append_route_kv then
     sr_decode_attention_quant. The cache (a QuantCache, or tensors like its
     parts) is the caller's; k0 and v0 stay bf16."""
 
+    def _check(self, q, k0, n_splits):
+        B, Hq, Hkv, _ = self.shape
+        _expect(q, "q", torch.bfloat16, (B, Hq, HEAD_DIM), self.out.device)
+        _expect(k0, "k0", torch.bfloat16, (B, Hkv, HEAD_DIM), self.out.device)
+        _expect_splits(self.shape, n_splits, 0, self.workspace)
+
     def step(self, q, cache: QuantCache, k0, v0, seq_lens, tau, n_splits: int = 0, stream=None):
+        self._check(q, k0, n_splits)
         route(q, k0, tau, self.route_mask, self.active_list, stream)
         return decode_attention_quant(q, cache.k, cache.v, cache.scales, v0, seq_lens, self.active_list, self.out,
                                       n_splits, self.workspace, stream)
@@ -628,7 +652,8 @@ class QuantDecoder(Decoder):
                     n_splits: int = 0, device_error=None, stream=None):
         """A whole decode step from the un-rotated projections; the cache, k0 / v0
         and seq_lens are updated in place, the rotated query is kept in self.q."""
-        if getattr(self, "q", None) is None or self.q.shape != q_in.shape:
+        self._check(q_in, k0, n_splits)
+        if getattr(self, "q", None) is None:
             self.q = torch.empty_like(q_in)
         rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, cache.k, cache.v, cache.scales, k0, v0,
                              tau, q_out=self.q, route_mask=self.route_mask, active_list=self.active_list,

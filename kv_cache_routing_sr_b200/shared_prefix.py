@@ -45,14 +45,35 @@ class SharedPrefixDecoder:
     def active_list(self):
         return self.suffix.active_list
 
+    def _check(self, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, kv_scales, n_splits):
+        """Everything that a launch of the step would refuse or read past, before the
+        first one: an appended token is not taken back."""
+        s, bf16 = self.suffix, torch.bfloat16
+        B, Hq, Hkv, _ = s.shape
+        device, rows = s.out.device, (B, Hkv, native.HEAD_DIM)
+        native._expect(q, "q", bf16, (B, Hq, native.HEAD_DIM), device)
+        native._expect(k0, "k0", bf16, rows, device)
+        native._expect(v0, "v0", bf16, rows, device)
+        prefix = (Hkv, *k_prefix.shape[1:2], native.HEAD_DIM)
+        native._expect(k_prefix, "k_prefix", bf16, prefix, device)
+        native._expect(v_prefix, "v_prefix", bf16, prefix, device)
+        if prefix[1] < 1 or not 0 <= prefix_len <= prefix[1]:
+            raise ValueError(f"prefix_len must be in [0, {prefix[1]}] of at least one position, got {prefix_len}")
+        cache = (B, Hkv, *k_cache.shape[2:3], native.HEAD_DIM)
+        native._expect(k_cache, "k_cache", bf16 if kv_scales is None else k_cache.dtype, cache, device)
+        native._expect(v_cache, "v_cache", k_cache.dtype, cache, device)
+        native._expect(seq_lens, "seq_lens", torch.int32, (B,), device)
+        native._expect_splits(s.shape, n_splits, native.SPLITS_BY_UNIT, s.workspace)
+
     def _attend(self, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, v0, seq_lens, kv_scales, n_splits, stream):
         s = self.suffix
         if kv_scales is None:
             native.decode_attention_partial(q, k_cache, v_cache, None, v0, seq_lens, s.active_list, self.o_suffix,
                                             self.lse_suffix, n_splits or native.SPLITS_BY_UNIT, s.workspace, stream)
         else:
+            # 0 cuts an 8-bit cache by unit
             native.decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens, s.active_list,
-                                                  self.o_suffix, self.lse_suffix, n_splits, s.workspace, stream)
+                                                  self.o_suffix, self.lse_suffix, max(n_splits, 0), s.workspace, stream)
         return native.prefix_attention(q, k_prefix, v_prefix, prefix_len, v0, s.route_mask, s.out, None, self.o_suffix,
                                        self.lse_suffix, self.workspace, stream)
 
@@ -61,6 +82,7 @@ class SharedPrefixDecoder:
         """One step on rotated queries; seq_lens [B] are the suffixes' lengths (>= 1).
         kv_scales: the scales of an 8-bit suffix cache, None for bf16. Returns out
         bf16 [B, Hq, 128]."""
+        self._check(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, kv_scales, n_splits)
         native.route(q, k0, tau, self.route_mask, self.active_list, stream)
         return self._attend(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, v0, seq_lens, kv_scales, n_splits,
                             stream)
@@ -72,7 +94,8 @@ class SharedPrefixDecoder:
         sequence's suffix at position prefix_len + seq_lens[b], then the attention.
         The suffix caches and seq_lens are updated in place; the rotated query is
         kept in self.q."""
-        if getattr(self, "q", None) is None or self.q.shape != q_in.shape:
+        self._check(q_in, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, kv_scales, n_splits)
+        if getattr(self, "q", None) is None:
             self.q = torch.empty_like(q_in)
         native.rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache, v_cache, kv_scales, k0,
                                     v0, tau, pos_offset=prefix_len, q_out=self.q, route_mask=self.route_mask,

@@ -186,3 +186,107 @@ def test_a_binding_of_another_torch_is_noticed(lib, unloaded, monkeypatch):
     assert build.binding_current() and not build.needs_build()
     monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
     assert not build.binding_current() and build.needs_build()
+
+
+# ---- the decoders' own checks: nothing is launched, appended or routed before they pass ----
+
+@pytest.fixture
+def launched(monkeypatch):
+    """Names of the entry points that a step has reached."""
+    calls = []
+    for name in ("route", "rope_append_route_kv", "decode_attention_partial", "decode_attention_quant",
+                 "decode_attention_quant_partial", "prefix_attention"):
+        monkeypatch.setattr(native, name, lambda *a, _n=name, **k: calls.append(_n))
+    return calls
+
+
+def bare(cls, B, Hq, Hkv, L):
+    """A decoder of CPU buffers, as far as the checks look at it."""
+    d = object.__new__(cls)
+    d.shape = (B, Hq, Hkv, L)
+    d.out = torch.zeros(B, Hq, 128, dtype=torch.bfloat16)
+    d.route_mask = d.active_list = None
+    d.workspace = type("W", (), dict(nbytes=native.workspace_bytes(B, Hq, Hkv, L), ptr=FAKE))
+    return d
+
+
+def half(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def shifted(*shape):
+    """bf16, contiguous, two bytes off a 16-byte boundary."""
+    n = torch.Size(shape).numel()
+    return half(n + 16)[1:n + 1].view(shape)
+
+
+def test_quant_decoder_refuses_tensors_of_another_shape_before_it_launches(lib, launched):
+    B, Hq, Hkv, L = 2, 8, 4, 9
+    dec = bare(native.QuantDecoder, B, Hq, Hkv, L)
+    cache = native.QuantCache(B, Hkv, L, device="cpu")
+    lens = torch.ones(B, dtype=torch.int32)
+    good = dict(q=half(B, Hq, 128), k0=half(B, Hkv, 128), n_splits=0)
+    bad = dict(q=[half(B + 1, Hq, 128), half(1, Hq, 128), half(B, 16, 128), half(B, Hq, 64), half(B, Hq, 128).float(),
+                  half(Hq, B, 128).transpose(0, 1), shifted(B, Hq, 128), half(B, Hq, 128).to("meta")],
+               k0=[half(B + 1, Hkv, 128), half(B, 8, 128), half(B, Hkv, 128).float()],
+               n_splits=[-1, native.SR_MAX_SPLITS + 1, 2000])
+
+    def steps(q, k0, n_splits):
+        yield lambda: dec.step(q, cache, k0, good["k0"], lens, 0.6, n_splits)
+        yield lambda: dec.append_step(q, good["k0"], good["k0"], half(L, 64), half(L, 64), cache, k0, good["k0"], lens, 0.6,
+                                      n_splits)
+    for name, values in bad.items():
+        for v in values:
+            for call in steps(**{**good, name: v}):
+                with pytest.raises((ValueError, native.SinkRouterError)):
+                    call()
+    assert launched == []
+    for call in steps(**good):
+        call()
+    assert launched == ["route", "decode_attention_quant", "rope_append_route_kv", "decode_attention_quant"]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_shared_prefix_decoder_refuses_what_does_not_fit_before_it_launches(lib, launched, quant):
+    B, Hq, Hkv, cap, L = 2, 8, 4, 20, 9
+    dec = object.__new__(shared_prefix.SharedPrefixDecoder)
+    dec.suffix = bare(native.Decoder, B, Hq, Hkv, L)
+    dec.workspace = dec.o_suffix = dec.lse_suffix = None
+    if quant:
+        c = native.QuantCache(B, Hkv, L, device="cpu")
+        k, scales = c.k, c.scales
+        caches = [native.QuantCache(1, Hkv, L, device="cpu").k, k.view(torch.int8), k.transpose(1, 2)]
+    else:
+        k, scales = half(B, Hkv, L, 128), None
+        caches = [half(1, Hkv, L, 128), half(B, Hkv + 1, L, 128), k.float(), half(B, Hkv, L, 64), k.transpose(1, 2),
+                  shifted(B, Hkv, L, 128), half(Hkv, L, 128)]
+    rows = half(B, Hkv, 128)
+    good = dict(q=half(B, Hq, 128), k_prefix=half(Hkv, cap, 128), v_prefix=half(Hkv, cap, 128), prefix_len=cap, k_cache=k,
+                v_cache=k, k0=rows, v0=rows, seq_lens=torch.ones(B, dtype=torch.int32), n_splits=0)
+    prefixes = [half(Hkv + 1, cap, 128), half(Hkv, cap, 64), half(Hkv, cap, 128).float(), half(cap, 128),
+                half(cap, Hkv, 128).transpose(0, 1), shifted(Hkv, cap, 128)]
+    bad = dict(q=[half(B + 1, Hq, 128), half(B, 16, 128), half(B, Hq, 128).float()], k_prefix=prefixes,
+               v_prefix=prefixes + [half(Hkv, cap - 1, 128)], prefix_len=[-1, cap + 1], v_cache=caches,
+               k0=[half(B + 1, Hkv, 128), half(B, Hkv + 1, 128)], v0=[half(1, Hkv, 128), rows.float()],
+               seq_lens=[torch.ones(B + 1, dtype=torch.int32), torch.ones(B, dtype=torch.int64)],
+               n_splits=[-2, 2000, native.SR_MAX_SPLITS + 1])
+    bad["k_cache"] = [c for c in caches if c.dtype != torch.int8]
+
+    def steps(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, n_splits):
+        yield lambda: dec.step(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, 0.6, scales, n_splits)
+        yield lambda: dec.append_step(q, rows, rows, None, None, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0,
+                                      seq_lens, 0.6, scales, n_splits)
+    for name, values in bad.items():
+        for v in values:
+            for call in steps(**{**good, name: v}):
+                with pytest.raises((ValueError, native.SinkRouterError)):
+                    call()
+    empty = half(Hkv, 0, 128)
+    for call in steps(**{**good, "k_prefix": empty, "v_prefix": empty, "prefix_len": 0}):
+        with pytest.raises(ValueError, match="prefix_len"):
+            call()
+    assert launched == []
+    part = "decode_attention_quant_partial" if quant else "decode_attention_partial"
+    for call in steps(**good):
+        call()
+    assert launched == ["route", part, "prefix_attention", "rope_append_route_kv", part, "prefix_attention"]
