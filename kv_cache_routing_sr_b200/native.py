@@ -671,10 +671,17 @@ class StepGraph:
     one graph launch. The programmatic dependency between the two kernels is
     kept as a graph edge, and the host cost per step is a single launch.
 
-    The tensors are bound at capture: replay reads whatever they hold then."""
+    The tensors are bound at capture: replay reads whatever they hold then.
+
+    For bf16 caches and a Decoder. The steps of a QuantDecoder and of a
+    SharedPrefixDecoder take other arguments: capture a call of theirs with
+    torch.cuda.graph, after one call outside the capture."""
 
     def __init__(self, decoder: "Decoder", q, k_cache, v_cache, k0, v0, seq_lens, tau, n_splits: int = 0,
                  with_route: bool = True, with_decode: bool = True):
+        if not isinstance(decoder, Decoder) or isinstance(decoder, QuantDecoder):
+            raise TypeError("StepGraph captures the step of a bf16 Decoder; capture other decoders' steps with "
+                            f"torch.cuda.graph, got {type(decoder).__name__}")
         self.decoder = decoder
         self.graph = torch.cuda.CUDAGraph()
         args = (q, k_cache, v_cache, k0, v0, seq_lens)

@@ -290,3 +290,12 @@ def test_shared_prefix_decoder_refuses_what_does_not_fit_before_it_launches(lib,
     for call in steps(**good):
         call()
     assert launched == ["route", part, "prefix_attention", "rope_append_route_kv", part, "prefix_attention"]
+
+
+def test_step_graph_refuses_decoders_whose_step_takes_other_arguments(launched):
+    """An 8-bit decoder's step would take the bf16 step's arguments one place off."""
+    shape = half(1, 1, 128)
+    for cls in (native.QuantDecoder, shared_prefix.SharedPrefixDecoder):
+        with pytest.raises(TypeError, match=cls.__name__):
+            native.StepGraph(object.__new__(cls), shape, shape, shape, shape, shape, shape, 0.6)
+    assert launched == []
