@@ -518,8 +518,9 @@ sr_status sr_decode_attention_quant_partial(const sr_dims *dims, int32_t kv_type
  *   lse         optional out fp32 [B, Hq] (NULL = not wanted)
  *   workspace   device buffer of >= sr_prefix_workspace_bytes(dims) bytes,
  *               256-byte aligned, zeroed once by sr_workspace_init; calls that
- *               overlap on the GPU must not share one. Its first word is the
- *               device error word (sr_get_device_error).
+ *               overlap on the GPU must not share one, calls in turn may, the
+ *               suffixes' scan of the same batch and heads among them. Its first
+ *               word is the device error word (sr_get_device_error).
  * fp32 logits, statistics and sums; the softmax weights enter the second product
  * in bf16. Asynchronous on `stream`. Errors: SR_ERR_INVALID_ARG,
  * SR_ERR_UNSUPPORTED, SR_ERR_WORKSPACE, SR_ERR_CUDA.

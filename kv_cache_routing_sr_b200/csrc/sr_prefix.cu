@@ -79,8 +79,10 @@ template <int TILE> struct Form {
 };
 constexpr float kGrowth = 8.f; // log2 growth of a row's maximum that O is rescaled for
 
-// Workspace: [error word | total weight | first item of each KV head | active
-// sequences of each head | rank of each unit | items | item at each weight | (m, l) | O]
+// Workspace: [error word | total weight | left alone | first item of each KV head | active
+// sequences of each head | rank of each unit | items | item at each weight | (m, l) | O].
+// What is left alone is where a decode workspace keeps its units' arrival counters,
+// which have to stay 0 between launches: one buffer serves both kinds of call in turn.
 struct Layout {
     size_t first, list, rank, items, item_of, ml, o, total;
     int row_cap; // rows of a stream's partial
@@ -95,7 +97,7 @@ Layout layout(int B, int Hq, int Hkv)
     w.row_cap = rows < kRows ? (int)((rows + 7) / 8 * 8) : kRows;
     w.max_items = Hkv * ((rows + kItemRows - 1) / kItemRows);
     w.slots = kGridCap + w.max_items;
-    size_t at = 256;
+    size_t at = WorkspaceLayout{}.cnt_off + sizeof(int32_t) * SR_MAX_UNITS;
     auto take = [&](size_t bytes) {
         const size_t here = at;
         at = align_up(at + bytes, 256);

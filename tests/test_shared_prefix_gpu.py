@@ -353,3 +353,34 @@ def test_items_of_one_tile(B, Hkv, M, Lp):
     assert ws.device_error() == 0
     check(q, lambda b, g, rows: [R.attention(rows, k[g], v[g], Lp)], v0, mask.tolist(), outs[0], lse)
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+@pytest.mark.parametrize("kind", ["bf16", *R.IDS])
+def test_one_workspace_for_suffix_and_prefix_in_turn(kind):
+    """The scans of a step on one buffer that is large enough for both, several steps in
+    a row, against a buffer each: the prefix's plan stays off the decode counters."""
+    B, Hkv, M, Lp, n = 5, 8, 4, 900, 4000
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    kp, vp = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    ks, vs, sc = suffix_of(kind, B, Hkv, n, 7)
+    mask = (torch.rand(B, Hkv, generator=gen(5), device=DEV) < 0.25).to(torch.uint8).reshape(-1)
+    units = (mask == 0).nonzero().reshape(-1).to(torch.int32)
+    active = torch.zeros(1 + B * Hkv, dtype=torch.int32, device=DEV)
+    active[0], active[1:1 + len(units)] = len(units), units
+    sl = torch.tensor([n - 700 * b for b in range(B)], dtype=torch.int32, device=DEV)
+    need = native.workspace_bytes(B, Hkv * M, Hkv, n), native.prefix_workspace_bytes(B, Hkv * M, Hkv, Lp)
+    one = native.Workspace(B, Hkv * M, Hkv, n)
+    one._allocate(max(need), None)
+
+    def step(first, second):
+        if sc is None:
+            o, z = native.decode_attention_partial(q, ks, vs, None, v0, sl, active, workspace=first)
+        else:
+            o, z = native.decode_attention_quant_partial(q, ks, vs, sc, v0, sl, active, workspace=first)
+        return o, native.prefix_attention(q, kp, vp, Lp, v0, mask, o_suffix=o, lse_suffix=z, workspace=second)
+
+    want = step(native.Workspace(B, Hkv * M, Hkv, n), native.PrefixWorkspace(B, Hkv * M, Hkv, Lp))
+    for _ in range(4):
+        got = step(one, one)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert one.device_error() == 0
