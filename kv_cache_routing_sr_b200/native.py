@@ -204,6 +204,14 @@ def _handle(stream) -> int | None:
     return None if stream is None else stream.cuda_stream
 
 
+def _same_device(workspace, t):
+    """The workspace reaches the library as an address: hold its device against the
+    call's tensors (CPU tensors are refused with them)."""
+    d = t.get_device()
+    if d >= 0 and workspace.device_index != d:
+        raise ValueError(f"workspace must be on cuda:{d}, got cuda:{workspace.device_index}")
+
+
 def _loaded():
     return _bound if _bound is not None else _bind()
 
@@ -230,6 +238,7 @@ class Workspace:
     def _allocate(self, nbytes: int, device):
         self.nbytes = nbytes
         self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self.device_index = self.buffer.get_device()
         off = (-self.buffer.data_ptr()) % 256
         self.view = self.buffer[off:off + self.nbytes]
         with torch.cuda.device(self.buffer.device):
@@ -494,6 +503,8 @@ def decode_attention_quant(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_
     log-sum-exp (NaN for sink heads)."""
     if workspace is None:
         workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
+    else:
+        _same_device(workspace, q)
     st, out, _ = _loaded().decode_quant(False, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out,
                                         lse, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_decode_attention_quant", st)
@@ -506,6 +517,8 @@ def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens,
     cache. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
     if workspace is None:
         workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
+    else:
+        _same_device(workspace, q)
     st, o_part, lse_part = _loaded().decode_quant(True, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list,
                                                   n_splits, o_part, lse_part, workspace.ptr, workspace.nbytes,
                                                   _handle(stream))
@@ -537,6 +550,8 @@ def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out
     128]; ``lse`` (fp32 [B, Hq]) receives the log-sum-exp (NaN for sink heads)."""
     if workspace is None:
         workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
+    else:
+        _same_device(workspace, q)
     st, out, _ = _loaded().prefix(False, q, k_prefix, v_prefix, prefix_len, v0, route_mask, o_suffix, lse_suffix, out,
                                   lse, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_prefix_attention", st)
@@ -549,6 +564,8 @@ def prefix_attention_partial(q, k_prefix, v_prefix, prefix_len: int, v0, route_m
     takes it. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
     if workspace is None:
         workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
+    else:
+        _same_device(workspace, q)
     st, o_part, lse_part = _loaded().prefix(True, q, k_prefix, v_prefix, prefix_len, v0, route_mask, None, None, o_part,
                                             lse_part, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_prefix_attention_partial", st)

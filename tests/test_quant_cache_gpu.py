@@ -825,3 +825,24 @@ def test_append_quant_takes_the_largest_token_count(dtype):
     assert int(err) == 0
     assert_rows(c.k[0, :, 1:4], c.scales[0, :, 1:4, 0], x[0, 0, :, None].expand(2, 3, R.D), dtype, "rows")
     assert (c.scales[0, :, [0, 4, 5, 6, 7]] == -7.0).all()
+
+
+def test_a_workspace_of_another_device_is_refused(monkeypatch):
+    """Its memory may not be reachable from the call's device. One GPU: the workspace
+    says that it is elsewhere."""
+    c = native.QuantCache(2, 4, 9)
+    q = torch.zeros(2, 8, R.D, device=DEV, dtype=torch.bfloat16)
+    v0 = torch.zeros(2, 4, R.D, device=DEV, dtype=torch.bfloat16)
+    sl, act = torch.ones(2, dtype=torch.int32, device=DEV), torch.zeros(9, dtype=torch.int32, device=DEV)
+    ws, pws = native.Workspace(2, 8, 4, 9), native.PrefixWorkspace(2, 8, 4, 9)
+    assert ws.device_index == pws.device_index == q.get_device()
+    monkeypatch.setattr(ws, "device_index", 7)
+    monkeypatch.setattr(pws, "device_index", 7)
+    mask = torch.zeros(8, dtype=torch.uint8, device=DEV)
+    kp = torch.zeros(4, 9, R.D, device=DEV, dtype=torch.bfloat16)
+    for call, w in ((native.decode_attention_quant, ws), (native.decode_attention_quant_partial, ws)):
+        with pytest.raises(ValueError, match="cuda:7"):
+            call(q, c.k, c.v, c.scales, v0, sl, act, workspace=w)
+    for call in (native.prefix_attention, native.prefix_attention_partial):
+        with pytest.raises(ValueError, match="cuda:7"):
+            call(q, kp, kp, 9, v0, mask, workspace=pws)
