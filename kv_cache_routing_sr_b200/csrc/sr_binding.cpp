@@ -109,11 +109,18 @@ struct Call {
         return o == Py_None ? nullptr : ptr(o, name, type, shape);
     }
 
-    // An output: the given tensor, or a new one.
-    at::Tensor out(PyObject *o, const char *name, at::ScalarType type, Shape shape) const
+    // An output: the given tensor, or a new one, which belongs to the stream that the
+    // call runs on: what earlier owners of its memory have in flight on another stream
+    // would not be waited for.
+    at::Tensor out(PyObject *o, const char *name, at::ScalarType type, Shape shape, PyObject *on_stream) const
     {
-        if (o == Py_None)
+        if (o == Py_None) {
+            std::optional<c10::cuda::CUDAStreamGuard> guard;
+            if (on_stream != Py_None)
+                guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream(on_stream)),
+                                                               static_cast<c10::DeviceIndex>(device)));
             return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+        }
         const at::Tensor &t = tensor(o, name);
         check(t, name, type, shape);
         return t;
@@ -257,8 +264,8 @@ PyObject *rope_append_route_kv(PyObject *const *a)
     }
     auto *lens_out = static_cast<int32_t *>(c.opt(a[13], "seq_lens_out", kI32, {k.B}));
     auto *err = static_cast<int32_t *>(c.opt(a[17], "device_error", kI32, {1}));
-    const at::Tensor qo = c.out(a[14], "q_out", kBf16, qs), mask = c.out(a[15], "route_mask", kU8, {U}),
-                     active = c.out(a[16], "active_list", kI32, {1 + U});
+    const at::Tensor qo = c.out(a[14], "q_out", kBf16, qs, a[18]), mask = c.out(a[15], "route_mask", kU8, {U}, a[18]),
+                     active = c.out(a[16], "active_list", kI32, {1 + U}, a[18]);
     const sr_dims d{k.B, Hq, k.Hkv, 128, k.Lmax};
     sr_status st;
     {
@@ -288,10 +295,10 @@ PyObject *decode_quant(PyObject *const *a)
     void *v0 = c.ptr(a[5], "v0", kBf16, {k.B, k.Hkv, 128});
     auto *lens = static_cast<int32_t *>(c.ptr(a[6], "seq_lens", kI32, {k.B}));
     auto *active = static_cast<int32_t *>(c.ptr(a[7], "active_list", kI32, {1 + (int64_t)k.B * k.Hkv}));
-    const at::Tensor out = c.out(a[9], partial ? "o_part" : "out", partial ? kF32 : kBf16, qs);
+    const at::Tensor out = c.out(a[9], partial ? "o_part" : "out", partial ? kF32 : kBf16, qs, a[13]);
     at::Tensor lse;
     if (partial || a[10] != Py_None)
-        lse = c.out(a[10], partial ? "lse_part" : "lse", kF32, hs);
+        lse = c.out(a[10], partial ? "lse_part" : "lse", kF32, hs, a[13]);
     auto *z = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
     const sr_dims d{k.B, Hq, k.Hkv, 128, k.Lmax};
     const int32_t ns = whole(a[8], "n_splits");
@@ -328,10 +335,10 @@ PyObject *prefix(PyObject *const *a)
     auto *mask = static_cast<uint8_t *>(c.ptr(a[6], "route_mask", kU8, {(int64_t)B * Hkv}));
     auto *os = static_cast<float *>(c.opt(a[7], "o_suffix", kF32, qs));
     auto *ls = static_cast<float *>(c.opt(a[8], "lse_suffix", kF32, hs));
-    const at::Tensor out = c.out(a[9], partial ? "o_part" : "out", partial ? kF32 : kBf16, qs);
+    const at::Tensor out = c.out(a[9], partial ? "o_part" : "out", partial ? kF32 : kBf16, qs, a[13]);
     at::Tensor lse;
     if (partial || a[10] != Py_None)
-        lse = c.out(a[10], partial ? "lse_part" : "lse", kF32, hs);
+        lse = c.out(a[10], partial ? "lse_part" : "lse", kF32, hs, a[13]);
     auto *z = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
     const sr_dims d{B, Hq, Hkv, 128, Lmax};
     const int32_t len = whole(a[4], "prefix_len");

@@ -461,6 +461,9 @@ class QuantCache:
         self.scales = torch.zeros((*shape[:3], 2), dtype=torch.float32, device=device)
 
 
+# The calls below run on `stream`, or on the current stream of their tensors' device.
+# Tensors that they allocate belong to that stream.
+
 def kv_append_quant(k_new, v_new, start, n_new, k_cache, v_cache, kv_scales, k0=None, v0=None, device_error=None,
                     stream=None):
     """sr_kv_append_quant: quantise tokens t < n_new[b] of k_new / v_new (bf16
@@ -501,13 +504,16 @@ def decode_attention_quant(q, k_cache, v_cache, kv_scales, v0, seq_lens, active_
     """sr_decode_attention_quant: decode_attention over an 8-bit cache. Returns
     out bf16 [B, Hq, 128]; ``lse`` (fp32 [B, Hq]) receives the per-head
     log-sum-exp (NaN for sink heads)."""
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
     else:
         _same_device(workspace, q)
     st, out, _ = _loaded().decode_quant(False, q, k_cache, v_cache, kv_scales, v0, seq_lens, active_list, n_splits, out,
                                         lse, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_decode_attention_quant", st)
+    if own and stream is not None:  # released here, still in use there
+        workspace.buffer.record_stream(stream)
     return out
 
 
@@ -515,7 +521,8 @@ def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens,
                                    lse_part=None, n_splits: int = 0, workspace: Workspace | None = None, stream=None):
     """sr_decode_attention_quant_partial: decode_attention_partial over an 8-bit
     cache. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = Workspace(q.shape[0], q.shape[1], *k_cache.shape[1:3], n_splits, device=q.device)
     else:
         _same_device(workspace, q)
@@ -523,6 +530,8 @@ def decode_attention_quant_partial(q, k_cache, v_cache, kv_scales, v0, seq_lens,
                                                   n_splits, o_part, lse_part, workspace.ptr, workspace.nbytes,
                                                   _handle(stream))
     _check("sr_decode_attention_quant_partial", st)
+    if own and stream is not None:  # released here, still in use there
+        workspace.buffer.record_stream(stream)
     return o_part, lse_part
 
 
@@ -548,13 +557,16 @@ def prefix_attention(q, k_prefix, v_prefix, prefix_len: int, v0, route_mask, out
     prefix_len positions of it), joined with each sequence's suffix when o_suffix
     and lse_suffix (decode_attention_partial's) are given. Returns out bf16 [B, Hq,
     128]; ``lse`` (fp32 [B, Hq]) receives the log-sum-exp (NaN for sink heads)."""
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
     else:
         _same_device(workspace, q)
     st, out, _ = _loaded().prefix(False, q, k_prefix, v_prefix, prefix_len, v0, route_mask, o_suffix, lse_suffix, out,
                                   lse, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_prefix_attention", st)
+    if own and stream is not None:  # released here, still in use there
+        workspace.buffer.record_stream(stream)
     return out
 
 
@@ -562,13 +574,16 @@ def prefix_attention_partial(q, k_prefix, v_prefix, prefix_len: int, v0, route_m
                              workspace: PrefixWorkspace | None = None, stream=None):
     """sr_prefix_attention_partial: the prefix's part alone, as combine_partials
     takes it. Returns (o_part fp32 [B, Hq, 128], lse_part fp32 [B, Hq])."""
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = PrefixWorkspace(q.shape[0], q.shape[1], *k_prefix.shape[:2], device=q.device)
     else:
         _same_device(workspace, q)
     st, o_part, lse_part = _loaded().prefix(True, q, k_prefix, v_prefix, prefix_len, v0, route_mask, None, None, o_part,
                                             lse_part, workspace.ptr, workspace.nbytes, _handle(stream))
     _check("sr_prefix_attention_partial", st)
+    if own and stream is not None:  # released here, still in use there
+        workspace.buffer.record_stream(stream)
     return o_part, lse_part
 
 
@@ -653,6 +668,11 @@ class QuantDecoder(Decoder):
     sr_decode_attention_quant. The cache (a QuantCache, or tensors like its
     parts) is the caller's; k0 and v0 stay bf16."""
 
+    def __init__(self, batch, n_q_heads, n_kv_heads, max_seq_len, max_splits: int = 0, device="cuda"):
+        # before the workspace, behind whose initialisation any stream may use it
+        self.q = torch.empty(batch, n_q_heads, HEAD_DIM, dtype=torch.bfloat16, device=device)
+        super().__init__(batch, n_q_heads, n_kv_heads, max_seq_len, max_splits, device)
+
     def _check(self, q, k0, n_splits):
         B, Hq, Hkv, _ = self.shape
         _expect(q, "q", torch.bfloat16, (B, Hq, HEAD_DIM), self.out.device)
@@ -670,8 +690,6 @@ class QuantDecoder(Decoder):
         """A whole decode step from the un-rotated projections; the cache, k0 / v0
         and seq_lens are updated in place, the rotated query is kept in self.q."""
         self._check(q_in, k0, n_splits)
-        if getattr(self, "q", None) is None:
-            self.q = torch.empty_like(q_in)
         rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, cache.k, cache.v, cache.scales, k0, v0,
                              tau, q_out=self.q, route_mask=self.route_mask, active_list=self.active_list,
                              device_error=device_error, stream=stream)

@@ -28,10 +28,12 @@ class SharedPrefixDecoder:
 
     def __init__(self, batch, n_q_heads, n_kv_heads, max_prefix_len, max_suffix_len, max_splits: int = 0,
                  device="cuda"):
-        self.suffix = native.Decoder(batch, n_q_heads, n_kv_heads, max_suffix_len, max_splits, device=device)
-        self.workspace = native.PrefixWorkspace(batch, n_q_heads, n_kv_heads, max_prefix_len, device=device)
+        # before the workspaces, behind whose initialisation any stream may use them
+        self.q = torch.empty(batch, n_q_heads, native.HEAD_DIM, dtype=torch.bfloat16, device=device)
         self.o_suffix = torch.empty(batch, n_q_heads, native.HEAD_DIM, dtype=torch.float32, device=device)
         self.lse_suffix = torch.empty(batch, n_q_heads, dtype=torch.float32, device=device)
+        self.suffix = native.Decoder(batch, n_q_heads, n_kv_heads, max_suffix_len, max_splits, device=device)
+        self.workspace = native.PrefixWorkspace(batch, n_q_heads, n_kv_heads, max_prefix_len, device=device)
 
     @property
     def out(self):
@@ -95,8 +97,6 @@ class SharedPrefixDecoder:
         The suffix caches and seq_lens are updated in place; the rotated query is
         kept in self.q."""
         self._check(q_in, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, kv_scales, n_splits)
-        if getattr(self, "q", None) is None:
-            self.q = torch.empty_like(q_in)
         native.rope_append_route_kv(q_in, k_new, v_new, rope_cos, rope_sin, seq_lens, k_cache, v_cache, kv_scales, k0,
                                     v0, tau, pos_offset=prefix_len, q_out=self.q, route_mask=self.route_mask,
                                     active_list=self.active_list, device_error=device_error, stream=stream)

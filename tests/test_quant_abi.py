@@ -204,7 +204,7 @@ def bare(cls, B, Hq, Hkv, L):
     """A decoder of CPU buffers, as far as the checks look at it."""
     d = object.__new__(cls)
     d.shape = (B, Hq, Hkv, L)
-    d.out = torch.zeros(B, Hq, 128, dtype=torch.bfloat16)
+    d.out = d.q = torch.zeros(B, Hq, 128, dtype=torch.bfloat16)
     d.route_mask = d.active_list = None
     d.workspace = type("W", (), dict(nbytes=native.workspace_bytes(B, Hq, Hkv, L), ptr=FAKE))
     return d
@@ -251,7 +251,7 @@ def test_shared_prefix_decoder_refuses_what_does_not_fit_before_it_launches(lib,
     B, Hq, Hkv, cap, L = 2, 8, 4, 20, 9
     dec = object.__new__(shared_prefix.SharedPrefixDecoder)
     dec.suffix = bare(native.Decoder, B, Hq, Hkv, L)
-    dec.workspace = dec.o_suffix = dec.lse_suffix = None
+    dec.q = dec.workspace = dec.o_suffix = dec.lse_suffix = None
     if quant:
         c = native.QuantCache(B, Hkv, L, device="cpu")
         k, scales = c.k, c.scales

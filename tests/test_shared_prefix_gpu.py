@@ -384,3 +384,63 @@ def test_one_workspace_for_suffix_and_prefix_in_turn(kind):
         got = step(one, one)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert one.device_error() == 0
+
+
+def stream_calls():
+    """Every entry point that allocates, as (call(stream=..., workspace...), workspace bytes)."""
+    B, Hkv, M, n = 2, 4, 4, 700
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v, sc = suffix_of("e4m3", B, Hkv, n, 3)
+    kp, vp = randn((Hkv, n, R.D), 5), randn((Hkv, n, R.D), 6)
+    sl = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    active = torch.arange(-1, B * Hkv, dtype=torch.int32, device=DEV)
+    active[0] = B * Hkv
+    mask = torch.zeros(B * Hkv, dtype=torch.uint8, device=DEV)
+    cs, sn = inputs.rope_tables(n + 1, device=DEV)
+    kn, k0 = randn((B, Hkv, R.D), 7), randn((B, Hkv, R.D), 8)
+    lens = torch.full_like(sl, n - 1)
+    done = torch.zeros_like(sl)
+    ws, pws = native.Workspace(B, Hkv * M, Hkv, n), native.PrefixWorkspace(B, Hkv * M, Hkv, n)
+    one = lambda x: x if isinstance(x, tuple) else (x,)  # noqa: E731
+    return [
+        (lambda w=ws, **a: one(native.decode_attention_quant(q, k, v, sc, v0, sl, active, workspace=w, **a)), ws),
+        (lambda w=ws, **a: one(native.decode_attention_quant_partial(q, k, v, sc, v0, sl, active, workspace=w, **a)), ws),
+        (lambda w=pws, **a: one(native.prefix_attention(q, kp, vp, n, v0, mask, workspace=w, **a)), pws),
+        (lambda w=pws, **a: one(native.prefix_attention_partial(q, kp, vp, n, v0, mask, workspace=w, **a)), pws),
+        (lambda w=None, **a: one(native.rope_append_route_kv(q, kn, kn, cs, sn, lens, k, v, sc, k0, v0, TAU,
+                                                             seq_lens_out=done, **a)), None),
+    ]
+
+
+@pytest.mark.parametrize("i", range(5), ids=["scan", "scan_partial", "prefix", "prefix_partial", "append"])
+def test_outputs_allocated_for_another_stream(i):
+    """The current stream still writes tensors that have just been released there: an
+    output for a side stream must not lie in their memory."""
+    call, _ = stream_calls()[i]
+    want = [t.clone() for t in call()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = [torch.empty_like(t) for t in want for _ in range(3)]
+    torch.cuda._sleep(40_000_000)
+    for t in late:
+        t.fill_(7)
+    del late, t
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("i", range(4), ids=["scan", "scan_partial", "prefix", "prefix_partial"])
+def test_a_calls_own_workspace_outlives_its_kernels_on_another_stream(i):
+    """A workspace that the call allocates is released when it returns; the side stream
+    has not begun yet, and the current stream takes memory of the same size."""
+    call, ws = stream_calls()[i]
+    want = [t.clone() for t in call()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    got = call(w=None, stream=side)
+    others = [torch.full((ws.nbytes + 256,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(others) == 4
