@@ -33,9 +33,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+template <int BATCH>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock)
-combine_kernel(const float *__restrict__ o_parts, const float *__restrict__ lse_parts, int64_t stride, int n_parts,
-               int n_heads, __nv_bfloat16 *__restrict__ out)
+combine_kernel(const float *o_parts, const float *lse_parts, int64_t stride, int n_parts, int n_heads,
+               __nv_bfloat16 *out)
 {
     // The partials are the previous kernels' output (the decode kernel, or the
     // exchange): wait for them, then let the next kernel launch.
@@ -46,25 +47,46 @@ combine_kernel(const float *__restrict__ o_parts, const float *__restrict__ lse_
     const int warp0 = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
     const int nwarps = gridDim.x * kWarpsPerBlock;
     for (int h = warp0; h < n_heads; h += nwarps) {
-        const float lse0 = __ldg(lse_parts + h);
+        const float lse0 = ld_dep(lse_parts + h);
         float4 acc;
         if (isnan(lse0)) {
-            acc = __ldg(reinterpret_cast<const float4 *>(o_parts + (size_t)h * kHeadDim) + lane);
+            acc = ld_dep(reinterpret_cast<const float4 *>(o_parts + (size_t)h * kHeadDim) + lane);
         } else {
+            // BATCH parts in flight: the first ones' values are asked for before the
+            // maximum of all is known.
+            float4 o[BATCH];
+            float z[BATCH];
+            auto fetch = [&](int r0) {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = min(r0 + i, n_parts - 1);
+                    z[i] = ld_dep(lse_parts + r * stride + h);
+                    o[i] = ld_dep(reinterpret_cast<const float4 *>(o_parts + r * stride + (size_t)h * kHeadDim) + lane);
+                }
+            };
+            fetch(0);
             float mx = -INFINITY;
-            for (int r = 0; r < n_parts; ++r)
-                mx = fmaxf(mx, __ldg(lse_parts + r * stride + h));
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                mx = fmaxf(mx, z[i]);
+            for (int r = BATCH; r < n_parts; ++r)
+                mx = fmaxf(mx, ld_dep(lse_parts + r * stride + h));
             float den = 0.f;
             acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < n_parts; ++r) {
-                const float wr = expf(__ldg(lse_parts + r * stride + h) - mx); // 0 for an empty part
-                const float4 o = __ldg(reinterpret_cast<const float4 *>(o_parts + r * stride +
-                                                                        (size_t)h * kHeadDim) + lane);
-                den += wr;
-                acc.x = fmaf(wr, o.x, acc.x);
-                acc.y = fmaf(wr, o.y, acc.y);
-                acc.z = fmaf(wr, o.z, acc.z);
-                acc.w = fmaf(wr, o.w, acc.w);
+            for (int r0 = 0; r0 < n_parts; r0 += BATCH) {
+                if (r0 > 0)
+                    fetch(r0);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    if (r0 + i >= n_parts)
+                        break;
+                    const float wr = expf(z[i] - mx); // 0 for an empty part
+                    den += wr;
+                    acc.x = fmaf(wr, o[i].x, acc.x);
+                    acc.y = fmaf(wr, o[i].y, acc.y);
+                    acc.z = fmaf(wr, o[i].z, acc.z);
+                    acc.w = fmaf(wr, o[i].w, acc.w);
+                }
             }
             const float inv = 1.f / den;
             acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
@@ -99,8 +121,10 @@ cudaError_t launch_combine(int n_heads, int n_parts, const float *o_parts, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, combine_kernel, o_parts, lse_parts, part_stride, n_parts, n_heads,
-                           static_cast<__nv_bfloat16 *>(out));
+    // Parts in flight a warp, four against eight: 2.6 us against 3.3 for 2 parts of 8192
+    // heads; 2.1 / 1.7 for 8 parts of 32 heads, 5.0 / 4.4 of 8192.
+    e = cudaLaunchKernelEx(&cfg, n_parts <= 4 ? combine_kernel<4> : combine_kernel<8>, o_parts, lse_parts, part_stride,
+                           n_parts, n_heads, static_cast<__nv_bfloat16 *>(out));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -254,7 +254,7 @@ __device__ __forceinline__ long long div_nonneg(long long a, long long b)
 // when the batch fits it.
 __device__ __forceinline__ int unit_len(const Params &p, int u, const int32_t *seqtab)
 {
-    const int L = seqtab ? seqtab[u / p.Hkv] : __ldg(p.seq_lens + u / p.Hkv);
+    const int L = seqtab ? seqtab[u / p.Hkv] : ld_dep(p.seq_lens + u / p.Hkv);
     return L < 1 ? 1 : (L > p.Lmax ? p.Lmax : L);
 }
 
@@ -309,7 +309,7 @@ __device__ __forceinline__ long long block_scan(long long x, Misc *misc, long lo
 template <int M, int NWARPS>
 __device__ __forceinline__ void route_all_units(const Params &p, int U, uint8_t *flag)
 {
-    route_units_warp<M, true>(reinterpret_cast<const uint4 *>(p.q), reinterpret_cast<const uint4 *>(p.k0), U, p.tau,
+    route_units_warp<M>(reinterpret_cast<const uint4 *>(p.q), reinterpret_cast<const uint4 *>(p.k0), U, p.tau,
                               (int)threadIdx.x >> 5, NWARPS, [&](int u, bool sink) {
                                   flag[u] = sink ? 1 : 0;
                                   if (blockIdx.x == 0 && p.mask_out)
@@ -517,10 +517,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #endif
         // All inputs are read after the wait: the preceding kernel may write
         // any of them (the routing kernel the list, the append step seq_lens).
-        const int sl = (lane < p.B) ? __ldg(p.seq_lens + lane) : 1;
+        const int sl = (lane < p.B) ? ld_dep(p.seq_lens + lane) : 1;
         if constexpr (!FUSED) {
-            n = __ldg(p.active);
-            const int e = (lane < U) ? __ldg(p.active + 1 + lane) : -1;
+            n = ld_dep(p.active);
+            const int e = (lane < U) ? ld_dep(p.active + 1 + lane) : -1;
             if (n < 0 || n > U) {
                 errbits |= SR_DEVERR_ACTIVE_LIST;
                 n = n < 0 ? 0 : U;
@@ -583,10 +583,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             SR_STAMP(tl_decode, 1);
         __syncthreads();
 
-        n = __ldg(p.active);
+        n = ld_dep(p.active);
         if (seq_smem)
             for (int b = tid; b < p.B; b += kThreads)
-                seqtab[b] = __ldg(p.seq_lens + b);
+                seqtab[b] = ld_dep(p.seq_lens + b);
         if (n < 0 || n > U) {
             errbits |= SR_DEVERR_ACTIVE_LIST;
             n = n < 0 ? 0 : U;
@@ -594,8 +594,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         // Keep the longest well-formed prefix of the list (indices in range and
         // strictly ascending); a malformed entry ends it and is reported.
         for (int i = tid; i < U; i += kThreads) {
-            const int u = __ldg(p.active + 1 + i);
-            const int prev = (i > 0) ? __ldg(p.active + i) : -1;
+            const int u = ld_dep(p.active + 1 + i);
+            const int prev = (i > 0) ? ld_dep(p.active + i) : -1;
             if (i >= n)
                 continue;
             if (u < 0 || u >= U || u <= prev)
@@ -612,7 +612,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         }
         for (int i = tid; i < n; i += kThreads) {
             const int u = utab[i];
-            int L = seq_smem ? seqtab[u / p.Hkv] : __ldg(p.seq_lens + u / p.Hkv);
+            int L = seq_smem ? seqtab[u / p.Hkv] : ld_dep(p.seq_lens + u / p.Hkv);
             if (L < 1 || L > p.Lmax) {
                 errbits |= SR_DEVERR_SEQ_LEN;
                 L = L < 1 ? 1 : p.Lmax;
@@ -627,7 +627,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         grid_launch_dependents();
         if (seq_smem)
             for (int b = tid; b < p.B; b += kThreads)
-                seqtab[b] = __ldg(p.seq_lens + b);
+                seqtab[b] = ld_dep(p.seq_lens + b);
         route_all_units<kThreads / 32>(p, U, sflag, M);
         __syncthreads();
         // Ordered compaction of the active units into the same tables the
@@ -639,7 +639,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             const long long incl = block_scan<kThreads / 32>(act ? 1 : 0, misc, &tot);
             if (act) {
                 const int i = n + (int)incl - 1;
-                int L = seq_smem ? seqtab[u / p.Hkv] : __ldg(p.seq_lens + u / p.Hkv);
+                int L = seq_smem ? seqtab[u / p.Hkv] : ld_dep(p.seq_lens + u / p.Hkv);
                 if (L < 1 || L > p.Lmax) {
                     errbits |= SR_DEVERR_SEQ_LEN;
                     L = L < 1 ? 1 : p.Lmax;
@@ -980,13 +980,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             const size_t row0 = (size_t)b * p.Hq + (size_t)gg * M;
             if (p.out_f32) {
                 // fp32 copy of v0 (exact): lane c4 widens elements 4 c4 .. 4 c4 + 3
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v0 + (size_t)u * kHeadDim) + lane);
+                const uint2 v = ld_dep(reinterpret_cast<const uint2 *>(p.v0 + (size_t)u * kHeadDim) + lane);
                 const float4 f = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
                                              __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
                 for (int hh = 0; hh < M; ++hh)
                     reinterpret_cast<float4 *>(p.out_f32 + (row0 + hh) * kHeadDim)[lane] = f;
             } else {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.v0 + (size_t)u * kHeadDim) + (lane & 15));
+                const uint4 v = ld_dep(reinterpret_cast<const uint4 *>(p.v0 + (size_t)u * kHeadDim) + (lane & 15));
                 for (int e = lane; e < M * 16; e += 32) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + (row0 + (e >> 4)) * kHeadDim);
                     dst[e & 15] = v;

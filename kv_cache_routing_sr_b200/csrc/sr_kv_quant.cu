@@ -75,8 +75,8 @@ template <int KV> __global__ void __launch_bounds__(kThreads, 6) write_kernel(Kv
     const long long nw = (long long)gridDim.x * kWarps;
     for (long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += nw) {
         const Item it = item_of(i, a.n_kv_heads, nblk, lane);
-        const int n = clamp_count(__ldg(a.n + it.b), a.n_tokens, a.error);
-        const long long slot = (long long)__ldg(a.start + it.b) + it.t;
+        const int n = clamp_count(ld_dep(a.n + it.b), a.n_tokens, a.error);
+        const long long slot = (long long)ld_dep(a.start + it.b) + it.t;
         bool live = it.t < n;
         if (live && (slot < 0 || slot >= a.max_seq_len)) {
             live = false;
@@ -159,8 +159,8 @@ template <int KV> __global__ void __launch_bounds__(kThreads) read_kernel(KvRead
     const long long nw = (long long)gridDim.x * kWarps;
     for (long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += nw) {
         const Item it = item_of(i, a.n_kv_heads, nblk, lane);
-        const int n = clamp_count(__ldg(a.n + it.b), a.n_rows, a.error);
-        const long long pos = (long long)__ldg(a.start + it.b) + it.t;
+        const int n = clamp_count(ld_dep(a.n + it.b), a.n_rows, a.error);
+        const long long pos = (long long)ld_dep(a.start + it.b) + it.t;
         if (it.t >= n)
             continue;
         if (pos < 0 || pos >= a.max_seq_len) {

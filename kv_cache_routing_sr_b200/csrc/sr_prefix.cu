@@ -474,7 +474,7 @@ __device__ __forceinline__ void stage_query(const Params &p, uint8_t *tile, cons
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int f = __shfl_sync(kFull, from, 2 * (h + i) + (lane >> 4));
-            x[i] = f >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q) + (size_t)f * (kHeadDim / 8) + c)
+            x[i] = f >= 0 ? ld_dep(reinterpret_cast<const uint4 *>(p.q) + (size_t)f * (kHeadDim / 8) + c)
                           : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
@@ -1150,7 +1150,7 @@ template <Join J> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel
     float wp = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
     bool suffix = false;
     if (p.o_suffix && rank >= 0) {
-        const float ls = __ldg(p.lse_suffix + row), top = fmaxf(lse, ls);
+        const float ls = ld_dep(p.lse_suffix + row), top = fmaxf(lse, ls);
         if ((suffix = ls != -INFINITY)) {
             const float ep = expf(lse - top), es = expf(ls - top), tot = ep + es;
             wp *= ep / tot;
@@ -1163,13 +1163,13 @@ template <Join J> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel
         const int at = one ? lane : 8 * (split ? warp : c) + (lane & 7); // of the row's 32 float4
         float4 x = acc[c];
         if (rank < 0) { // a sink head
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v0 + u * kHeadDim) + at);
+            const uint2 v = ld_dep(reinterpret_cast<const uint2 *>(p.v0 + u * kHeadDim) + at);
             x = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                             __uint_as_float(v.y & 0xffff0000u));
         } else {
             float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
             if (suffix)
-                os = __ldg(reinterpret_cast<const float4 *>(p.o_suffix + (size_t)row * kHeadDim) + at);
+                os = ld_dep(reinterpret_cast<const float4 *>(p.o_suffix + (size_t)row * kHeadDim) + at);
             x.x = x.x * wp + os.x * ws;
             x.y = x.y * wp + os.y * ws;
             x.z = x.z * wp + os.z * ws;

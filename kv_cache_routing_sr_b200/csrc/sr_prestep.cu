@@ -163,8 +163,8 @@ template <int KV> __device__ __forceinline__ float store_row(uint8_t *cache, siz
 __device__ __forceinline__ void load_table8(const float *tab, int pos, int j, float4 (&v)[2])
 {
     const float4 *t = reinterpret_cast<const float4 *>(tab + (size_t)pos * (kHeadDim / 2) + 8 * j);
-    v[0] = __ldg(t);
-    v[1] = __ldg(t + 1);
+    v[0] = ld_dep(t);
+    v[1] = ld_dep(t + 1);
 }
 
 template <int M, int KV, int SPREAD>
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
         // same round trip as the slot itself.
         const uint4 *kn = reinterpret_cast<const uint4 *>(p.k_new + (size_t)u * kHeadDim);
         const uint4 *vn = reinterpret_cast<const uint4 *>(p.v_new + (size_t)u * kHeadDim);
-        const uint4 klo = __ldg(kn + j), khi = __ldg(kn + j + 8);
-        const uint4 vlo = __ldg(vn + j), vhi = __ldg(vn + j + 8);
+        const uint4 klo = ld_dep(kn + j), khi = ld_dep(kn + j + 8);
+        const uint4 vlo = ld_dep(vn + j), vhi = ld_dep(vn + j + 8);
         const int pos = slot_of(p, u / p.Hkv);
         uint4 *ks = krows + lu * 16;
         uint4 *k0g = reinterpret_cast<uint4 *>(p.k0 + (size_t)u * kHeadDim);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) rope_append_route_kernel(PrestepP
     __syncthreads();
     if constexpr (SPREAD == kCluster)
         cooperative_groups::this_cluster().barrier_wait(); // CTA 0 runs: its shared memory may be written
-    route_units_warp<M, false>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
+    route_units_warp<M>(rows, krows, nu, p.tau, (int)threadIdx.x >> 5, kWarps, [&](int lu, bool sink) {
         if constexpr (SPREAD != kWide)
             all_flags[u0 + lu] = sink ? 1 : 0;
         p.mask[u0 + lu] = sink ? 1 : 0;

@@ -74,6 +74,12 @@ __device__ __forceinline__ void grid_launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads an input that the kernel just before in the stream may have written while this
+// one was already resident: an ordinary load, behind the wait above. A read-only load
+// (ld.global.nc) promises that nobody writes the place while the kernel lives, and may
+// be moved ahead of the wait.
+template <typename T> __device__ __forceinline__ T ld_dep(const T *p) { return *p; }
+
 __device__ __forceinline__ uint64_t global_timer_ns()
 {
     uint64_t t;

@@ -46,8 +46,7 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 // one sink flag per unit.
 template <int M>
 __global__ void __launch_bounds__(kRouteThreads, 1)
-route_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k0, float tau,
-             uint8_t *__restrict__ mask, int32_t *__restrict__ active, int B, int Hkv)
+route_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *k0, float tau, uint8_t *mask, int32_t *active, int B, int Hkv)
 {
     extern __shared__ uint8_t sink_flag[]; // [B*Hkv]
     __shared__ int32_t warp_cnt[kRouteWarps];
@@ -74,7 +73,7 @@ route_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restric
     }
 #endif
 
-    route_units_warp<M, true>(reinterpret_cast<const uint4 *>(q), reinterpret_cast<const uint4 *>(k0), U, tau,
+    route_units_warp<M>(reinterpret_cast<const uint4 *>(q), reinterpret_cast<const uint4 *>(k0), U, tau,
                               (int)threadIdx.x >> 5, kRouteWarps, [&](int u, bool sink) {
                                   sink_flag[u] = sink ? 1 : 0;
                                   mask[u] = sink ? 1 : 0;
@@ -91,14 +90,13 @@ route_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restric
 // group (or 4 / M) a warp, with the same arithmetic.
 template <int M>
 __global__ void __launch_bounds__(kRouteThreads)
-wide_route_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k0, float tau,
-                  uint8_t *__restrict__ mask, int U)
+wide_route_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *k0, float tau, uint8_t *mask, int U)
 {
     constexpr int kUnits = kRouteWarps * RouteLanes<M>::UNITS;
     grid_dependency_wait();
     grid_launch_dependents();
     const int u0 = blockIdx.x * kUnits;
-    route_units_warp<M, true>(reinterpret_cast<const uint4 *>(q) + (size_t)u0 * M * 16,
+    route_units_warp<M>(reinterpret_cast<const uint4 *>(q) + (size_t)u0 * M * 16,
                               reinterpret_cast<const uint4 *>(k0) + (size_t)u0 * 16, min(kUnits, U - u0), tau,
                               (int)threadIdx.x >> 5, kRouteWarps, [&](int u, bool sink) { mask[u0 + u] = sink ? 1 : 0; });
 }

@@ -75,9 +75,9 @@ __device__ __forceinline__ float group_min_cosine(const uint4 (&qv)[RouteLanes<M
 
 // This lane's blocks of warp chunk `chunk` (units chunk*UNITS ..): qrows holds
 // nu*M query rows (row u*M+m) and krows nu key rows, 16 blocks each, in global
-// memory (kGlobal: read-only loads) or shared memory. Units past nu read as
-// zero. Returns this lane's unit.
-template <int M, bool kGlobal>
+// or shared memory. Ordinary loads: the kernel before may have written the rows.
+// Units past nu read as zero. Returns this lane's unit.
+template <int M>
 __device__ __forceinline__ int load_route_blocks(const uint4 *qrows, const uint4 *krows, int nu, int chunk,
                                                  uint4 (&qv)[RouteLanes<M>::V], uint4 (&kv)[RouteLanes<M>::V])
 {
@@ -91,8 +91,8 @@ __device__ __forceinline__ int load_route_blocks(const uint4 *qrows, const uint4
         if (unit < nu) {
             const uint4 *qp = qrows + qrow * 16 + j * RL::V + v;
             const uint4 *kp = krows + (size_t)unit * 16 + j * RL::V + v;
-            qv[v] = kGlobal ? __ldg(qp) : *qp;
-            kv[v] = kGlobal ? __ldg(kp) : *kp;
+            qv[v] = *qp;
+            kv[v] = *kp;
         } else {
             qv[v] = make_uint4(0u, 0u, 0u, 0u);
             kv[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -105,7 +105,7 @@ __device__ __forceinline__ int load_route_blocks(const uint4 *qrows, const uint4
 // wid + nwarps, ..., and issues the loads of its next chunk before reducing
 // the current one. For every unit one lane calls store(u, sink), sink being
 // (s_g >= tau). Called by whole warps; no block barrier inside.
-template <int M, bool kGlobal, typename Store>
+template <int M, typename Store>
 __device__ __forceinline__ void route_units_warp(const uint4 *qrows, const uint4 *krows, int nu, float tau, int wid,
                                                  int nwarps, Store &&store)
 {
@@ -116,12 +116,12 @@ __device__ __forceinline__ void route_units_warp(const uint4 *qrows, const uint4
     if (c >= nchunks)
         return;
     uint4 qa[RL::V], ka[RL::V];
-    int ua = load_route_blocks<M, kGlobal>(qrows, krows, nu, c, qa, ka);
+    int ua = load_route_blocks<M>(qrows, krows, nu, c, qa, ka);
     for (; c < nchunks; c += nwarps) {
         uint4 qb[RL::V], kb[RL::V];
         int ub = nu;
         if (c + nwarps < nchunks)
-            ub = load_route_blocks<M, kGlobal>(qrows, krows, nu, c + nwarps, qb, kb);
+            ub = load_route_blocks<M>(qrows, krows, nu, c + nwarps, qb, kb);
         const float s = group_min_cosine<M>(qa, ka);
         if (lane % (RL::W * M) == 0 && ua < nu)
             store(ua, s >= tau);

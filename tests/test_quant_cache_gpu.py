@@ -846,3 +846,55 @@ def test_a_workspace_of_another_device_is_refused(monkeypatch):
     for call in (native.prefix_attention, native.prefix_attention_partial):
         with pytest.raises(ValueError, match="cuda:7"):
             call(q, kp, kp, 9, v0, mask, workspace=pws)
+
+
+def test_calls_in_a_row_see_what_the_one_before_wrote():
+    """Chains without a host wait in which a call's inputs are what the previous call's
+    kernel wrote, while its own kernel may already be resident: position-0 rows into
+    routing and the sink bypass, lengths into a read-back, a partial into the
+    combination. Fresh values in the same buffers every time."""
+    B, Hkv, M, L = 3, 8, 4, 6
+    Hq = Hkv * M
+    c = native.QuantCache(B, Hkv, L)
+    k0, v0 = (torch.zeros(B, Hkv, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    zero, n = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(2))
+    mask = torch.zeros(B * Hkv, dtype=torch.uint8, device=DEV)
+    active = torch.zeros(1 + B * Hkv, dtype=torch.int32, device=DEV)
+    ws = native.Workspace(B, Hq, Hkv, L)
+    out = torch.zeros(B, Hq, R.D, device=DEV, dtype=torch.bfloat16)
+    ko, vo = (torch.zeros(B, Hkv, L, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    cs, sn = inputs.rope_tables(L, device=DEV)
+    part = torch.zeros(2, B * Hq * R.D, device=DEV)
+    lse = torch.zeros(2, B * Hq * R.D, device=DEV)
+    joined = torch.zeros_like(out)
+    rounds = 40
+    x = torch.randn(rounds, 2, B, 1, Hkv, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    q = torch.randn(rounds, B, Hkv, M, R.D, generator=gen(2), device=DEV)
+    near = torch.rand(rounds, B, Hkv, 1, 1, generator=gen(3), device=DEV) < 0.5
+    q = torch.where(near, x[:, 0, :, 0, :, None].float() + 0.1 * q, q).to(torch.bfloat16).reshape(rounds, B, Hq, R.D)
+    lens = torch.randint(1, L, (rounds, B), generator=gen(4), device=DEV, dtype=torch.int32)
+    one = torch.ones_like(n)
+    seen = []
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        native.kv_append_quant(x[i, 0], x[i, 1], zero, one, c.k, c.v, c.scales, k0, v0)
+        native.route(q[i], k0, TAU, mask, active)
+        native.decode_attention_quant_partial(q[i], c.k, c.v, c.scales, v0, one, active, part[0].view(B, Hq, R.D),
+                                              lse[0, :B * Hq].view(B, Hq), workspace=ws)
+        native.combine_partials(part, lse, B * Hq * R.D, 1, B, Hq, joined)
+        native.decode_attention_quant(q[i], c.k, c.v, c.scales, v0, one, active, out, workspace=ws)
+        native.rope_append_route_kv(q[i], x[i, 0, :, 0], x[i, 1, :, 0], cs, sn, lens[i], c.k, c.v, c.scales, k0, v0, TAU,
+                                    seq_lens_out=n)
+        native.kv_dequant(c.k, c.v, c.scales, zero, n, ko, vo)
+        seen.append([t.clone() for t in (mask, out, joined, n, ko, vo)])
+    torch.cuda.synchronize()
+    for i, (m, o, j, nn, k, v) in enumerate(seen):
+        assert torch.equal(m.view(B, Hkv), near[i, ..., 0, 0].to(torch.uint8)) and torch.equal(nn, lens[i] + 1)
+        assert torch.equal(o, j)
+        kc, ks = R.quantise(x[i, :, :, 0], R.E4M3)  # [2, B, Hkv, 128]
+        row = (kc * ks[..., None].double()).to(torch.bfloat16)
+        for b in range(B):
+            for g in range(Hkv):  # one position: its value row, or the position-0 value
+                want = x[i, 1, b, 0, g] if near[i, b, g] else row[1, b, g]
+                assert torch.equal(o.view(B, Hkv, M, R.D)[b, g], want.expand(M, -1))
+            assert torch.equal(v[b, :, int(nn[b]) - 1], row[1, b])
