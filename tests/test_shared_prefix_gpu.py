@@ -444,3 +444,31 @@ def test_a_calls_own_workspace_outlives_its_kernels_on_another_stream(i):
     others = [torch.full((ws.nbytes + 256,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(others) == 4
+
+
+@pytest.mark.parametrize("kind", ["bf16", *R.IDS])
+@pytest.mark.parametrize("B,Hkv,M,Lp", [(2, 8, 4, 600), (9, 4, 8, 77), (5, 32, 1, 0), (40, 2, 4, 129)])
+def test_shared_prefix_step_routes_the_planted_sinks_and_no_others(B, Hkv, M, Lp, kind):
+    """The step's mask is the planted one, with active units in every case, and active
+    heads are the attention over prefix and suffix together: neither part alone."""
+    cap, n = max(1, Lp), 90
+    lens = [1 + (31 * b) % n for b in range(B)]
+    k0, v0 = randn((B, Hkv, R.D), 5), randn((B, Hkv, R.D), 6)
+    r = randn((B, Hkv, M, R.D), 1).float()
+    hat = k0.float() / k0.float().norm(dim=-1, keepdim=True)
+    r = r - (r * hat[:, :, None]).sum(-1, keepdim=True) * hat[:, :, None]  # cosine 0 to the position-0 key
+    planted = torch.tensor([[g == b % Hkv for g in range(Hkv)] for b in range(B)], device=DEV)
+    q = torch.where(planted[..., None, None], k0[:, :, None].float() + 0.05 * r, r).to(torch.bfloat16).reshape(B, Hkv * M, R.D)
+    kp, vp = randn((Hkv, cap, R.D), 3), randn((Hkv, cap, R.D), 4)
+    ks, vs, sc = suffix_of(kind, B, Hkv, n, 7)
+    dec = shared_prefix.SharedPrefixDecoder(B, Hkv * M, Hkv, cap, n)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = dec.step(q, kp, vp, Lp, ks, vs, k0, v0, sl, TAU, kv_scales=sc)
+    mask = dec.route_mask.view(B, Hkv)
+    assert torch.equal(mask, planted.to(torch.uint8)) and not bool(mask.all())
+    part = [lambda b, g, rows: R.attention(rows, kp[g], vp[g], Lp),
+            lambda b, g, rows: R.attention(rows, *suffix_rows(ks, vs, sc, b, g, lens[b]), lens[b])]
+    check(q, lambda b, g, rows: [p(b, g, rows) for p in part], v0, mask.tolist(), out, None)
+    for p in part if Lp else part[:1]:
+        with pytest.raises(AssertionError):
+            check(q, lambda b, g, rows: [p(b, g, rows)], v0, mask.tolist(), out, None)  # noqa: B023
