@@ -898,3 +898,52 @@ def test_calls_in_a_row_see_what_the_one_before_wrote():
                 want = x[i, 1, b, 0, g] if near[i, b, g] else row[1, b, g]
                 assert torch.equal(o.view(B, Hkv, M, R.D)[b, g], want.expand(M, -1))
             assert torch.equal(v[b, :, int(nn[b]) - 1], row[1, b])
+
+
+def spread(n, count):
+    """About `count` indices over [0, n), the last among them."""
+    return sorted({*range(0, n, max(1, n // count)), n - 1})
+
+
+@pytest.mark.parametrize("ns", [0, 2])
+@pytest.mark.parametrize("B,Hkv,M,Lmax", [(16384, 1, 1, 3), (2048, 8, 8, 70), (5000, 1, 8, 130)])
+def test_scan_of_the_largest_launches(B, Hkv, M, Lmax, ns):
+    """Up to the most units that a launch takes, more sequences than the length table
+    holds, an odd number of scale pairs; a spread of sequences is checked."""
+    lens = [1 + (7 * b) % Lmax for b in range(B)]
+    c = filled_cache(B, Hkv, Lmax, lens, R.E4M3, 3, poison=False)
+    q = torch.randn(B, Hkv * M, R.D, generator=gen(1), device=DEV).to(torch.bfloat16)
+    v0 = torch.randn(B, Hkv, R.D, generator=gen(2), device=DEV).to(torch.bfloat16)
+    mask = torch.rand(B, Hkv, generator=gen(3), device=DEV) < 0.3
+    out, lse, o = scan(q, c, v0, lens, mask, ns)
+    at = spread(B, 40)
+    part = native.QuantCache(len(at), Hkv, Lmax)
+    for to, x in ((part.k, c.k), (part.v, c.v)):
+        to.view(torch.uint8).copy_(x.view(torch.uint8)[at])
+    part.scales.copy_(c.scales[at])
+    check_scan(q[at], part, v0[at], [lens[i] for i in at], mask[at].tolist(), out[at], lse[at], o[at])
+
+
+@both
+@pytest.mark.parametrize("B,Hkv,M", [(2048, 8, 8), (16384, 1, 1), (33, 8, 8), (12, 4, 8), (48, 1, 8)])
+def test_append_of_the_largest_launches(B, Hkv, M, dtype):
+    """The 8-bit append in its three spreads, up to the most units, against the bf16 one:
+    the same query, routing and lengths, and its rotated key quantised."""
+    Lmax = 5
+    c = native.QuantCache(B, Hkv, Lmax, dtype)
+    q, kn, vn = inputs.make_projections(B, Hkv * M, Hkv, seed=1, device=DEV)
+    cs, sn = inputs.rope_tables(Lmax, device=DEV)
+    k0, v0 = (torch.randn(B, Hkv, R.D, generator=gen(i), device=DEV).to(torch.bfloat16) for i in (1, 2))
+    seq = torch.tensor([(3 * b) % Lmax for b in range(B)], dtype=torch.int32, device=DEV)
+    at = seq.long()
+    kb, vb = (torch.zeros(B, Hkv, Lmax, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    k0b, v0b, seqb = k0.clone(), v0.clone(), seq.clone()
+    q1, m1, a1 = native.rope_append_route_kv(q, kn, vn, cs, sn, seq, c.k, c.v, c.scales, k0, v0, TAU)
+    q2, m2, a2 = native.rope_append_route(q, kn, vn, cs, sn, seqb, kb, vb, k0b, v0b, TAU)
+    n = int(a2[0])
+    for x, y in ((q1, q2), (m1, m2), (a1[:1 + n], a2[:1 + n]), (seq, seqb), (k0, k0b), (v0, v0b)):
+        assert torch.equal(x, y)
+    i = torch.arange(B, device=DEV)
+    for codes, part, rows_of in ((c.k, 0, kb), (c.v, 1, vb)):
+        assert_rows(codes.view(torch.uint8)[i, :, at].view(dtype), c.scales[i, :, at][..., part], rows_of[i, :, at], dtype,
+                    "appended rows")

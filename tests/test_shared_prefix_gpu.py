@@ -472,3 +472,51 @@ def test_shared_prefix_step_routes_the_planted_sinks_and_no_others(B, Hkv, M, Lp
     for p in part if Lp else part[:1]:
         with pytest.raises(AssertionError):
             check(q, lambda b, g, rows: [p(b, g, rows)], v0, mask.tolist(), out, None)  # noqa: B023
+
+
+def spread(n, count):
+    """About `count` indices over [0, n), the last among them."""
+    return sorted({*range(0, n, max(1, n // count)), n - 1})
+
+
+@pytest.mark.parametrize("B,Hkv,M,Lp", [(16384, 1, 8, 70), (2048, 8, 8, 300), (16384, 1, 1, 5000), (1, 16384, 1, 2),
+                                        (8, 2048, 1, 130)])
+def test_largest_launches(B, Hkv, M, Lp):
+    """Up to the most units and 131072 rows; a spread of sequences and heads is checked."""
+    q, v0 = randn((B, Hkv * M, R.D), 1), randn((B, Hkv, R.D), 2)
+    k, v = randn((Hkv, Lp, R.D), 3), randn((Hkv, Lp, R.D), 4)
+    mask = (torch.rand(B, Hkv, generator=gen(5), device=DEV) < 0.25).to(torch.uint8)
+    ws = native.PrefixWorkspace(B, Hkv * M, Hkv, Lp)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = native.prefix_attention(q, k, v, Lp, v0, mask.reshape(-1), lse=lse, workspace=ws)
+    assert ws.device_error() == 0
+    at, gs = spread(B, 30), spread(Hkv, 20)
+    hs = [g * M + m for g in gs for m in range(M)]
+    check(q[at][:, hs], lambda b, g, rows: [R.attention(rows, k[gs[g]], v[gs[g]], Lp)], v0[at][:, gs],
+          mask[at][:, gs].tolist(), out[at][:, hs], lse[at][:, hs])
+
+
+def test_far_positions_of_a_prefix_over_4_gib():
+    """Positions behind 2^24 and rows behind byte offset 2^32: all keys but the last three
+    are zero (logit 0), and so are all values."""
+    Hkv, M, B, n = 2, 4, 3, (1 << 24) + 5
+    k, v = (torch.zeros(Hkv, n, R.D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    k[:, -3:], v[:, -3:] = randn((Hkv, 3, R.D), 1), randn((Hkv, 3, R.D), 2)
+    q = (4 * k[:, -2].float()[None, :, None] + 0.1 * randn((B, Hkv, M, R.D), 3).float()).to(torch.bfloat16)
+    q, v0 = q.reshape(B, Hkv * M, R.D), randn((B, Hkv, R.D), 5)
+    lse = torch.zeros(B, Hkv * M, device=DEV)
+    out = native.prefix_attention(q, k, v, n, v0, torch.zeros(B * Hkv, dtype=torch.uint8, device=DEV), lse=lse)
+    for g in range(Hkv):
+        h = slice(g * M, (g + 1) * M)
+        kd, vd, rows = k[g, -3:].double(), v[g, -3:].double(), q[:, h].double().reshape(-1, R.D)
+        e = torch.exp(rows @ kd.T / math.sqrt(R.D))
+        tot = e.sum(-1, keepdim=True) + (n - 3)
+        o, a = e @ vd / tot, e @ vd.abs() / tot
+        delta = 130 * R.HALF_F32 * (rows.abs() @ kd.abs().T / math.sqrt(R.D)).amax(-1)
+        # the sum of 2^24 ones in fp32: a tile's 128 in two chains, a CTA's tiles and the CTAs' partials in a row add
+        # at most 2^11 of them one after another
+        lim = R.bound(o, a, delta, R.HALF_BF16, R.HALF_BF16) + 2.0 ** -12 * a
+        err = (out[:, h].double().reshape(-1, R.D) - o).abs()
+        assert bool((err <= lim).all()), float((err / lim).max())
+        z = torch.log(tot[:, 0])
+        assert ((lse[:, h].double().reshape(-1) - z).abs() <= R.lse_bound(z, delta) + 2.0 ** -12).all()
