@@ -27,12 +27,6 @@ namespace {
 
 constexpr int kWarpsPerBlock = 8;
 
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <int BATCH>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock)
 combine_kernel(const float *o_parts, const float *lse_parts, int64_t stride, int n_parts, int n_heads,
@@ -92,8 +86,8 @@ combine_kernel(const float *o_parts, const float *lse_parts, int64_t stride, int
             acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
         }
         uint2 packed;
-        packed.x = pack2(acc.x, acc.y);
-        packed.y = pack2(acc.z, acc.w);
+        packed.x = pack_bf16x2(acc.x, acc.y);
+        packed.y = pack_bf16x2(acc.z, acc.w);
         reinterpret_cast<uint2 *>(out + (size_t)h * kHeadDim)[lane] = packed;
     }
 }

@@ -9,9 +9,10 @@
 // Figure 1 caption, eq. (1) (attention-weighted sum of cached values).
 //
 // Design (B200, sm_100a):
-//  * One persistent CTA per SM: 4 consumer warps + 1 producer warp. The grid
-//    never depends on the route result, so the launch needs no host sync; each
-//    CTA reads the active list and seq_lens and derives its share of the work.
+//  * One persistent CTA per SM: 4 consumer warps (8 for an 8-bit cache with eight
+//    heads a group) + 1 producer warp. The grid never depends on the route result,
+//    so the launch needs no host sync; each CTA reads the active list and seq_lens
+//    and derives its share of the work.
 //  * Automatic splits: the active positions of all units are concatenated and
 //    cut into one contiguous chunk per CTA (rounded to whole tiles, >= 256
 //    positions), so every SM streams the same number of bytes whatever the mix
@@ -29,7 +30,7 @@
 //    P^T moved into the B-operand layout with movmatrix, O^T += V^T * P^T with
 //    ldmatrix.trans. The contraction is tiny (M <= 8 heads), so the tensor
 //    cores only serve to keep the issue rate far below the HBM stream rate.
-//  * At the end of a split the four warps merge their (m, l, O) in shared
+//  * At the end of a split the consumer warps merge their (m, l, O) in shared
 //    memory, write one fp32 partial, and count it on the unit's arrival
 //    counter. The CTA that brings the counter to the unit's split count merges
 //    all partials of the unit in a fixed order, writes the bf16 output and
@@ -1304,7 +1305,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 SR_STAMP(tl_decode, 7);
             ++tl_splits;
 #endif
-            // ---- merge the four warps' states into one partial of this split
+            // ---- merge the consumer warps' states into one partial of this split
             float l0 = lrun[0], l1 = lrun[1];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -1315,7 +1316,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 mlsm[w * kMaxGroup + 2 * t] = make_float2(mrun[0], l0);
                 mlsm[w * kMaxGroup + 2 * t + 1] = make_float2(mrun[1], l1);
             }
-            // Unscaled O of this warp; the readers below weight the four warps.
+            // Unscaled O of this warp; the readers below weight the warps.
             float *cw = comb + w * (kMaxGroup * kCombStride);
             if constexpr (C::QUANT) {
                 const float unit = vref * 6.103515625e-05f; // 2^-14

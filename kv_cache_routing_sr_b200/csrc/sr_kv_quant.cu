@@ -19,12 +19,14 @@
 // two or four items in flight were slower. Nothing is read twice, so loads and stores
 // are streaming ones.
 //
-// Measured, inputs larger than L2: 131 us for the 128K x 8 rows of a prompt (814 MB,
-// 6.2 TB/s); with 58 registers and four blocks per SM in place of 40 and six 144 us. To
-// int8, whose quotients take five operations a value, 150 us (162 with four blocks); with
-// an operation a value in place of one for two, and scales by three divisions, 173.
-// Reading 32K x 8 rows back takes 34.1 us (203 MB, 6.0 TB/s); with cached loads 38.0, and
-// with 16 consecutive values a lane, whose stores cover half sectors, 39.7.
+// Measured, inputs larger than L2: 129 us for the 128K x 8 rows of a prompt (814 MB,
+// 6.3 TB/s) in bursts, 151 (5.4 TB/s) when run for seconds; with 58 registers and four
+// blocks per SM in place of 40 and six 144 in bursts. To int8, whose quotients take five
+// operations a value, 151 in bursts and 181 for seconds (162 in bursts with four blocks);
+// with an operation a value in place of one for two, and scales by three divisions, 173.
+// Reading 32K x 8 rows back takes 33.5 us (203 MB, 6.1 TB/s), 34.6 for seconds; with
+// cached loads 38.0, and with 16 consecutive values a lane, whose stores cover half
+// sectors, 39.7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -214,7 +216,7 @@ cudaError_t launch_rows(void (*kernel)(Args, long long, int), const Args &a, int
 
 cudaError_t launch_kv_write(const KvWriteArgs &a, cudaStream_t stream)
 {
-    // 8 blocks per SM take 152 us for a 128K prompt, 16 134, 32 131
+    // 8 blocks per SM take 152 us for a 128K prompt in bursts, 16 134, 32 129
     return a.kv == SR_KV_E4M3 ? launch_rows(write_kernel<SR_KV_E4M3>, a, a.n_tokens, 32, stream)
                               : launch_rows(write_kernel<SR_KV_INT8>, a, a.n_tokens, 32, stream);
 }

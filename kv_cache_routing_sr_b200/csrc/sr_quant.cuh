@@ -17,6 +17,7 @@
 #include <cstdint>
 
 #include "sinkrouter.h"
+#include "sr_ptx.cuh"
 
 namespace sr {
 
@@ -27,13 +28,6 @@ constexpr uint32_t kTopFloor = 0x0d800000u; // 2^-100 as fp32 bits
 __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t acc, uint32_t w)
 {
     return __vmaxu2(acc, w & 0x7fff7fffu);
-}
-
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
 }
 
 // What a row's codes are computed from.
@@ -100,8 +94,8 @@ template <int KV> __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32
         // away from a tie, since x and top have 8 bits each. Adding 1.5 2^23
         // rounds to an integer, ties to even, whose low byte is the code. Two
         // values an instruction.
-        const uint64_t mul = pack_f32x2(r.mul, r.mul), up = pack_f32x2(r.up, r.up), nf = pack_f32x2(-r.f, -r.f),
-                       rcp = pack_f32x2(r.rcp, r.rcp), magic = pack_f32x2(12582912.f, 12582912.f);
+        const uint64_t mul = pack2(r.mul, r.mul), up = pack2(r.up, r.up), nf = pack2(-r.f, -r.f),
+                       rcp = pack2(r.rcp, r.rcp), magic = pack2(12582912.f, 12582912.f);
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; i += 2)
@@ -113,7 +107,7 @@ template <int KV> __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32
                 "add.rn.f32x2 z, y, %7;\n\t"
                 "mov.b64 {%0, %1}, z;\n\t}"
                 : "=r"(c[i]), "=r"(c[i + 1])
-                : "l"(pack_f32x2(x[i], x[i + 1])), "l"(mul), "l"(up), "l"(nf), "l"(rcp), "l"(magic));
+                : "l"(pack2(x[i], x[i + 1])), "l"(mul), "l"(up), "l"(nf), "l"(rcp), "l"(magic));
         return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
 }

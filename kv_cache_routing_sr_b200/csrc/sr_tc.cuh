@@ -134,19 +134,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// ---- fp32 pairs -------------------------------------------------------------------------
-
-__device__ __forceinline__ uint64_t pack2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
+// ---- arithmetic of fp32 pairs (pack2) -----------------------------------------------------
 
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
