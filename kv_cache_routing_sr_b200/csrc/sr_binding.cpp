@@ -2,7 +2,8 @@
 // tensor against the shapes, type and device that the call implies, allocates
 // outputs that were not given, and calls the C ABI on the tensors' device and
 // stream. The same checks in Python with ctypes take 8 to 16 us a call, more than
-// the kernels of a short one (4 to 9 us); here they take about 1.
+// the kernels of a short one (4 to 9 us); here they take about 1. The decoders' steps
+// check theirs here too (step_fits).
 //
 // The entry points come as addresses (use), from whichever build of the library is
 // loaded. No C++ exception leaves a function: each becomes a Python exception.
@@ -357,6 +358,44 @@ PyObject *prefix(PyObject *const *a)
     return Py_BuildValue("(iNN)", (int)st, THPVariable_Wrap(out), zo);
 }
 
+// (out, n_kv_heads, q, k0, v0, k_prefix, v_prefix, prefix_len, k_cache, v_cache, kv_scales, seq_lens) -> None
+// The checks of a decoder's step before it launches anything, against the decoder's own
+// output: its other buffers have that shape whatever the tensors' is, and an appended
+// token is not taken back. Without v0 only the first two, which the call on an 8-bit
+// cache does not see.
+PyObject *step_fits(PyObject *const *a)
+{
+    const at::Tensor &out = tensor(a[0], "out");
+    const int64_t B = out.size(0), Hq = out.size(1), Hkv = whole(a[1], "n_kv_heads");
+    auto fits = [&](PyObject *o, const char *name, at::ScalarType type, Shape shape) {
+        const at::Tensor &t = tensor(o, name);
+        if (t.scalar_type() != type || t.sizes() != shape || t.device() != out.device() || !t.is_contiguous())
+            throw ValueError(std::string(name) + " must be contiguous " + c10::toString(type) + " of shape " + text(shape) +
+                             " on " + out.device().str() + ", got " + c10::toString(t.scalar_type()) + " of " +
+                             text(t.sizes()) + " on " + t.device().str());
+        if (type != kI32 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+            throw ValueError(std::string(name) + " must be 16-byte aligned");
+    };
+    fits(a[2], "q", kBf16, {B, Hq, 128});
+    fits(a[3], "k0", kBf16, {B, Hkv, 128});
+    if (a[4] == Py_None)
+        Py_RETURN_NONE;
+    fits(a[4], "v0", kBf16, {B, Hkv, 128});
+    const at::Tensor &kp = tensor(a[5], "k_prefix"), &kc = tensor(a[8], "k_cache");
+    const int64_t cap = kp.dim() == 3 ? kp.size(1) : 0, len = whole(a[7], "prefix_len");
+    fits(a[5], "k_prefix", kBf16, {Hkv, cap, 128});
+    fits(a[6], "v_prefix", kBf16, {Hkv, cap, 128});
+    if (cap < 1 || len < 0 || len > cap)
+        throw ValueError("prefix_len must be in [0, " + std::to_string(cap) + "] of at least one position, got " +
+                         std::to_string(len));
+    const at::ScalarType type = a[10] == Py_None ? kBf16 : kc.scalar_type();
+    const int64_t L = kc.dim() == 4 ? kc.size(2) : 0;
+    fits(a[8], "k_cache", type, {B, Hkv, L, 128});
+    fits(a[9], "v_cache", type, {B, Hkv, L, 128});
+    fits(a[11], "seq_lens", kI32, {B});
+    Py_RETURN_NONE;
+}
+
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N> PyObject *guarded(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     if (n != N) {
@@ -413,6 +452,7 @@ PyMethodDef g_methods[] = {
     {"rope_append_route_kv", fast(&guarded<rope_append_route_kv, 19>), METH_FASTCALL, nullptr},
     {"decode_quant", fast(&guarded<decode_quant, 14>), METH_FASTCALL, nullptr},
     {"prefix", fast(&guarded<prefix, 14>), METH_FASTCALL, nullptr},
+    {"step_fits", fast(&guarded<step_fits, 12>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 // The docstring names the torch that this was compiled against: the build looks for it

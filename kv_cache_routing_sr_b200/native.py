@@ -645,16 +645,6 @@ class Decoder:
         return self.out
 
 
-def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device):
-    """The argument checks of a decoder's step, before it launches anything: its own
-    buffers have the decoder's shape, whatever the tensors' is."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on {device}, got {t.dtype} of "
-                         f"{tuple(t.shape)} on {t.device}")
-    if dtype != torch.int32 and t.data_ptr() % 16:
-        raise ValueError(f"{name} must be 16-byte aligned")
-
-
 def _expect_splits(shape, n_splits: int, lowest: int, workspace: Workspace):
     if n_splits < lowest or n_splits > SR_MAX_SPLITS:
         raise ValueError(f"n_splits must be in [{lowest}, {SR_MAX_SPLITS}], got {n_splits}")
@@ -674,10 +664,9 @@ class QuantDecoder(Decoder):
         super().__init__(batch, n_q_heads, n_kv_heads, max_seq_len, max_splits, device)
 
     def _check(self, q, k0, n_splits):
-        B, Hq, Hkv, _ = self.shape
-        _expect(q, "q", torch.bfloat16, (B, Hq, HEAD_DIM), self.out.device)
-        _expect(k0, "k0", torch.bfloat16, (B, Hkv, HEAD_DIM), self.out.device)
-        _expect_splits(self.shape, n_splits, 0, self.workspace)
+        _loaded().step_fits(self.out, self.shape[2], q, k0, *[None] * 8)
+        if n_splits != 0:
+            _expect_splits(self.shape, n_splits, 0, self.workspace)
 
     def step(self, q, cache: QuantCache, k0, v0, seq_lens, tau, n_splits: int = 0, stream=None):
         self._check(q, k0, n_splits)

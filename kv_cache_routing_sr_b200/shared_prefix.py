@@ -50,22 +50,11 @@ class SharedPrefixDecoder:
     def _check(self, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, k0, v0, seq_lens, kv_scales, n_splits):
         """Everything that a launch of the step would refuse or read past, before the
         first one: an appended token is not taken back."""
-        s, bf16 = self.suffix, torch.bfloat16
-        B, Hq, Hkv, _ = s.shape
-        device, rows = s.out.device, (B, Hkv, native.HEAD_DIM)
-        native._expect(q, "q", bf16, (B, Hq, native.HEAD_DIM), device)
-        native._expect(k0, "k0", bf16, rows, device)
-        native._expect(v0, "v0", bf16, rows, device)
-        prefix = (Hkv, *k_prefix.shape[1:2], native.HEAD_DIM)
-        native._expect(k_prefix, "k_prefix", bf16, prefix, device)
-        native._expect(v_prefix, "v_prefix", bf16, prefix, device)
-        if prefix[1] < 1 or not 0 <= prefix_len <= prefix[1]:
-            raise ValueError(f"prefix_len must be in [0, {prefix[1]}] of at least one position, got {prefix_len}")
-        cache = (B, Hkv, *k_cache.shape[2:3], native.HEAD_DIM)
-        native._expect(k_cache, "k_cache", bf16 if kv_scales is None else k_cache.dtype, cache, device)
-        native._expect(v_cache, "v_cache", k_cache.dtype, cache, device)
-        native._expect(seq_lens, "seq_lens", torch.int32, (B,), device)
-        native._expect_splits(s.shape, n_splits, native.SPLITS_BY_UNIT, s.workspace)
+        s = self.suffix
+        native._loaded().step_fits(s.out, s.shape[2], q, k0, v0, k_prefix, v_prefix, prefix_len, k_cache, v_cache,
+                                   kv_scales, seq_lens)
+        if n_splits != 0:
+            native._expect_splits(s.shape, n_splits, native.SPLITS_BY_UNIT, s.workspace)
 
     def _attend(self, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, v0, seq_lens, kv_scales, n_splits, stream):
         s = self.suffix
